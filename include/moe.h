@@ -139,7 +139,8 @@ moe_status moe_capacity(const moe_problem* p, int64_t* C);
  * all of them). The workspace holds the device error word, scratch counters, the router's
  * bf16 operand (bf16 X with more than 16 experts: the three bf16 terms of W_r, written by each
  * router call) and, for moe_forward, the intermediate buffers (routing results, X_perm, H,
- * Y). */
+ * Y), and for problems of at most MOE_FEW_MAX_TOKENS tokens moe_forward_few's partial sums and
+ * intermediate activations. */
 moe_status moe_workspace_size(const moe_problem* p, size_t* bytes);
 
 /* Router + softmax + top-k + gates (Grok-1 book 5.2, 5.2.3; walkthrough 1.1, 1.2;
@@ -325,6 +326,36 @@ moe_status moe_forward_ex(const moe_problem* p, const void* X, const float* W_r,
                           float* topk_gate, int32_t* load, int32_t* offsets, int32_t* pos,
                           uint8_t* dropped, float* prob_colsum, float* z_loss, void* ws,
                           size_t ws_bytes, void* stream);
+
+/* ---- The layer for a few tokens (token-by-token generation): one launch for the whole layer. */
+#define MOE_FEW_MAX_TOKENS 64
+/* moe_forward for N <= MOE_FEW_MAX_TOKENS in one cooperative kernel: the same layer, arguments
+ * and optional exports, with the experts' weights streamed once through the SMs instead of
+ * tiles of 128 rows (Grok-1 book 5.2, 5.3.5; LLMs-from-scratch 12.1, 12.2; walkthrough 1.1-3.2).
+ * Differences from moe_forward:
+ *   - Logits are fp32 sums in another order, so a selection decided by a gap of a few fp32
+ *     roundings may differ; everything after the logits follows the same rules.
+ *   - The intermediate activations H keep 16 bits of mantissa (two bf16 terms) and the k
+ *     contributions are summed in fp32 without rounding Y: the output is rounded once.
+ *   - Nothing of moe_forward's intermediates (row_token, X_perm, H, Y) is written.
+ * More than 64 tokens: MOE_ERR_UNSUPPORTED. Needs routing_mode = TOPK. out must not overlap any
+ * input. The kernel needs every SM of the device to itself at once (a cooperative launch of one
+ * block per SM): it starts when the SMs have room, and the device must not be shared with a
+ * kernel that never ends. Workspace: moe_workspace_size bytes. Deterministic. */
+moe_status moe_forward_few(const moe_problem* p, const void* X, const float* W_r,
+                           const float* bias, const void* W1, const void* W2, const void* W3,
+                           void* out, float* logits, int32_t* topk_idx, float* topk_gate,
+                           int32_t* load, int32_t* offsets, int32_t* pos, uint8_t* dropped,
+                           float* prob_colsum, void* ws, size_t ws_bytes, void* stream);
+/* moe_forward_few with 8-bit expert weights (layouts, scales and shape rules of
+ * moe_forward_w8: bf16 activations, D and F multiples of 16). */
+moe_status moe_forward_few_w8(const moe_problem* p, const void* X, const float* W_r,
+                              const float* bias, const int8_t* W1q, const float* S1,
+                              const int8_t* W2q, const float* S2, const int8_t* W3q,
+                              const float* S3, void* out, float* logits, int32_t* topk_idx,
+                              float* topk_gate, int32_t* load, int32_t* offsets, int32_t* pos,
+                              uint8_t* dropped, float* prob_colsum, void* ws, size_t ws_bytes,
+                              void* stream);
 
 /* moe_forward with HOST activations: X_host [N,D] and out_host [N,D] are host pointers
  * (page-locked memory gives asynchronous copies), the weights and W_r/bias are device

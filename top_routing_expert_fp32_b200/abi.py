@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_b200.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE = range(5)
 DEVERR_NONE, DEVERR_WAIT_TIMEOUT, DEVERR_BAD_INDEX = range(3)
+FEW_MAX_TOKENS = 64  # MOE_FEW_MAX_TOKENS
 
 # Every symbol include/moe.h declares.
 EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_workspace_size_host", "moe_route",
@@ -29,7 +30,7 @@ EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_workspace_size_host", "moe
            "moe_forward_host", "moe_expert_up_w8", "moe_expert_down_w8", "moe_forward_w8",
            "moe_pack_w8", "moe_expert_up_w8p", "moe_expert_down_w8p", "moe_forward_w8p",
            "moe_gather_rows", "moe_forward_host_many", "moe_selftest_wait_timeout",
-           "moe_balance_loss", "moe_drop_rate",
+           "moe_balance_loss", "moe_drop_rate", "moe_forward_few", "moe_forward_few_w8",
            "moe_workspace_init", "moe_get_device_error", "moe_status_string", "moe_last_error",
            "moe_version")
 
@@ -84,6 +85,8 @@ def _load() -> ctypes.CDLL:
         "moe_expert_up_w8p": [PP, P, P, P, P, P, P, P, P, S, P],
         "moe_expert_down_w8p": [PP, P, P, P, P, P, P, S, P],
         "moe_forward_w8p": [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
+        "moe_forward_few": [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
+        "moe_forward_few_w8": [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
         "moe_workspace_init": [P, S, P],
         "moe_get_device_error": [P, P, ctypes.POINTER(ctypes.c_int32)],
     }
@@ -206,6 +209,29 @@ def forward(p, X, W_r, bias, W1, W2, W3, out, ws, *, logits=None, topk_idx=None,
                            _ptr(prob_colsum), _ptr(ws), ws.numel(), _stream(stream)))
 
 
+def forward_few(p, X, W_r, bias, W1, W2, W3, out, ws, *, logits=None, topk_idx=None,
+                topk_gate=None, load=None, offsets=None, pos=None, dropped=None, prob_colsum=None,
+                stream=None):
+    """moe_forward_few: the whole layer for at most FEW_MAX_TOKENS tokens in one kernel."""
+    _check(lib.moe_forward_few(ctypes.byref(p), _ptr(X), _ptr(W_r), _ptr(bias), _ptr(W1),
+                               _ptr(W2), _ptr(W3), _ptr(out), _ptr(logits), _ptr(topk_idx),
+                               _ptr(topk_gate), _ptr(load), _ptr(offsets), _ptr(pos),
+                               _ptr(dropped), _ptr(prob_colsum), _ptr(ws), ws.numel(),
+                               _stream(stream)))
+
+
+def forward_few_w8(p, X, W_r, bias, w8, out, ws, *, logits=None, topk_idx=None, topk_gate=None,
+                   load=None, offsets=None, pos=None, dropped=None, prob_colsum=None,
+                   stream=None):
+    """forward_few with 8-bit expert weights (w8 as in forward_w8, unpacked)."""
+    _check(lib.moe_forward_few_w8(ctypes.byref(p), _ptr(X), _ptr(W_r), _ptr(bias), _ptr(w8.W1q),
+                                  _ptr(w8.S1), _ptr(w8.W2q), _ptr(w8.S2), _ptr(w8.W3q),
+                                  _ptr(w8.S3), _ptr(out), _ptr(logits), _ptr(topk_idx),
+                                  _ptr(topk_gate), _ptr(load), _ptr(offsets), _ptr(pos),
+                                  _ptr(dropped), _ptr(prob_colsum), _ptr(ws), ws.numel(),
+                                  _stream(stream)))
+
+
 def forward_ex(p, X, W_r, bias, noise, W1, W2, W3, out, ws, *, logits=None, topk_idx=None,
                topk_gate=None, load=None, offsets=None, pos=None, dropped=None, prob_colsum=None,
                z_loss=None, stream=None):
@@ -321,4 +347,10 @@ class Layer:
         if out is None:
             out = torch.empty_like(X)
         forward(self.p, X, W_r, bias, W1, W2, W3, out, self.ws, **exports)
+        return out
+
+    def forward_few(self, X, W_r, bias, W1, W2, W3, out=None, **exports):
+        if out is None:
+            out = torch.empty_like(X)
+        forward_few(self.p, X, W_r, bias, W1, W2, W3, out, self.ws, **exports)
         return out

@@ -86,12 +86,16 @@ int* sched_of(int* header) { return header + kSchedInt; }
 constexpr int kDispatchBarInt = 20;
 int* dispatch_bar_of(int* header) { return header + kDispatchBarInt; }
 
+// Ints 24 and 25: moe_forward_few's grid-barrier arrivals and finished count (zero at rest).
+constexpr int kFewBarInt = 24;
+int* few_bar_of(int* header) { return header + kFewBarInt; }
+
 size_t elem_size(const moe_problem& p) { return p.dtype == MOE_DTYPE_BF16 ? 2 : 4; }
 
 // Device workspace regions (byte offsets from the workspace base).
 struct Layout {
   size_t err, colsum_part, zl_part, route_op, counts, idx, gate, pos, dropped, load, offsets,
-      row_token, xperm, h, y;
+      row_token, xperm, h, y, few;
   size_t total;       // moe_forward and every other entry point
   size_t xin, xout;   // moe_forward_host / moe_forward_host_many
   size_t xin2, xout2; // second buffers of moe_forward_host_many
@@ -123,6 +127,7 @@ Layout make_layout(const moe_problem& p) {
   L.xperm = take(es * R * static_cast<size_t>(p.D));
   L.h = take(es * R * static_cast<size_t>(p.F));
   L.y = take(es * R * static_cast<size_t>(p.D));
+  L.few = take(few_workspace_bytes(p));
   L.total = o;
   L.xin = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
   L.xout = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
@@ -395,6 +400,27 @@ moe_status forward_impl(const moe_problem& p, const void* X, const float* W_r, c
   return MOE_OK;
 }
 
+moe_status few_impl(const moe_problem& p, const FewTensors& t, void* ws, cudaStream_t stream) {
+  if (p.N > kFewMaxTokens)
+    return fail(MOE_ERR_UNSUPPORTED, "more than 64 tokens: use moe_forward");
+  MOE_TRY(need_topk(p));
+  if (p.N == 0) {
+    if (t.load) MOE_CUDA(cudaMemsetAsync(t.load, 0, sizeof(int32_t) * p.E, stream), "memset");
+    if (t.offsets)
+      MOE_CUDA(cudaMemsetAsync(t.offsets, 0, sizeof(int32_t) * (p.E + 1), stream), "memset");
+    if (t.colsum) MOE_CUDA(cudaMemsetAsync(t.colsum, 0, sizeof(float) * p.E, stream), "memset");
+    return MOE_OK;
+  }
+  MOE_TRY(check_sm100());
+  const Layout L = make_layout(p);
+  int* err = at<int>(ws, L.err);
+  NvtxRange range("moe few tokens");
+  MOE_CUDA(launch_few(p, capacity_of(p), t, at<void>(ws, L.few), err, few_bar_of(err),
+                      wait_timeout_ns(), stream),
+           "few-token layer");
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -633,6 +659,67 @@ moe_status moe_forward_ex(const moe_problem* p, const void* X, const float* W_r,
   return forward_impl(*p, X, W_r, bias, noise, w, out, logits, topk_idx, topk_gate, load,
                       offsets, pos, dropped, prob_colsum, z_loss, ws,
                       static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_forward_few(const moe_problem* p, const void* X, const float* W_r,
+                           const float* bias, const void* W1, const void* W2, const void* W3,
+                           void* out, float* logits, int32_t* topk_idx, float* topk_gate,
+                           int32_t* load, int32_t* offsets, int32_t* pos, uint8_t* dropped,
+                           float* prob_colsum, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_problem(p));
+  MOE_TRY(check_ws(*p, ws, ws_bytes, false));
+  MOE_TRY(need(X, "X"));
+  MOE_TRY(need(W_r, "W_r"));
+  MOE_TRY(opt(bias, "bias", 4));
+  MOE_TRY(need(W1, "W1"));
+  MOE_TRY(need(W2, "W2"));
+  MOE_TRY(need(W3, "W3"));
+  MOE_TRY(need(out, "out"));
+  MOE_TRY(opt(logits, "logits", 4));
+  MOE_TRY(opt(topk_idx, "topk_idx", 4));
+  MOE_TRY(opt(topk_gate, "topk_gate", 4));
+  MOE_TRY(opt(load, "load", 4));
+  MOE_TRY(opt(offsets, "offsets", 4));
+  MOE_TRY(opt(pos, "pos", 4));
+  MOE_TRY(opt(dropped, "dropped", 1));
+  MOE_TRY(opt(prob_colsum, "prob_colsum", 4));
+  const FewTensors t{X,       W_r,     bias,      W1,   W2,      W3,  nullptr, nullptr, nullptr,
+                     out,     logits,  topk_idx,  topk_gate, load, offsets, pos, dropped,
+                     prob_colsum};
+  return few_impl(*p, t, ws, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_forward_few_w8(const moe_problem* p, const void* X, const float* W_r,
+                              const float* bias, const int8_t* W1q, const float* S1,
+                              const int8_t* W2q, const float* S2, const int8_t* W3q,
+                              const float* S3, void* out, float* logits, int32_t* topk_idx,
+                              float* topk_gate, int32_t* load, int32_t* offsets, int32_t* pos,
+                              uint8_t* dropped, float* prob_colsum, void* ws, size_t ws_bytes,
+                              void* stream) {
+  MOE_TRY(check_problem(p));
+  MOE_TRY(check_w8(*p));
+  MOE_TRY(check_ws(*p, ws, ws_bytes, false));
+  MOE_TRY(need(X, "X"));
+  MOE_TRY(need(W_r, "W_r"));
+  MOE_TRY(opt(bias, "bias", 4));
+  MOE_TRY(need(W1q, "W1q"));
+  MOE_TRY(need(S1, "S1"));
+  MOE_TRY(need(W2q, "W2q"));
+  MOE_TRY(need(S2, "S2"));
+  MOE_TRY(need(W3q, "W3q"));
+  MOE_TRY(need(S3, "S3"));
+  MOE_TRY(need(out, "out"));
+  MOE_TRY(opt(logits, "logits", 4));
+  MOE_TRY(opt(topk_idx, "topk_idx", 4));
+  MOE_TRY(opt(topk_gate, "topk_gate", 4));
+  MOE_TRY(opt(load, "load", 4));
+  MOE_TRY(opt(offsets, "offsets", 4));
+  MOE_TRY(opt(pos, "pos", 4));
+  MOE_TRY(opt(dropped, "dropped", 1));
+  MOE_TRY(opt(prob_colsum, "prob_colsum", 4));
+  const FewTensors t{X,   W_r,    bias,     W1q,       W2q,  W3q,     S1,  S2,      S3,
+                     out, logits, topk_idx, topk_gate, load, offsets, pos, dropped, prob_colsum};
+  return few_impl(*p, t, ws, static_cast<cudaStream_t>(stream));
 }
 
 // Non-blocking streams per device for the host copies of moe_forward_host[_many] (created on

@@ -1,0 +1,949 @@
+// The whole layer for a few tokens (at most 64) in one cooperative kernel:
+//   z = x W_r + b,  softmax, top-k, capacity,  H = g act(x W1_e) (.) (x W2_e),
+//   out[t] = sum over t's kept experts of H W3_e
+// (Grok-1 book ch.5, 5.2 and 5.3.5; LLMs-from-scratch ch.12, 12.1; walkthrough 1.1-3.2).
+//
+// What bounds it: one pass over the matrices of the experts that keep a token. Everything else
+// is latency, so there is one launch and two grid barriers:
+//   1. Router. The D reduction is cut over the blocks (fp32 partial logits to L2), barrier, then
+//      every block adds the partials and takes all decisions itself (one warp per token; ballots
+//      for the capacity positions), which is cheaper than a second exchange.
+//   2. Up. The (expert, 64 columns of F, 64 rows of D) stages of W1 and W2 run through the
+//      ring (stream.cuh) in equal shares per block. The gate is folded into H here, so that the
+//      combine below is a plain sum. H is kept as two bf16 terms (16 bits of mantissa): the
+//      second term costs one more instruction per stage on tensor cores that are idle anyway, and
+//      leaves the output's own rounding as the only one that shows.
+//   3. Barrier, while the ring already fills with W3, which does not depend on H.
+//   4. Down. Stages ordered (64 columns of D, expert, 128 rows of F): a column block's sum runs
+//      over all experts in shared memory per token, which is the combine.
+// Rows of an expert are its kept tokens in capacity order, read from X by index: no
+// permutation is written. A tile shared by several blocks is summed by the last to finish, in
+// block order, so equal inputs give equal bits.
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "internal.h"
+#include "stream.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace stream;
+
+constexpr int kStages = 11;
+constexpr int kMaxRecords = kMaxRows * 8;
+constexpr int kMaxE = 64;
+constexpr int kMaxSlices = 64;  // pieces of D of the router's partial logits
+
+struct FewArgs {
+  const void* X;
+  const float* W_r;
+  const float* bias;
+  const float* S1;
+  const float* S2;
+  const float* S3;
+  void* out;
+  float* logits;
+  int32_t* idx;
+  float* gate;
+  int32_t* load;
+  int32_t* offsets;
+  int32_t* pos;
+  uint8_t* dropped;
+  float* colsum;
+  float* part_logits;  // [slices][N][E]
+  float* part;         // [grid][2][part_floats]: sums of shared tiles
+  int* counters;       // [2][kMaxGrid]: arrivals at shared up and down tiles
+  void* H;             // [N k rows]: see h_row_bytes
+  int* bar;            // [2] workspace header ints, zero at rest
+  int* err;
+  int64_t part_floats;
+  int64_t capacity;
+  uint64_t timeout_ns;
+  int N, D, F, E, k;
+  int tokens_per_group, slices;  // router split
+  bool x_f32, renorm, token_major, renorm_kept;
+  int act;
+};
+
+struct Tables {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  float gate[kMaxRecords];
+  float row_gate[kMaxRecords];
+  float zmax[kMaxRows];
+  float sum[kMaxRows];
+  int load[kMaxE];
+  int off[kMaxE + 1];
+  int used[kMaxE];
+  int n_used;
+  int flag;
+  int16_t row_tok[kMaxRecords];
+  int16_t pos[kMaxRecords];
+  uint8_t idx[kMaxRecords];
+};
+
+constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kStageBytes;
+constexpr size_t kOutAccBytes = sizeof(float) * kMaxRows * 64;
+constexpr size_t kSmemBytes =
+    1024 + kRingBytes + sizeof(float) * kRedFloats + kOutAccBytes + sizeof(Tables);
+static_assert(kSmemBytes <= 232448, "shared memory of a block");
+
+// H of one row. 16-bit kinds: per 16 values of F four 16-byte words, word t holding the values
+// (2t, 2t+1), (2t+8, 2t+9) of the first bf16 term and then of the second: one load per thread
+// and instruction operand. fp32: plain.
+__host__ __device__ inline int64_t h_row_bytes(int kind, int64_t F) {
+  return kind == kF32 ? ((F + 31) / 32) * 32 * 4 : ((F + 63) / 64) * 64 * 4;
+}
+
+__device__ __forceinline__ float act_value(int act, float a) {
+  if (act == MOE_ACT_SILU) return activation<MOE_ACT_SILU>(a);
+  if (act == MOE_ACT_GELU_ERF) return activation<MOE_ACT_GELU_ERF>(a);
+  return activation<MOE_ACT_GELU_TANH>(a);
+}
+
+// Order-preserving integer image of a float (+0 and -0 alike), for selection by maximum.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// ------------------------------------------------------------------ router
+
+// This block's partial logits: tokens [t0, t1) over rows [d0, d1) of D.
+template <bool XF32>
+__device__ void partial_logits(const FewArgs& a, float* red, int tid) {
+  const int groups = (a.N + a.tokens_per_group - 1) / a.tokens_per_group;
+  const int group = static_cast<int>(blockIdx.x) % groups;
+  const int slice = static_cast<int>(blockIdx.x) / groups;
+  if (slice >= a.slices) return;
+  const int t0 = group * a.tokens_per_group;
+  const int nt = min(a.tokens_per_group, a.N - t0);
+  const int rows = (a.D + a.slices - 1) / a.slices;
+  const int d0 = min(a.D, slice * rows), d1 = min(a.D, d0 + rows);
+  int ep = 1;
+  while (ep < a.E) ep <<= 1;
+  const int e = tid & (ep - 1), sl = tid / ep, subs = kConsumers / ep;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int d = d0 + sl; d < d1; d += subs) {
+      const float w = __ldg(a.W_r + static_cast<int64_t>(d) * a.E + e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < nt) {
+          const int64_t at = static_cast<int64_t>(t0 + i) * a.D + d;
+          const float x = XF32 ? __ldg(static_cast<const float*>(a.X) + at)
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[at]);
+          acc[i] = fmaf(x, w, acc[i]);
+        }
+      }
+    }
+  }
+  for (int i = 0; i < nt; ++i) {  // sum the row interleave in order
+    float v = acc[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+      if (q == i) v = acc[q];
+    red[(i * subs + sl) * ep + e] = v;
+  }
+  named_bar_sync(kBarConsumers, kConsumers);
+  for (int o = tid; o < nt * ep; o += kConsumers) {
+    const int i = o / ep, ee = o & (ep - 1);
+    if (ee < a.E) {
+      float s = 0.0f;
+      for (int q = 0; q < subs; ++q) s += red[(i * subs + q) * ep + ee];
+      a.part_logits[(static_cast<int64_t>(slice) * a.N + t0 + i) * a.E + ee] = s;
+    }
+  }
+}
+
+// All logits in shared memory, z[t * E + e].
+__device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
+  const int n = a.N * a.E;
+  int parts = 1;  // threads per logit
+  while (parts < a.slices && parts * 2 * n <= kConsumers) parts *= 2;
+  if (parts > 1) {
+    const int l = tid % n, part = tid / n;
+    if (part < parts) {
+      float s = 0.0f;
+#pragma unroll 8
+      for (int q = part; q < a.slices; q += parts)
+        s += __ldcg(a.part_logits + static_cast<int64_t>(q) * n + l);
+      red[part * n + l] = s;
+    }
+    named_bar_sync(kBarConsumers, kConsumers);
+    if (tid < n) {
+      float s = a.bias != nullptr ? a.bias[tid % a.E] : 0.0f;
+      float sum = 0.0f;
+      for (int q = 0; q < parts; ++q) sum += red[q * n + tid];
+      z[tid] = sum + s;
+    }
+  } else {
+    for (int l = tid; l < n; l += kConsumers) {
+      float s = 0.0f;
+#pragma unroll 8
+      for (int q = 0; q < a.slices; ++q)
+        s += __ldcg(a.part_logits + static_cast<int64_t>(q) * n + l);
+      z[l] = s + (a.bias != nullptr ? a.bias[l % a.E] : 0.0f);
+    }
+  }
+  named_bar_sync(kBarConsumers, kConsumers);
+}
+
+// Top-k and gates, one warp per token (the rules of select.cuh's plain top-k: descending fp32
+// logits, the lower index first among equals, gates from exp(z - max)). The selection always
+// yields k distinct experts, whatever the logits hold.
+__device__ void select_all(const FewArgs& a, Tables& tb, const float* z, int warp, int lane) {
+  for (int t = warp; t < a.N; t += kConsumerWarps) {
+    const float* zt = z + t * a.E;
+    const bool in0 = lane < a.E, in1 = lane + 32 < a.E;
+    const float z0 = in0 ? zt[lane] : 0.0f, z1 = in1 ? zt[lane + 32] : 0.0f;
+    uint64_t k0 = in0 ? (static_cast<uint64_t>(ordered(z0)) << 32) | (0xFFFFu - lane) : 0;
+    uint64_t k1 = in1 ? (static_cast<uint64_t>(ordered(z1)) << 32) | (0xFFFFu - lane - 32) : 0;
+    float zmax = 0.0f, zsel = 0.0f;
+    int mine = 0;
+    for (int j = 0; j < a.k; ++j) {
+      uint64_t best = k0 > k1 ? k0 : k1;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+        best = other > best ? other : best;
+      }
+      const int e = 0xFFFF - static_cast<int>(best & 0xFFFFu);
+      if (e == lane) k0 = 0;
+      if (e == lane + 32) k1 = 0;
+      const float v = zt[e];
+      if (j == 0) zmax = v;
+      if (lane == j) {
+        mine = e;
+        zsel = v;
+      }
+    }
+    float all = (in0 ? expf(z0 - zmax) : 0.0f) + (in1 ? expf(z1 - zmax) : 0.0f);
+    float sel = lane < a.k ? expf(zsel - zmax) : 0.0f;
+    const float num = sel;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+      sel += __shfl_xor_sync(0xFFFFFFFFu, sel, o);
+    }
+    if (lane < a.k) {
+      tb.idx[t * a.k + lane] = static_cast<uint8_t>(mine);
+      tb.gate[t * a.k + lane] = num / (a.renorm ? sel : all);
+    }
+    if (lane == 0) {
+      tb.zmax[t] = zmax;
+      tb.sum[t] = all;
+    }
+  }
+}
+
+// Loads, capacity positions, segment offsets, the experts with rows, and the rows' tokens and
+// gates (walkthrough 1.3, 3.1, 3.2; MoE series 2.2).
+__device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int lane) {
+  const int R = a.N * a.k;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int e = warp; e < a.E; e += kConsumerWarps) {
+    int base = 0;
+    for (int r0 = 0; r0 < R; r0 += 32) {
+      const int r = r0 + lane;  // record in capacity order
+      int at = 0;
+      bool hit = false;
+      if (r < R) {
+        at = a.token_major ? r : (r % a.N) * a.k + r / a.N;
+        hit = tb.idx[at] == e;
+      }
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
+      if (hit) tb.pos[at] = static_cast<int16_t>(base + __popc(m & below));
+      base += __popc(m);
+    }
+    if (lane == 0) tb.load[e] = base;
+  }
+  named_bar_sync(kBarConsumers, kConsumers);
+  if (warp == 0) {
+    int before = 0, used = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? static_cast<int>(min(static_cast<int64_t>(tb.load[e]), a.capacity))
+                            : 0;
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, n > 0);
+      if (e < a.E) tb.off[e] = before + sum - n;
+      if (n > 0) tb.used[used + __popc(m & below)] = e;
+      before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      used += __popc(m);
+    }
+    if (lane == 0) {
+      tb.off[a.E] = before;
+      tb.n_used = used;
+    }
+  }
+  named_bar_sync(kBarConsumers, kConsumers);
+  for (int r = tid; r < R; r += kConsumers) {
+    const int t = r / a.k;
+    const int p = tb.pos[r];
+    if (p < a.capacity) {
+      float g = tb.gate[r];
+      if (a.renorm_kept) {
+        float kept = 0.0f;
+        bool lost = false;
+        for (int j = 0; j < a.k; ++j) {
+          if (tb.pos[t * a.k + j] < a.capacity) kept += tb.gate[t * a.k + j];
+          else lost = true;
+        }
+        if (lost) g = g / kept;
+      }
+      const int row = tb.off[tb.idx[r]] + p;
+      tb.row_tok[row] = static_cast<int16_t>(t);
+      tb.row_gate[row] = g;
+    }
+  }
+}
+
+__device__ void export_routing(const FewArgs& a, const Tables& tb, const float* z, int tid) {
+  const int R = a.N * a.k;
+  for (int r = tid; r < R; r += kConsumers) {
+    const int p = tb.pos[r];
+    if (a.idx) a.idx[r] = tb.idx[r];
+    if (a.gate) a.gate[r] = tb.gate[r];
+    if (a.pos) a.pos[r] = p;
+    if (a.dropped) a.dropped[r] = p >= a.capacity;
+  }
+  if (a.logits)
+    for (int l = tid; l < a.N * a.E; l += kConsumers) a.logits[l] = z[l];
+  if (tid < a.E) {
+    if (a.load) a.load[tid] = tb.load[tid];
+    if (a.colsum) {
+      float s = 0.0f;
+      for (int t = 0; t < a.N; ++t) s += expf(z[t * a.E + tid] - tb.zmax[t]) / tb.sum[t];
+      a.colsum[tid] = s;
+    }
+  }
+  if (a.offsets && tid <= a.E) a.offsets[tid] = tb.off[tid];
+}
+
+// ------------------------------------------------------------------ consumers
+
+struct Consumer {
+  Ring ring;
+  Cursor cur;
+  float* red;
+  int tid, warp, lane;
+  bool ok;
+  uint64_t timeout_ns;
+  int* err;
+
+  __device__ void wait_full() {
+    if (ok && !mbar_wait(&ring.full[cur.stage], cur.phase, timeout_ns)) {
+      ok = false;
+      record_error(err, MOE_DEVERR_WAIT_TIMEOUT);
+    }
+  }
+  __device__ uint32_t my_box() const {
+    return ring.base + static_cast<uint32_t>(cur.stage) * kStageBytes +
+           static_cast<uint32_t>(warp >> 2) * kBoxBytes;
+  }
+  __device__ void release() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ring.empty[cur.stage]);
+    cur.next(ring.stages);
+  }
+};
+
+// ---- up: stages [k0, k1) of one 64-column tile of expert e
+
+template <int WK, int NT>
+__device__ __forceinline__ void load_x(Frag<WK, NT, false>& f,
+                                       const __nv_bfloat16* const (&row)[NT], int d0, int D) {
+#pragma unroll
+  for (int s = 0; s < Box<WK>::kK16; ++s) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int d = d0 + 16 * s;
+      f.r[s][j][0] = row[j] != nullptr && d < D
+                         ? __ldg(reinterpret_cast<const uint32_t*>(row[j] + d))
+                         : 0u;
+      f.r[s][j][1] = row[j] != nullptr && d + 8 < D
+                         ? __ldg(reinterpret_cast<const uint32_t*>(row[j] + d + 8))
+                         : 0u;
+    }
+  }
+}
+
+// Write one thread's two H values of a row: columns f, f + 1 (f even).
+template <int WK>
+__device__ __forceinline__ void store_h(const FewArgs& a, int row, int f, float h0, float h1) {
+  uint8_t* base =
+      static_cast<uint8_t*>(a.H) + static_cast<int64_t>(row) * h_row_bytes(WK, a.F);
+  if constexpr (WK == kF32) {
+    *reinterpret_cast<float2*>(base + static_cast<int64_t>(f) * 4) = make_float2(h0, h1);
+  } else {
+    const int in = (f & 15) >> 1;  // pair within its 16
+    uint32_t* w = reinterpret_cast<uint32_t*>(base) + static_cast<int64_t>(f >> 4) * 16 +
+                  (in & 3) * 4 + (in >> 2);
+    const uint32_t hi = pack_bf16x2(h0, h1);
+    const float r0 = h0 - bf16_bits_to_float(hi & 0xFFFFu);
+    const float r1 = h1 - bf16_bits_to_float(hi >> 16);
+    // An infinite value has no remainder.
+    w[0] = hi;
+    w[2] = pack_bf16x2(fabsf(h0) < INFINITY ? r0 : 0.0f, fabsf(h1) < INFINITY ? r1 : 0.0f);
+  }
+}
+
+template <int WK>
+__device__ __forceinline__ void finish_h(const FewArgs& a, const Tables& tb, int e, int n, int r,
+                                         int f, float2 h1, float2 h2) {
+  if (r >= n) return;
+  float v0 = 0.0f, v1 = 0.0f;  // columns past F: zeros, which the down projection reads
+  const int row = tb.off[e] + r;
+  if (f < a.F) {
+    if constexpr (WK == kW8) {
+      const int64_t at = static_cast<int64_t>(e) * a.F + f;
+      const float2 s1 = __ldg(reinterpret_cast<const float2*>(a.S1 + at));
+      const float2 s2 = __ldg(reinterpret_cast<const float2*>(a.S2 + at));
+      h1.x *= s1.x;
+      h1.y *= s1.y;
+      h2.x *= s2.x;
+      h2.y *= s2.y;
+    }
+    const float g = tb.row_gate[row];
+    v0 = act_value(a.act, h1.x) * h2.x * g;
+    v1 = act_value(a.act, h1.y) * h2.y * g;
+  }
+  store_h<WK>(a, row, f, v0, v1);
+}
+
+template <int WK, int NT>
+__device__ __noinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& consumer,
+                                     const SplitK& sp, long long tile, int steps, int k0, int k1,
+                                     int e, int fb) {
+  using B = Box<WK>;
+  Consumer c = consumer;  // in registers over the stages
+  const int n = tb.off[e + 1] - tb.off[e];
+  const int16_t* tok = tb.row_tok + tb.off[e];
+  Acc<WK, NT> acc;
+  acc.zero();
+  const int quarter = c.warp & 3;
+  if constexpr (WK == kF32) {
+    const float* X = static_cast<const float*>(a.X);
+    for (int s = k0; s < k1; ++s) {
+      c.wait_full();
+      multiply_f32<NT>(acc, c.my_box(), quarter, c.lane, n, s * B::kRows + quarter * 16, a.D,
+                       [&](int r) { return X + static_cast<int64_t>(tok[r]) * a.D; });
+      c.release();
+    }
+  } else {
+    const __nv_bfloat16* row[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = 8 * j + (c.lane >> 2);
+      row[j] = r < n ? static_cast<const __nv_bfloat16*>(a.X) +
+                           static_cast<int64_t>(tok[r]) * a.D + 2 * (c.lane & 3)
+                     : nullptr;
+    }
+    constexpr int kQuarter = B::kRows / 4;
+    Frag<WK, NT, false> f;
+    load_x<WK, NT>(f, row, k0 * B::kRows + quarter * kQuarter, a.D);
+    for (int s = k0; s < k1; ++s) {
+      Frag<WK, NT, false> next;
+      if constexpr (NT <= 4) {
+        if (s + 1 < k1) load_x<WK, NT>(next, row, (s + 1) * B::kRows + quarter * kQuarter, a.D);
+      }
+      c.wait_full();
+      multiply<WK, NT, false>(acc, c.my_box(), quarter, c.lane, f);
+      c.release();
+      if constexpr (NT <= 4) {
+        f = next;
+      } else {
+        if (s + 1 < k1) load_x<WK, NT>(f, row, (s + 1) * B::kRows + quarter * kQuarter, a.D);
+      }
+    }
+  }
+  consumer.cur = c.cur;
+  consumer.ok = c.ok;
+
+  // Both branches' sums over the block's stages; the whole tile's, or a share of it.
+  const Place<WK> at(c.tid);
+  const bool whole = k0 == 0 && k1 == steps;
+  const int f = fb * B::kCols + 2 * at.pair;
+  float2* mine = reinterpret_cast<float2*>(
+      a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
+  for (int j = 0; j < NT && 8 * j < n; ++j) {
+    put_tile<WK, NT>(c.red, acc, j, c.warp, c.lane);
+    named_bar_sync(kBarConsumers, kConsumers);
+    if (at.active) {
+      const float2 h1 = take_pair(c.red, 0, 4, at.row, at.pair);
+      const float2 h2 = take_pair(c.red, 4, 8, at.row, at.pair);
+      if (whole) {
+        finish_h<WK>(a, tb, e, n, 8 * j + at.row, f, h1, h2);
+      } else {
+        mine[(2 * j) * kConsumers + c.tid] = h1;
+        mine[(2 * j + 1) * kConsumers + c.tid] = h2;
+      }
+    }
+    named_bar_sync(kBarConsumers, kConsumers);
+  }
+  if (whole) return;
+  const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
+  if (!last_to_finish(a.counters + first, last - first + 1, c.tid, &tb.flag)) return;
+  if (!at.active) return;
+  for (int j = 0; j < NT && 8 * j < n; ++j) {
+    float2 h1 = make_float2(0.0f, 0.0f), h2 = h1;
+    for (int b = first; b <= last; ++b) {
+      const float2* p = reinterpret_cast<const float2*>(
+          a.part + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * a.part_floats);
+      const float2 v1 = __ldcg(p + (2 * j) * kConsumers + c.tid);
+      const float2 v2 = __ldcg(p + (2 * j + 1) * kConsumers + c.tid);
+      h1.x += v1.x;
+      h1.y += v1.y;
+      h2.x += v2.x;
+      h2.y += v2.y;
+    }
+    finish_h<WK>(a, tb, e, n, 8 * j + at.row, f, h1, h2);
+  }
+}
+
+// ---- down: stages [s0, s1) of expert e's part of one column block, added into outacc
+
+template <int WK, int NT>
+__device__ __forceinline__ void load_h(Frag<WK, NT, true>& f, const uint4* const (&row)[NT],
+                                       int g0, int groups) {
+#pragma unroll
+  for (int s = 0; s < Box<WK>::kK16; ++s) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row[j] != nullptr && g0 + s < groups) v = __ldcg(row[j] + (g0 + s) * 4);
+      f.r[s][j][0] = v.x;
+      f.r[s][j][1] = v.y;
+      f.r[s][j][2] = v.z;
+      f.r[s][j][3] = v.w;
+    }
+  }
+}
+
+template <int WK, int NT>
+__device__ __noinline__ void down_run(const FewArgs& a, Tables& tb, Consumer& consumer, int s0,
+                                      int s1, int e, int cb, float* outacc) {
+  using B = Box<WK>;
+  Consumer c = consumer;  // in registers over the stages
+  const int off = tb.off[e], n = tb.off[e + 1] - off;
+  const int64_t row_bytes = h_row_bytes(WK, a.F);
+  const uint8_t* H = static_cast<const uint8_t*>(a.H) + off * row_bytes;
+  Acc<WK, NT> acc;
+  acc.zero();
+  // Warp w takes k-rows [w, w+1) * kRows / 4 of the stage's 2 kRows.
+  constexpr int kQuarter = B::kRows / 4;
+  if constexpr (WK == kF32) {
+    for (int s = s0; s < s1; ++s) {
+      c.wait_full();
+      multiply_f32<NT>(acc, c.my_box(), c.warp & 3, c.lane, n,
+                       s * 2 * B::kRows + c.warp * kQuarter, a.F, [&](int r) {
+                         return reinterpret_cast<const float*>(H + r * row_bytes);
+                       });
+      c.release();
+    }
+  } else {
+    const int groups = ((a.F + 63) / 64) * 4;  // 16-value groups that the up phase wrote
+    constexpr int kG = kQuarter / 16;          // per warp and stage
+    const uint4* row[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = 8 * j + (c.lane >> 2);
+      row[j] = r < n ? reinterpret_cast<const uint4*>(H + r * row_bytes) + (c.lane & 3) : nullptr;
+    }
+    Frag<WK, NT, true> f;
+    load_h<WK, NT>(f, row, (s0 * 8 + c.warp) * kG, groups);
+    for (int s = s0; s < s1; ++s) {
+      Frag<WK, NT, true> next;
+      if constexpr (NT * kG <= 4) {
+        if (s + 1 < s1) load_h<WK, NT>(next, row, ((s + 1) * 8 + c.warp) * kG, groups);
+      }
+      c.wait_full();
+      multiply<WK, NT, true>(acc, c.my_box(), c.warp & 3, c.lane, f);
+      c.release();
+      if constexpr (NT * kG <= 4) {
+        f = next;
+      } else {
+        if (s + 1 < s1) load_h<WK, NT>(f, row, ((s + 1) * 8 + c.warp) * kG, groups);
+      }
+    }
+  }
+  consumer.cur = c.cur;
+  consumer.ok = c.ok;
+  const Place<WK> at(c.tid);
+  const int d = cb * B::kCols + 2 * at.pair;
+  for (int j = 0; j < NT && 8 * j < n; ++j) {
+    put_tile<WK, NT>(c.red, acc, j, c.warp, c.lane);
+    named_bar_sync(kBarConsumers, kConsumers);
+    const int r = 8 * j + at.row;
+    if (at.active && r < n) {
+      float2 v = take_pair(c.red, 0, kConsumerWarps, at.row, at.pair);
+      if constexpr (WK == kW8) {
+        if (d < a.D) {
+          const float2 s =
+              __ldg(reinterpret_cast<const float2*>(a.S3 + static_cast<int64_t>(e) * a.D + d));
+          v.x *= s.x;
+          v.y *= s.y;
+        }
+      }
+      float2* o = reinterpret_cast<float2*>(
+          outacc + static_cast<int>(tb.row_tok[off + r]) * B::kCols + 2 * at.pair);
+      o->x += v.x;
+      o->y += v.y;
+    }
+    named_bar_sync(kBarConsumers, kConsumers);
+  }
+}
+
+template <int WK>
+__device__ __forceinline__ void store_out(const FewArgs& a, int t, int d, float2 v) {
+  if (t >= a.N || d >= a.D) return;
+  const int64_t at = static_cast<int64_t>(t) * a.D + d;
+  if constexpr (WK == kF32)
+    *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = v;
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) = pack_bf16x2(v.x, v.y);
+}
+
+#define MOE_FEW_ROWS(n, CALL)      \
+  do {                             \
+    if ((n) <= 8) CALL(1);         \
+    else if ((n) <= 16) CALL(2);   \
+    else if ((n) <= 32) CALL(4);   \
+    else CALL(8);                  \
+  } while (0)
+
+// ------------------------------------------------------------------ the kernel
+
+template <int WK>
+__global__ void __launch_bounds__(kThreads, 1)
+few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,
+           const __grid_constant__ CUtensorMap m3, const __grid_constant__ FewArgs a) {
+  using B = Box<WK>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* red = reinterpret_cast<float*>(smem + kRingBytes);
+  float* outacc = red + kRedFloats;  // the logits first, then the column block's sums
+  Tables& tb = *reinterpret_cast<Tables*>(outacc + kMaxRows * 64);
+  const int tid = static_cast<int>(threadIdx.x);
+  const int warp = tid >> 5, lane = tid & 31;
+  const int G = static_cast<int>(gridDim.x);
+
+  Ring ring{smem_u32(smem), tb.full, tb.empty, kStages};
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&tb.full[i], 1);
+      mbar_init(&tb.empty[i], kConsumerWarps);
+    }
+    fence_barrier_init();
+    // Arrivals at this block's shared tiles; seen by the others after the first grid barrier.
+    a.counters[blockIdx.x] = 0;
+    a.counters[kMaxGrid + blockIdx.x] = 0;
+  }
+  __syncthreads();
+
+  bool ok = true;
+  if (warp < kConsumerWarps) {
+    if (a.x_f32) partial_logits<true>(a, red, tid);
+    else partial_logits<false>(a, red, tid);
+    ok = grid_barrier(a.bar, G, tid, &tb.flag, a.timeout_ns, a.err);
+    sum_logits(a, outacc, red, tid);
+    select_all(a, tb, outacc, warp, lane);
+    named_bar_sync(kBarConsumers, kConsumers);
+    assign_rows(a, tb, tid, warp, lane);
+  }
+  named_bar_sync(kBarAll, kThreads);
+
+  const int up_steps = (a.D + B::kRows - 1) / B::kRows;
+  const int up_cols = (a.F + B::kCols - 1) / B::kCols;
+  const int down_run_steps = (a.F + 2 * B::kRows - 1) / (2 * B::kRows);
+  const int down_cols = (a.D + B::kCols - 1) / B::kCols;
+  const int used = tb.n_used;
+  const int down_steps = used * down_run_steps;
+  SplitK up{static_cast<long long>(used) * up_cols * up_steps, 0};
+  SplitK down{static_cast<long long>(down_cols) * down_steps, 0};
+  up.grid = static_cast<int>(min(static_cast<long long>(G), up.total));
+  down.grid = static_cast<int>(min(static_cast<long long>(G), down.total));
+  const int me = static_cast<int>(blockIdx.x);
+  const long long u0 = me < up.grid ? up.start(me) : 0, u1 = me < up.grid ? up.start(me + 1) : 0;
+  const long long d0 = me < down.grid ? down.start(me) : 0,
+                  d1 = me < down.grid ? down.start(me + 1) : 0;
+
+  if (warp == kConsumerWarps) {
+    // Producer: one thread issues this block's stages of both products in order.
+    if (lane == 0) {
+      const uint64_t policy = l2_policy(-1);  // weights are read once
+      Cursor c;
+      bool good = true;
+      long long issued = 0;
+      for (long long s = u0; s < u1 && good;) {
+        const long long tile = s / up_steps;
+        int k = static_cast<int>(s - tile * up_steps);
+        const int k_end = static_cast<int>(min(static_cast<long long>(up_steps), k + (u1 - s)));
+        const int e = tb.used[tile / up_cols];
+        const int col = static_cast<int>(tile % up_cols) * B::kCols;
+        s += k_end - k;
+        for (; k < k_end; ++k) {
+          if (!(good = acquire_stage(ring, c, a.timeout_ns))) break;
+          uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
+          tma_load_3d_hint(dst, &m1, &tb.full[c.stage], col, k * B::kRows, e, policy);
+          tma_load_3d_hint(dst + kBoxBytes, &m2, &tb.full[c.stage], col, k * B::kRows, e, policy);
+          c.next(kStages);
+          ++issued;
+        }
+      }
+      for (long long s = d0; s < d1 && good;) {
+        const long long tile = s / down_steps;
+        const int in = static_cast<int>(s - tile * down_steps);
+        const int ei = in / down_run_steps;
+        int k = in - ei * down_run_steps;
+        const int k_end =
+            static_cast<int>(min(static_cast<long long>(down_run_steps), k + (d1 - s)));
+        const int e = tb.used[ei];
+        const int col = static_cast<int>(tile) * B::kCols;
+        s += k_end - k;
+        for (; k < k_end; ++k) {
+          if (!(good = acquire_stage(ring, c, a.timeout_ns))) break;
+          uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
+          tma_load_3d_hint(dst, &m3, &tb.full[c.stage], col, 2 * k * B::kRows, e, policy);
+          tma_load_3d_hint(dst + kBoxBytes, &m3, &tb.full[c.stage], col, (2 * k + 1) * B::kRows,
+                           e, policy);
+          c.next(kStages);
+          ++issued;
+        }
+      }
+      if (!good) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+      drain(ring, c, issued, a.timeout_ns);
+    }
+    __syncwarp();
+  } else {
+    if (me == 0) export_routing(a, tb, outacc, tid);
+    if (used == 0) {  // a capacity of zero keeps nothing: zeros
+      const Place<WK> z(tid);
+      for (int cb = me; cb < down_cols && z.active; cb += G)
+        for (int t = z.row; t < a.N; t += 8)
+          store_out<WK>(a, t, cb * B::kCols + 2 * z.pair, make_float2(0.0f, 0.0f));
+    }
+    Consumer c{ring, Cursor{}, red, tid, warp, lane, ok, a.timeout_ns, a.err};
+    for (long long s = u0; s < u1;) {
+      const long long tile = s / up_steps;
+      const int k0 = static_cast<int>(s - tile * up_steps);
+      const int k1 = static_cast<int>(min(static_cast<long long>(up_steps), k0 + (u1 - s)));
+      const int e = tb.used[tile / up_cols];
+      const int fb = static_cast<int>(tile % up_cols);
+      const int n = tb.off[e + 1] - tb.off[e];
+#define MOE_UP(NT) up_tile<WK, NT>(a, tb, c, up, tile, up_steps, k0, k1, e, fb)
+      MOE_FEW_ROWS(n, MOE_UP);
+#undef MOE_UP
+      s += k1 - k0;
+    }
+    if (!grid_barrier(a.bar, 2 * G, tid, &tb.flag, a.timeout_ns, a.err)) c.ok = false;
+
+    const Place<WK> at(tid);
+    for (long long s = d0; s < d1;) {
+      const long long tile = s / down_steps;
+      const int k0 = static_cast<int>(s - tile * down_steps);
+      const int k1 = static_cast<int>(min(static_cast<long long>(down_steps), k0 + (d1 - s)));
+      const int cb = static_cast<int>(tile);
+      for (int i = tid; i < a.N * B::kCols; i += kConsumers) outacc[i] = 0.0f;
+      named_bar_sync(kBarConsumers, kConsumers);
+      for (int k = k0; k < k1;) {
+        const int ei = k / down_run_steps;
+        const int s0 = k - ei * down_run_steps;
+        const int s1 = min(down_run_steps, s0 + (k1 - k));
+        const int e = tb.used[ei];
+        const int n = tb.off[e + 1] - tb.off[e];
+#define MOE_DOWN(NT) down_run<WK, NT>(a, tb, c, s0, s1, e, cb, outacc)
+        MOE_FEW_ROWS(n, MOE_DOWN);
+#undef MOE_DOWN
+        k += s1 - s0;
+      }
+      const int d = cb * B::kCols + 2 * at.pair;
+      const bool whole = k0 == 0 && k1 == down_steps;
+      float2* mine = reinterpret_cast<float2*>(
+          a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
+      if (at.active) {
+        for (int t = at.row; t < a.N; t += 8) {
+          const float2 v = *reinterpret_cast<const float2*>(outacc + t * B::kCols + 2 * at.pair);
+          if (whole) store_out<WK>(a, t, d, v);
+          else mine[t * Place<WK>::kPairs + at.pair] = v;
+        }
+      }
+      if (!whole) {
+        const int first = down.owner(tile * down_steps),
+                  last = down.owner(tile * down_steps + down_steps - 1);
+        if (last_to_finish(a.counters + kMaxGrid + first, last - first + 1, tid, &tb.flag) &&
+            at.active) {
+          for (int t = at.row; t < a.N; t += 8) {
+            float2 v = make_float2(0.0f, 0.0f);
+            for (int b = first; b <= last; ++b) {
+              const float2 p = __ldcg(reinterpret_cast<const float2*>(
+                                          a.part + (static_cast<int64_t>(b) * 2 +
+                                                    (b == first ? 1 : 0)) * a.part_floats) +
+                                      t * Place<WK>::kPairs + at.pair);
+              v.x += p.x;
+              v.y += p.y;
+            }
+            store_out<WK>(a, t, d, v);
+          }
+        }
+      }
+      named_bar_sync(kBarConsumers, kConsumers);
+      s += k1 - k0;
+    }
+  }
+
+  // The last block out returns the barrier counters to zero for the next launch.
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(&a.bar[1], 1) == G - 1) {
+      atomicExch(&a.bar[0], 0);
+      atomicExch(&a.bar[1], 0);
+    }
+  }
+}
+
+int64_t part_floats_of(int64_t N) { return ((N + 7) / 8) * 4 * kConsumers; }
+
+template <int WK>
+cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const void* W2,
+                   const void* W3, cudaStream_t stream) {
+  CUtensorMap m1, m2, m3;
+  if (!make_stream_map(&m1, W1, WK, p.F, p.D, p.E) || !make_stream_map(&m2, W2, WK, p.F, p.D, p.E) ||
+      !make_stream_map(&m3, W3, WK, p.D, p.F, p.E))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(
+      few_kernel<WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(num_sms(), kMaxGrid)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, few_kernel<WK>, m1, m2, m3, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+}  // namespace
+
+bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, uint64_t rows,
+                     uint64_t count) {
+  if (encode_fn() == nullptr) return false;
+  const uint64_t el = kind == kF32 ? 4 : kind == kBF16 ? 2 : 1;
+  const cuuint64_t dims[3] = {cols, rows, count};
+  const cuuint64_t strides[2] = {cols * el, cols * rows * el};
+  const cuuint32_t box[3] = {kind == kF32 ? 32u : 64u, kind == kW8 ? 128u : 64u, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType type = kind == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : kind == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return encode_fn()(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     kind == kW8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace of moe_forward_few: partial logits, counters, shared-tile sums, H.
+size_t few_workspace_bytes(const moe_problem& p) {
+  if (p.N < 1 || p.N > kMaxRows) return 0;
+  auto up256 = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t rows = static_cast<size_t>(p.N) * p.k;
+  // 8-bit layers keep H in the 16-bit layout; both fit in the larger of the two.
+  const size_t h_row = static_cast<size_t>(h_row_bytes(kBF16, p.F));
+  return up256(sizeof(float) * kMaxSlices * p.N * p.E) + up256(sizeof(int) * 2 * kMaxGrid) +
+         up256(sizeof(float) * 2 * kMaxGrid * part_floats_of(p.N)) + up256(rows * h_row);
+}
+
+cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors& t, void* scratch,
+                       int* err, int* bar, uint64_t timeout_ns, cudaStream_t stream) {
+  FewArgs a{};
+  a.X = t.X;
+  a.W_r = t.W_r;
+  a.bias = t.bias;
+  a.S1 = t.S1;
+  a.S2 = t.S2;
+  a.S3 = t.S3;
+  a.out = t.out;
+  a.logits = t.logits;
+  a.idx = t.idx;
+  a.gate = t.gate;
+  a.load = t.load;
+  a.offsets = t.offsets;
+  a.pos = t.pos;
+  a.dropped = t.dropped;
+  a.colsum = t.colsum;
+  auto up256 = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  uint8_t* w = static_cast<uint8_t*>(scratch);
+  a.part_logits = reinterpret_cast<float*>(w);
+  w += up256(sizeof(float) * kMaxSlices * p.N * p.E);
+  a.counters = reinterpret_cast<int*>(w);
+  w += up256(sizeof(int) * 2 * kMaxGrid);
+  a.part = reinterpret_cast<float*>(w);
+  a.part_floats = part_floats_of(p.N);
+  w += up256(sizeof(float) * 2 * kMaxGrid * a.part_floats);
+  a.H = w;
+  a.bar = bar;
+  a.err = err;
+  a.capacity = capacity;
+  a.timeout_ns = timeout_ns;
+  a.N = static_cast<int>(p.N);
+  a.D = static_cast<int>(p.D);
+  a.F = static_cast<int>(p.F);
+  a.E = p.E;
+  a.k = p.k;
+  // Router split: few tokens share nothing but W_r, so each token's D goes over many blocks;
+  // with more tokens a block takes up to 8 of them, which bounds the partial logits that every
+  // block reads back.
+  a.tokens_per_group = p.N <= 8 ? 1 : p.N <= 32 ? 4 : 8;
+  const int groups = (a.N + a.tokens_per_group - 1) / a.tokens_per_group;
+  const int grid = std::min(num_sms(), kMaxGrid);
+  a.slices = std::max(1, std::min({grid / groups, kMaxSlices, (a.D + 31) / 32}));
+  a.x_f32 = p.dtype == MOE_DTYPE_F32;
+  a.renorm = p.renormalize != 0;
+  a.token_major = p.capacity_order == MOE_ORDER_TOKEN_MAJOR;
+  a.renorm_kept = p.drop_policy == MOE_DROP_RENORM_KEPT;
+  a.act = p.activation;
+  if (t.S1 != nullptr) return launch<kW8>(p, a, t.W1, t.W2, t.W3, stream);
+  if (p.dtype == MOE_DTYPE_F32) return launch<kF32>(p, a, t.W1, t.W2, t.W3, stream);
+  return launch<kBF16>(p, a, t.W1, t.W2, t.W3, stream);
+}
+
+}  // namespace moe

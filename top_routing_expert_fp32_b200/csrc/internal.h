@@ -144,6 +144,35 @@ cudaError_t launch_combine(const moe_problem& p, const void* Y, const int32_t* i
                            const float* gate, const int32_t* offsets, const int32_t* pos,
                            const uint8_t* dropped, void* out, int* err, cudaStream_t stream);
 
+// The whole layer for at most kFewMaxTokens tokens in one cooperative launch (few.cu). W1..W3:
+// fp32 or bf16 weights, or int8 ones when S1..S3 are given; every pointer from `logits` on may
+// be NULL. scratch: few_workspace_bytes(p) bytes, 256-byte aligned; bar: two ints of the
+// workspace header, zero at rest (returned to zero by the kernel).
+constexpr int64_t kFewMaxTokens = 64;
+struct FewTensors {
+  const void* X;
+  const float* W_r;
+  const float* bias;
+  const void* W1;
+  const void* W2;
+  const void* W3;
+  const float* S1;
+  const float* S2;
+  const float* S3;
+  void* out;
+  float* logits;
+  int32_t* idx;
+  float* gate;
+  int32_t* load;
+  int32_t* offsets;
+  int32_t* pos;
+  uint8_t* dropped;
+  float* colsum;
+};
+size_t few_workspace_bytes(const moe_problem& p);
+cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors& t, void* scratch,
+                       int* err, int* bar, uint64_t timeout_ns, cudaStream_t stream);
+
 // Failure-detection self-test: one bounded wait on a barrier nothing completes; records
 // MOE_DEVERR_WAIT_TIMEOUT in *err after timeout_ns and returns.
 cudaError_t launch_wait_timeout_probe(int* err, uint64_t timeout_ns, cudaStream_t stream);
