@@ -8,16 +8,18 @@
 //   1. Router. The D reduction is cut over the blocks (fp32 partial logits to L2), barrier, then
 //      every block adds the partials and takes all decisions itself (one warp per token; ballots
 //      for the capacity positions), which is cheaper than a second exchange.
-//   2. Up. The (expert, 64 columns of F, 64 rows of D) stages of W1 and W2 run through the
+//   2. Up. The (expert, 128 columns of F, 64 rows of D) stages of W1 and W2 run through the
 //      ring (stream.cuh) in equal shares per block. The gate is folded into H here, so that the
 //      combine below is a plain sum. H is kept as two bf16 terms (16 bits of mantissa): the
 //      second term costs one more instruction per stage on tensor cores that are idle anyway, and
 //      leaves the output's own rounding as the only one that shows.
 //   3. Barrier, while the ring already fills with W3, which does not depend on H.
-//   4. Down. Stages ordered (64 columns of D, expert, 128 rows of F): a column block's sum runs
+//   4. Down. Stages ordered (128 columns of D, expert, 128 rows of F): a column block's sum runs
 //      over all experts in shared memory per token, which is the combine.
+// (64 columns for fp32 weights, 256 for 8-bit ones: 256 bytes either way.)
 // Rows of an expert are its kept tokens in capacity order, read from X by index: no
-// permutation is written. A tile shared by several blocks is summed by the last to finish, in
+// permutation is written. More than 32 rows of an expert are two pieces, each reading the
+// expert's weights: the sums of 32 rows are what the registers hold. A tile shared by several blocks is summed by the last to finish, in
 // block order, so equal inputs give equal bits.
 #include <algorithm>
 #include <cstdint>
@@ -32,9 +34,10 @@ namespace {
 
 using namespace stream;
 
-constexpr int kStages = 11;
 constexpr int kMaxRecords = kMaxRows * 8;
 constexpr int kMaxE = 64;
+// Products: an expert's kept rows in pieces of at most kTileRows.
+constexpr int kMaxParts = kMaxE + kMaxRecords / kTileRows;
 constexpr int kMaxSlices = 64;  // pieces of D of the router's partial logits
 
 struct FewArgs {
@@ -56,7 +59,7 @@ struct FewArgs {
   float* part_logits;  // [slices][N][E]
   float* part;         // [grid][2][part_floats]: sums of shared tiles
   int* counters;       // [2][kMaxGrid]: arrivals at shared up and down tiles
-  void* H;             // [N k rows]: see h_row_bytes
+  void* H;             // see h_groups
   int* bar;            // [2] workspace header ints, zero at rest
   int* err;
   int64_t part_floats;
@@ -64,39 +67,62 @@ struct FewArgs {
   uint64_t timeout_ns;
   int N, D, F, E, k;
   int tokens_per_group, slices;  // router split
-  bool x_f32, renorm, token_major, renorm_kept;
+  int stages;
+  bool renorm, token_major, renorm_kept;
   int act;
 };
 
+struct Part {
+  int16_t expert;
+  int16_t row0;  // first row of the piece among all kept rows
+  int16_t n;     // rows, 1..kTileRows
+  int16_t tile;  // its first tile of 8 rows in H
+};
+
 struct Tables {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   float gate[kMaxRecords];
   float row_gate[kMaxRecords];
   float zmax[kMaxRows];
   float sum[kMaxRows];
   int load[kMaxE];
   int off[kMaxE + 1];
-  int used[kMaxE];
-  int n_used;
+  Part part[kMaxParts];
+  int n_parts;
   int flag;
   int16_t row_tok[kMaxRecords];
   int16_t pos[kMaxRecords];
   uint8_t idx[kMaxRecords];
 };
 
-constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kStageBytes;
-constexpr size_t kOutAccBytes = sizeof(float) * kMaxRows * 64;
-constexpr size_t kSmemBytes =
-    1024 + kRingBytes + sizeof(float) * kRedFloats + kOutAccBytes + sizeof(Tables);
-static_assert(kSmemBytes <= 232448, "shared memory of a block");
-
-// H of one row. 16-bit kinds: per 16 values of F four 16-byte words, word t holding the values
-// (2t, 2t+1), (2t+8, 2t+9) of the first bf16 term and then of the second: one load per thread
-// and instruction operand. fp32: plain.
-__host__ __device__ inline int64_t h_row_bytes(int kind, int64_t F) {
-  return kind == kF32 ? ((F + 31) / 32) * 32 * 4 : ((F + 63) / 64) * 64 * 4;
+// Shared memory: the ring, the warps' sums, the column block's sums per token (first the
+// logits), the tables. The ring takes what the batch leaves, 6 stages for small ones.
+template <int WK>
+constexpr size_t out_bytes(int N, int E) {
+  return sizeof(float) * static_cast<size_t>(N) *
+         static_cast<size_t>(E > Shape<WK>::kCols ? E : Shape<WK>::kCols);
 }
+template <int WK>
+constexpr size_t smem_bytes(int N, int E, int stages) {
+  return 1024 + static_cast<size_t>(stages) * kStageBytes + sizeof(float) * kRedFloats +
+         out_bytes<WK>(N, E) + sizeof(Tables) + 16;
+}
+constexpr size_t kMaxSmem = 232448;
+template <int WK>
+int stages_for(int N, int E) {
+  int s = kMaxStages;
+  while (s > 2 && smem_bytes<WK>(N, E, s) > kMaxSmem) --s;
+  return s;
+}
+static_assert(smem_bytes<kW8>(kMaxRows, kMaxE, 4) <= kMaxSmem, "at least four stages");
+
+// H. 16-bit kinds: per tile of 8 rows and 32 values of F two planes (the first and the second
+// bf16 term) of 32 threads x 16 bytes, each thread's four pairs in block order (stream.cuh):
+// one coalesced load per plane. fp32: plain rows.
+__host__ __device__ inline int64_t h_groups(int64_t F) { return (F + 255) / 256 * 8; }
+constexpr int kHGroupBytes = 1024;
+__host__ __device__ inline int64_t h_row_f32(int64_t F) { return (F + 63) / 64 * 64; }
 
 __device__ __forceinline__ float act_value(int act, float a) {
   if (act == MOE_ACT_SILU) return activation<MOE_ACT_SILU>(a);
@@ -266,26 +292,35 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
   }
   named_bar_sync(kBarConsumers, kConsumers);
   if (warp == 0) {
-    int before = 0, used = 0;
+    int before = 0, parts = 0, tiles = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
       const int n = e < a.E ? static_cast<int>(min(static_cast<int64_t>(tb.load[e]), a.capacity))
                             : 0;
-      int sum = n;
+      // Inclusive prefix sums over the lanes: rows, pieces and row tiles (n <= 64 a lane).
+      int sum = n | ((n + kTileRows - 1) / kTileRows) << 12 | ((n + 7) / 8) << 20;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
         if (lane >= o) sum += v;
       }
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, n > 0);
-      if (e < a.E) tb.off[e] = before + sum - n;
-      if (n > 0) tb.used[used + __popc(m & below)] = e;
-      before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-      used += __popc(m);
+      const int total = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      const int np = (n + kTileRows - 1) / kTileRows, nt = (n + 7) / 8;
+      const int row = before + (sum & 0xFFF) - n;
+      const int part = parts + ((sum >> 12) & 0xFF) - np;
+      const int tile = tiles + (sum >> 20) - nt;
+      if (e < a.E) tb.off[e] = row;
+      for (int q = 0; q < np; ++q)
+        tb.part[part + q] = {static_cast<int16_t>(e), static_cast<int16_t>(row + q * kTileRows),
+                             static_cast<int16_t>(min(kTileRows, n - q * kTileRows)),
+                             static_cast<int16_t>(tile + q * (kTileRows / 8))};
+      before += total & 0xFFF;
+      parts += (total >> 12) & 0xFF;
+      tiles += total >> 20;
     }
     if (lane == 0) {
       tb.off[a.E] = before;
-      tb.n_used = used;
+      tb.n_parts = parts;
     }
   }
   named_bar_sync(kBarConsumers, kConsumers);
@@ -351,7 +386,7 @@ struct Consumer {
   }
   __device__ uint32_t my_box() const {
     return ring.base + static_cast<uint32_t>(cur.stage) * kStageBytes +
-           static_cast<uint32_t>(warp >> 2) * kBoxBytes;
+           static_cast<uint32_t>(warp >> 1) * kBoxBytes;
   }
   __device__ void release() {
     __syncwarp();
@@ -360,55 +395,55 @@ struct Consumer {
   }
 };
 
-// ---- up: stages [k0, k1) of one 64-column tile of expert e
+// ---- up: stages [k0, k1) of one column tile of one piece
 
 template <int WK, int NT>
 __device__ __forceinline__ void load_x(Frag<WK, NT, false>& f,
-                                       const __nv_bfloat16* const (&row)[NT], int d0, int D) {
+                                       const __nv_bfloat16* const (&row)[NT], int d0, int t,
+                                       int D) {
 #pragma unroll
-  for (int s = 0; s < Box<WK>::kK16; ++s) {
+  for (int g = 0; g < Shape<WK>::kGroups; ++g) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int d = d0 + 16 * s;
-      f.r[s][j][0] = row[j] != nullptr && d < D
-                         ? __ldg(reinterpret_cast<const uint32_t*>(row[j] + d))
-                         : 0u;
-      f.r[s][j][1] = row[j] != nullptr && d + 8 < D
-                         ? __ldg(reinterpret_cast<const uint32_t*>(row[j] + d + 8))
-                         : 0u;
+      const int d = d0 + 32 * g;  // row[j] is already at 8 t
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row[j] != nullptr && d + 8 * t < D) v = __ldg(reinterpret_cast<const uint4*>(row[j] + d));
+      to_blocks(v, t, f.r[g][j][0]);
     }
   }
 }
 
-// Write one thread's two H values of a row: columns f, f + 1 (f even).
+// Two H values of row r of a piece: columns f, f + 1 (f even).
 template <int WK>
-__device__ __forceinline__ void store_h(const FewArgs& a, int row, int f, float h0, float h1) {
-  uint8_t* base =
-      static_cast<uint8_t*>(a.H) + static_cast<int64_t>(row) * h_row_bytes(WK, a.F);
+__device__ __forceinline__ void store_h(const FewArgs& a, const Part& pt, int r, int f, float h0,
+                                        float h1) {
   if constexpr (WK == kF32) {
-    *reinterpret_cast<float2*>(base + static_cast<int64_t>(f) * 4) = make_float2(h0, h1);
+    if (f < a.F)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.H) + (pt.row0 + r) * h_row_f32(a.F) + f) =
+          make_float2(h0, h1);
   } else {
-    const int in = (f & 15) >> 1;  // pair within its 16
-    uint32_t* w = reinterpret_cast<uint32_t*>(base) + static_cast<int64_t>(f >> 4) * 16 +
-                  (in & 3) * 4 + (in >> 2);
+    const int pair = (f & 31) >> 1, t = pair >> 2, block = ((pair & 3) - t) & 3;
+    uint32_t* w = reinterpret_cast<uint32_t*>(
+                      static_cast<uint8_t*>(a.H) +
+                      ((pt.tile + (r >> 3)) * h_groups(a.F) + (f >> 5)) * kHGroupBytes) +
+                  ((r & 7) * 4 + t) * 4 + block;
     const uint32_t hi = pack_bf16x2(h0, h1);
     const float r0 = h0 - bf16_bits_to_float(hi & 0xFFFFu);
     const float r1 = h1 - bf16_bits_to_float(hi >> 16);
     // An infinite value has no remainder.
     w[0] = hi;
-    w[2] = pack_bf16x2(fabsf(h0) < INFINITY ? r0 : 0.0f, fabsf(h1) < INFINITY ? r1 : 0.0f);
+    w[128] = pack_bf16x2(fabsf(h0) < INFINITY ? r0 : 0.0f, fabsf(h1) < INFINITY ? r1 : 0.0f);
   }
 }
 
 template <int WK>
-__device__ __forceinline__ void finish_h(const FewArgs& a, const Tables& tb, int e, int n, int r,
+__device__ __forceinline__ void finish_h(const FewArgs& a, const Tables& tb, const Part& pt, int r,
                                          int f, float2 h1, float2 h2) {
-  if (r >= n) return;
+  if (r >= pt.n) return;
   float v0 = 0.0f, v1 = 0.0f;  // columns past F: zeros, which the down projection reads
-  const int row = tb.off[e] + r;
   if (f < a.F) {
     if constexpr (WK == kW8) {
-      const int64_t at = static_cast<int64_t>(e) * a.F + f;
+      const int64_t at = static_cast<int64_t>(pt.expert) * a.F + f;
       const float2 s1 = __ldg(reinterpret_cast<const float2*>(a.S1 + at));
       const float2 s2 = __ldg(reinterpret_cast<const float2*>(a.S2 + at));
       h1.x *= s1.x;
@@ -416,79 +451,77 @@ __device__ __forceinline__ void finish_h(const FewArgs& a, const Tables& tb, int
       h2.x *= s2.x;
       h2.y *= s2.y;
     }
-    const float g = tb.row_gate[row];
+    const float g = tb.row_gate[pt.row0 + r];
     v0 = act_value(a.act, h1.x) * h2.x * g;
     v1 = act_value(a.act, h1.y) * h2.y * g;
   }
-  store_h<WK>(a, row, f, v0, v1);
+  store_h<WK>(a, pt, r, f, v0, v1);
 }
 
 template <int WK, int NT>
-__device__ __noinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& consumer,
-                                     const SplitK& sp, long long tile, int steps, int k0, int k1,
-                                     int e, int fb) {
-  using B = Box<WK>;
-  Consumer c = consumer;  // in registers over the stages
-  const int n = tb.off[e + 1] - tb.off[e];
-  const int16_t* tok = tb.row_tok + tb.off[e];
+__device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& c,
+                                        const SplitK& sp, long long tile, int steps, int k0,
+                                        int k1, const Part pt, int fb) {
+  using S = Shape<WK>;
+  using P = Places<WK>;
+  const int16_t* tok = tb.row_tok + pt.row0;
   Acc<WK, NT> acc;
   acc.zero();
-  const int quarter = c.warp & 3;
+  const int first_row = warp_row<WK>(c.warp);
   if constexpr (WK == kF32) {
     const float* X = static_cast<const float*>(a.X);
     for (int s = k0; s < k1; ++s) {
       c.wait_full();
-      multiply_f32<NT>(acc, c.my_box(), quarter, c.lane, n, s * B::kRows + quarter * 16, a.D,
+      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, pt.n, s * kBoxRows + first_row, a.D,
                        [&](int r) { return X + static_cast<int64_t>(tok[r]) * a.D; });
       c.release();
     }
   } else {
+    const int t = c.lane & 3;
     const __nv_bfloat16* row[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int r = 8 * j + (c.lane >> 2);
-      row[j] = r < n ? static_cast<const __nv_bfloat16*>(a.X) +
-                           static_cast<int64_t>(tok[r]) * a.D + 2 * (c.lane & 3)
-                     : nullptr;
+      row[j] = r < pt.n ? static_cast<const __nv_bfloat16*>(a.X) +
+                              static_cast<int64_t>(tok[r]) * a.D + 8 * t
+                        : nullptr;
     }
-    constexpr int kQuarter = B::kRows / 4;
-    Frag<WK, NT, false> f;
-    load_x<WK, NT>(f, row, k0 * B::kRows + quarter * kQuarter, a.D);
-    for (int s = k0; s < k1; ++s) {
-      Frag<WK, NT, false> next;
-      if constexpr (NT <= 4) {
-        if (s + 1 < k1) load_x<WK, NT>(next, row, (s + 1) * B::kRows + quarter * kQuarter, a.D);
-      }
-      c.wait_full();
-      multiply<WK, NT, false>(acc, c.my_box(), quarter, c.lane, f);
-      c.release();
-      if constexpr (NT <= 4) {
-        f = next;
-      } else {
-        if (s + 1 < k1) load_x<WK, NT>(f, row, (s + 1) * B::kRows + quarter * kQuarter, a.D);
+    // The rows' values are loaded kAhead stages before their use: an L2 access takes longer
+    // than a stage's arithmetic.
+    constexpr int kAhead = NT * S::kGroups <= 4 ? 2 : 1;
+    Frag<WK, NT, false> f[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (k0 + u < k1) load_x<WK, NT>(f[u], row, (k0 + u) * kBoxRows + first_row, t, a.D);
+    for (int s = k0; s < k1; s += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (s + u < k1) {
+          c.wait_full();
+          multiply<WK, NT, false>(acc, c.my_box(), c.warp, c.lane, f[u]);
+          c.release();
+          if (s + u + kAhead < k1)
+            load_x<WK, NT>(f[u], row, (s + u + kAhead) * kBoxRows + first_row, t, a.D);
+        }
       }
     }
   }
-  consumer.cur = c.cur;
-  consumer.ok = c.ok;
 
   // Both branches' sums over the block's stages; the whole tile's, or a share of it.
-  const Place<WK> at(c.tid);
   const bool whole = k0 == 0 && k1 == steps;
-  const int f = fb * B::kCols + 2 * at.pair;
   float2* mine = reinterpret_cast<float2*>(
       a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
-  for (int j = 0; j < NT && 8 * j < n; ++j) {
+  for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
     put_tile<WK, NT>(c.red, acc, j, c.warp, c.lane);
     named_bar_sync(kBarConsumers, kConsumers);
-    if (at.active) {
-      const float2 h1 = take_pair(c.red, 0, 4, at.row, at.pair);
-      const float2 h2 = take_pair(c.red, 4, 8, at.row, at.pair);
+    for (int i = c.tid; i < P::kCount; i += kConsumers) {
+      const float2 h1 = take_pair<WK>(c.red, 0, P::row(i), P::col(i));
+      const float2 h2 = take_pair<WK>(c.red, 1, P::row(i), P::col(i));
       if (whole) {
-        finish_h<WK>(a, tb, e, n, 8 * j + at.row, f, h1, h2);
+        finish_h<WK>(a, tb, pt, 8 * j + P::row(i), fb * S::kCols + P::col(i), h1, h2);
       } else {
-        mine[(2 * j) * kConsumers + c.tid] = h1;
-        mine[(2 * j + 1) * kConsumers + c.tid] = h2;
+        mine[(2 * j) * P::kCount + i] = h1;
+        mine[(2 * j + 1) * P::kCount + i] = h2;
       }
     }
     named_bar_sync(kBarConsumers, kConsumers);
@@ -496,109 +529,107 @@ __device__ __noinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& con
   if (whole) return;
   const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
   if (!last_to_finish(a.counters + first, last - first + 1, c.tid, &tb.flag)) return;
-  if (!at.active) return;
-  for (int j = 0; j < NT && 8 * j < n; ++j) {
-    float2 h1 = make_float2(0.0f, 0.0f), h2 = h1;
-    for (int b = first; b <= last; ++b) {
-      const float2* p = reinterpret_cast<const float2*>(
-          a.part + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * a.part_floats);
-      const float2 v1 = __ldcg(p + (2 * j) * kConsumers + c.tid);
-      const float2 v2 = __ldcg(p + (2 * j + 1) * kConsumers + c.tid);
-      h1.x += v1.x;
-      h1.y += v1.y;
-      h2.x += v2.x;
-      h2.y += v2.y;
+  for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
+    for (int i = c.tid; i < P::kCount; i += kConsumers) {
+      float2 h1 = make_float2(0.0f, 0.0f), h2 = h1;
+      for (int b = first; b <= last; ++b) {
+        const float2* p = reinterpret_cast<const float2*>(
+            a.part + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * a.part_floats);
+        const float2 v1 = __ldcg(p + (2 * j) * P::kCount + i);
+        const float2 v2 = __ldcg(p + (2 * j + 1) * P::kCount + i);
+        h1.x += v1.x;
+        h1.y += v1.y;
+        h2.x += v2.x;
+        h2.y += v2.y;
+      }
+      finish_h<WK>(a, tb, pt, 8 * j + P::row(i), fb * S::kCols + P::col(i), h1, h2);
     }
-    finish_h<WK>(a, tb, e, n, 8 * j + at.row, f, h1, h2);
   }
 }
 
-// ---- down: stages [s0, s1) of expert e's part of one column block, added into outacc
+// ---- down: stages [s0, s1) of one piece's part of one column block, added into outacc
 
+// row: this thread's 16 bytes of the piece's first group of each row tile (H is complete: the
+// grid barrier that ordered it lies behind).
 template <int WK, int NT>
-__device__ __forceinline__ void load_h(Frag<WK, NT, true>& f, const uint4* const (&row)[NT],
-                                       int g0, int groups) {
+__device__ __forceinline__ void load_h(Frag<WK, NT, true>& f, const uint8_t* base,
+                                       int64_t tile_bytes, int g0) {
 #pragma unroll
-  for (int s = 0; s < Box<WK>::kK16; ++s) {
+  for (int g = 0; g < Shape<WK>::kGroups; ++g) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (row[j] != nullptr && g0 + s < groups) v = __ldcg(row[j] + (g0 + s) * 4);
-      f.r[s][j][0] = v.x;
-      f.r[s][j][1] = v.y;
-      f.r[s][j][2] = v.z;
-      f.r[s][j][3] = v.w;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            base + j * tile_bytes + static_cast<int64_t>(g0 + g) * kHGroupBytes + q * 512);
+        f.r[g][j][q][0] = v.x;
+        f.r[g][j][q][1] = v.y;
+        f.r[g][j][q][2] = v.z;
+        f.r[g][j][q][3] = v.w;
+      }
     }
   }
 }
 
 template <int WK, int NT>
-__device__ __noinline__ void down_run(const FewArgs& a, Tables& tb, Consumer& consumer, int s0,
-                                      int s1, int e, int cb, float* outacc) {
-  using B = Box<WK>;
-  Consumer c = consumer;  // in registers over the stages
-  const int off = tb.off[e], n = tb.off[e + 1] - off;
-  const int64_t row_bytes = h_row_bytes(WK, a.F);
-  const uint8_t* H = static_cast<const uint8_t*>(a.H) + off * row_bytes;
+__device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer& c, int s0, int s1,
+                                         const Part pt, int cb, float* outacc) {
+  using S = Shape<WK>;
+  using P = Places<WK>;
   Acc<WK, NT> acc;
   acc.zero();
-  // Warp w takes k-rows [w, w+1) * kRows / 4 of the stage's 2 kRows.
-  constexpr int kQuarter = B::kRows / 4;
+  // Warps 0-3 take the stage's first 64 k-rows, warps 4-7 the others.
+  const int first_row = (c.warp >> 2) * kBoxRows + warp_row<WK>(c.warp);
   if constexpr (WK == kF32) {
+    const int64_t row_floats = h_row_f32(a.F);
+    const float* H = static_cast<const float*>(a.H) + pt.row0 * row_floats;
     for (int s = s0; s < s1; ++s) {
       c.wait_full();
-      multiply_f32<NT>(acc, c.my_box(), c.warp & 3, c.lane, n,
-                       s * 2 * B::kRows + c.warp * kQuarter, a.F, [&](int r) {
-                         return reinterpret_cast<const float*>(H + r * row_bytes);
-                       });
+      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, pt.n, s * 2 * kBoxRows + first_row, a.F,
+                       [&](int r) { return H + r * row_floats; });
       c.release();
     }
   } else {
-    const int groups = ((a.F + 63) / 64) * 4;  // 16-value groups that the up phase wrote
-    constexpr int kG = kQuarter / 16;          // per warp and stage
-    const uint4* row[NT];
+    const int64_t tile_bytes = h_groups(a.F) * kHGroupBytes;
+    const uint8_t* base =
+        static_cast<const uint8_t*>(a.H) + pt.tile * tile_bytes + c.lane * 16;
+    const int g0 = first_row / 32;
+    constexpr int kAhead = NT * S::kGroups <= 2 ? 2 : 1;
+    Frag<WK, NT, true> f[kAhead];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int r = 8 * j + (c.lane >> 2);
-      row[j] = r < n ? reinterpret_cast<const uint4*>(H + r * row_bytes) + (c.lane & 3) : nullptr;
-    }
-    Frag<WK, NT, true> f;
-    load_h<WK, NT>(f, row, (s0 * 8 + c.warp) * kG, groups);
-    for (int s = s0; s < s1; ++s) {
-      Frag<WK, NT, true> next;
-      if constexpr (NT * kG <= 4) {
-        if (s + 1 < s1) load_h<WK, NT>(next, row, ((s + 1) * 8 + c.warp) * kG, groups);
-      }
-      c.wait_full();
-      multiply<WK, NT, true>(acc, c.my_box(), c.warp & 3, c.lane, f);
-      c.release();
-      if constexpr (NT * kG <= 4) {
-        f = next;
-      } else {
-        if (s + 1 < s1) load_h<WK, NT>(f, row, ((s + 1) * 8 + c.warp) * kG, groups);
+    for (int u = 0; u < kAhead; ++u)
+      if (s0 + u < s1) load_h<WK, NT>(f[u], base, tile_bytes, (s0 + u) * 4 + g0);
+    for (int s = s0; s < s1; s += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (s + u < s1) {
+          c.wait_full();
+          multiply<WK, NT, true>(acc, c.my_box(), c.warp, c.lane, f[u]);
+          c.release();
+          if (s + u + kAhead < s1)
+            load_h<WK, NT>(f[u], base, tile_bytes, (s + u + kAhead) * 4 + g0);
+        }
       }
     }
   }
-  consumer.cur = c.cur;
-  consumer.ok = c.ok;
-  const Place<WK> at(c.tid);
-  const int d = cb * B::kCols + 2 * at.pair;
-  for (int j = 0; j < NT && 8 * j < n; ++j) {
+  for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
     put_tile<WK, NT>(c.red, acc, j, c.warp, c.lane);
     named_bar_sync(kBarConsumers, kConsumers);
-    const int r = 8 * j + at.row;
-    if (at.active && r < n) {
-      float2 v = take_pair(c.red, 0, kConsumerWarps, at.row, at.pair);
+    for (int i = c.tid; i < P::kCount; i += kConsumers) {
+      const int r = 8 * j + P::row(i);
+      if (r >= pt.n) continue;
+      float2 v = take_pair<WK>(c.red, -1, P::row(i), P::col(i));
       if constexpr (WK == kW8) {
+        const int d = cb * S::kCols + P::col(i);
         if (d < a.D) {
-          const float2 s =
-              __ldg(reinterpret_cast<const float2*>(a.S3 + static_cast<int64_t>(e) * a.D + d));
+          const float2 s = __ldg(reinterpret_cast<const float2*>(
+              a.S3 + static_cast<int64_t>(pt.expert) * a.D + d));
           v.x *= s.x;
           v.y *= s.y;
         }
       }
       float2* o = reinterpret_cast<float2*>(
-          outacc + static_cast<int>(tb.row_tok[off + r]) * B::kCols + 2 * at.pair);
+          outacc + static_cast<int>(tb.row_tok[pt.row0 + r]) * S::kCols + P::col(i));
       o->x += v.x;
       o->y += v.y;
     }
@@ -608,7 +639,7 @@ __device__ __noinline__ void down_run(const FewArgs& a, Tables& tb, Consumer& co
 
 template <int WK>
 __device__ __forceinline__ void store_out(const FewArgs& a, int t, int d, float2 v) {
-  if (t >= a.N || d >= a.D) return;
+  if (d >= a.D) return;
   const int64_t at = static_cast<int64_t>(t) * a.D + d;
   if constexpr (WK == kF32)
     *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = v;
@@ -620,8 +651,8 @@ __device__ __forceinline__ void store_out(const FewArgs& a, int t, int d, float2
   do {                             \
     if ((n) <= 8) CALL(1);         \
     else if ((n) <= 16) CALL(2);   \
-    else if ((n) <= 32) CALL(4);   \
-    else CALL(8);                  \
+    else if ((n) <= 24) CALL(3);   \
+    else CALL(4);                  \
   } while (0)
 
 // ------------------------------------------------------------------ the kernel
@@ -630,20 +661,22 @@ template <int WK>
 __global__ void __launch_bounds__(kThreads, 1)
 few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,
            const __grid_constant__ CUtensorMap m3, const __grid_constant__ FewArgs a) {
-  using B = Box<WK>;
+  using S = Shape<WK>;
+  using P = Places<WK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* red = reinterpret_cast<float*>(smem + kRingBytes);
+  float* red = reinterpret_cast<float*>(smem + static_cast<size_t>(a.stages) * kStageBytes);
   float* outacc = red + kRedFloats;  // the logits first, then the column block's sums
-  Tables& tb = *reinterpret_cast<Tables*>(outacc + kMaxRows * 64);
+  Tables& tb = *reinterpret_cast<Tables*>(
+      reinterpret_cast<uint8_t*>(outacc) + ((out_bytes<WK>(a.N, a.E) + 15) & ~size_t(15)));
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
   const int G = static_cast<int>(gridDim.x);
 
-  Ring ring{smem_u32(smem), tb.full, tb.empty, kStages};
+  Ring ring{smem_u32(smem), tb.full, tb.empty, a.stages};
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < a.stages; ++i) {
       mbar_init(&tb.full[i], 1);
       mbar_init(&tb.empty[i], kConsumerWarps);
     }
@@ -656,7 +689,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
 
   bool ok = true;
   if (warp < kConsumerWarps) {
-    if (a.x_f32) partial_logits<true>(a, red, tid);
+    if constexpr (WK == kF32) partial_logits<true>(a, red, tid);
     else partial_logits<false>(a, red, tid);
     ok = grid_barrier(a.bar, G, tid, &tb.flag, a.timeout_ns, a.err);
     sum_logits(a, outacc, red, tid);
@@ -666,13 +699,13 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   }
   named_bar_sync(kBarAll, kThreads);
 
-  const int up_steps = (a.D + B::kRows - 1) / B::kRows;
-  const int up_cols = (a.F + B::kCols - 1) / B::kCols;
-  const int down_run_steps = (a.F + 2 * B::kRows - 1) / (2 * B::kRows);
-  const int down_cols = (a.D + B::kCols - 1) / B::kCols;
-  const int used = tb.n_used;
-  const int down_steps = used * down_run_steps;
-  SplitK up{static_cast<long long>(used) * up_cols * up_steps, 0};
+  const int up_steps = (a.D + kBoxRows - 1) / kBoxRows;
+  const int up_cols = (a.F + S::kCols - 1) / S::kCols;
+  const int run_steps = (a.F + 2 * kBoxRows - 1) / (2 * kBoxRows);
+  const int down_cols = (a.D + S::kCols - 1) / S::kCols;
+  const int parts = tb.n_parts;
+  const int down_steps = parts * run_steps;
+  SplitK up{static_cast<long long>(parts) * up_cols * up_steps, 0};
   SplitK down{static_cast<long long>(down_cols) * down_steps, 0};
   up.grid = static_cast<int>(min(static_cast<long long>(G), up.total));
   down.grid = static_cast<int>(min(static_cast<long long>(G), down.total));
@@ -684,7 +717,8 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   if (warp == kConsumerWarps) {
     // Producer: one thread issues this block's stages of both products in order.
     if (lane == 0) {
-      const uint64_t policy = l2_policy(-1);  // weights are read once
+      // Weights are read once; evict_first read 6.4 TB/s where the default read 6.0.
+      const uint64_t policy = l2_policy(-1);
       Cursor c;
       bool good = true;
       long long issued = 0;
@@ -692,35 +726,42 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
         const long long tile = s / up_steps;
         int k = static_cast<int>(s - tile * up_steps);
         const int k_end = static_cast<int>(min(static_cast<long long>(up_steps), k + (u1 - s)));
-        const int e = tb.used[tile / up_cols];
-        const int col = static_cast<int>(tile % up_cols) * B::kCols;
+        const int e = tb.part[tile / up_cols].expert;
+        const int col = static_cast<int>(tile % up_cols) * S::kCols;
         s += k_end - k;
         for (; k < k_end; ++k) {
           if (!(good = acquire_stage(ring, c, a.timeout_ns))) break;
           uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
-          tma_load_3d_hint(dst, &m1, &tb.full[c.stage], col, k * B::kRows, e, policy);
-          tma_load_3d_hint(dst + kBoxBytes, &m2, &tb.full[c.stage], col, k * B::kRows, e, policy);
-          c.next(kStages);
+          uint64_t* bar = &tb.full[c.stage];
+          const int row = k * kBoxRows;
+          tma_load_3d_hint(dst, &m1, bar, col, row, e, policy);
+          tma_load_3d_hint(dst + kBoxBytes, &m1, bar, col + S::kBoxCols, row, e, policy);
+          tma_load_3d_hint(dst + 2 * kBoxBytes, &m2, bar, col, row, e, policy);
+          tma_load_3d_hint(dst + 3 * kBoxBytes, &m2, bar, col + S::kBoxCols, row, e, policy);
+          c.next(a.stages);
           ++issued;
         }
       }
       for (long long s = d0; s < d1 && good;) {
         const long long tile = s / down_steps;
         const int in = static_cast<int>(s - tile * down_steps);
-        const int ei = in / down_run_steps;
-        int k = in - ei * down_run_steps;
-        const int k_end =
-            static_cast<int>(min(static_cast<long long>(down_run_steps), k + (d1 - s)));
-        const int e = tb.used[ei];
-        const int col = static_cast<int>(tile) * B::kCols;
+        const int pi = in / run_steps;
+        int k = in - pi * run_steps;
+        const int k_end = static_cast<int>(min(static_cast<long long>(run_steps), k + (d1 - s)));
+        const int e = tb.part[pi].expert;
+        const int col = static_cast<int>(tile) * S::kCols;
         s += k_end - k;
         for (; k < k_end; ++k) {
           if (!(good = acquire_stage(ring, c, a.timeout_ns))) break;
           uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
-          tma_load_3d_hint(dst, &m3, &tb.full[c.stage], col, 2 * k * B::kRows, e, policy);
-          tma_load_3d_hint(dst + kBoxBytes, &m3, &tb.full[c.stage], col, (2 * k + 1) * B::kRows,
-                           e, policy);
-          c.next(kStages);
+          uint64_t* bar = &tb.full[c.stage];
+          const int row = 2 * k * kBoxRows;
+          tma_load_3d_hint(dst, &m3, bar, col, row, e, policy);
+          tma_load_3d_hint(dst + kBoxBytes, &m3, bar, col + S::kBoxCols, row, e, policy);
+          tma_load_3d_hint(dst + 2 * kBoxBytes, &m3, bar, col, row + kBoxRows, e, policy);
+          tma_load_3d_hint(dst + 3 * kBoxBytes, &m3, bar, col + S::kBoxCols, row + kBoxRows, e,
+                           policy);
+          c.next(a.stages);
           ++issued;
         }
       }
@@ -730,73 +771,64 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
     __syncwarp();
   } else {
     if (me == 0) export_routing(a, tb, outacc, tid);
-    if (used == 0) {  // a capacity of zero keeps nothing: zeros
-      const Place<WK> z(tid);
-      for (int cb = me; cb < down_cols && z.active; cb += G)
-        for (int t = z.row; t < a.N; t += 8)
-          store_out<WK>(a, t, cb * B::kCols + 2 * z.pair, make_float2(0.0f, 0.0f));
+    if (parts == 0) {  // a capacity of zero keeps nothing: zeros
+      for (int cb = me; cb < down_cols; cb += G)
+        for (int i = tid; i < a.N * P::kPairs; i += kConsumers)
+          store_out<WK>(a, P::row(i), cb * S::kCols + P::col(i), make_float2(0.0f, 0.0f));
     }
     Consumer c{ring, Cursor{}, red, tid, warp, lane, ok, a.timeout_ns, a.err};
     for (long long s = u0; s < u1;) {
       const long long tile = s / up_steps;
       const int k0 = static_cast<int>(s - tile * up_steps);
       const int k1 = static_cast<int>(min(static_cast<long long>(up_steps), k0 + (u1 - s)));
-      const int e = tb.used[tile / up_cols];
+      const Part pt = tb.part[tile / up_cols];
       const int fb = static_cast<int>(tile % up_cols);
-      const int n = tb.off[e + 1] - tb.off[e];
-#define MOE_UP(NT) up_tile<WK, NT>(a, tb, c, up, tile, up_steps, k0, k1, e, fb)
-      MOE_FEW_ROWS(n, MOE_UP);
+#define MOE_UP(NT) up_tile<WK, NT>(a, tb, c, up, tile, up_steps, k0, k1, pt, fb)
+      MOE_FEW_ROWS(pt.n, MOE_UP);
 #undef MOE_UP
       s += k1 - k0;
     }
     if (!grid_barrier(a.bar, 2 * G, tid, &tb.flag, a.timeout_ns, a.err)) c.ok = false;
 
-    const Place<WK> at(tid);
     for (long long s = d0; s < d1;) {
       const long long tile = s / down_steps;
       const int k0 = static_cast<int>(s - tile * down_steps);
       const int k1 = static_cast<int>(min(static_cast<long long>(down_steps), k0 + (d1 - s)));
       const int cb = static_cast<int>(tile);
-      for (int i = tid; i < a.N * B::kCols; i += kConsumers) outacc[i] = 0.0f;
+      for (int i = tid; i < a.N * S::kCols; i += kConsumers) outacc[i] = 0.0f;
       named_bar_sync(kBarConsumers, kConsumers);
       for (int k = k0; k < k1;) {
-        const int ei = k / down_run_steps;
-        const int s0 = k - ei * down_run_steps;
-        const int s1 = min(down_run_steps, s0 + (k1 - k));
-        const int e = tb.used[ei];
-        const int n = tb.off[e + 1] - tb.off[e];
-#define MOE_DOWN(NT) down_run<WK, NT>(a, tb, c, s0, s1, e, cb, outacc)
-        MOE_FEW_ROWS(n, MOE_DOWN);
+        const int pi = k / run_steps;
+        const int s0 = k - pi * run_steps;
+        const int s1 = min(run_steps, s0 + (k1 - k));
+        const Part pt = tb.part[pi];
+#define MOE_DOWN(NT) down_run<WK, NT>(a, tb, c, s0, s1, pt, cb, outacc)
+        MOE_FEW_ROWS(pt.n, MOE_DOWN);
 #undef MOE_DOWN
         k += s1 - s0;
       }
-      const int d = cb * B::kCols + 2 * at.pair;
       const bool whole = k0 == 0 && k1 == down_steps;
       float2* mine = reinterpret_cast<float2*>(
           a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
-      if (at.active) {
-        for (int t = at.row; t < a.N; t += 8) {
-          const float2 v = *reinterpret_cast<const float2*>(outacc + t * B::kCols + 2 * at.pair);
-          if (whole) store_out<WK>(a, t, d, v);
-          else mine[t * Place<WK>::kPairs + at.pair] = v;
-        }
+      for (int i = tid; i < a.N * P::kPairs; i += kConsumers) {
+        const float2 v = *reinterpret_cast<const float2*>(outacc + 2 * i);
+        if (whole) store_out<WK>(a, P::row(i), cb * S::kCols + P::col(i), v);
+        else mine[i] = v;
       }
       if (!whole) {
         const int first = down.owner(tile * down_steps),
                   last = down.owner(tile * down_steps + down_steps - 1);
-        if (last_to_finish(a.counters + kMaxGrid + first, last - first + 1, tid, &tb.flag) &&
-            at.active) {
-          for (int t = at.row; t < a.N; t += 8) {
+        if (last_to_finish(a.counters + kMaxGrid + first, last - first + 1, tid, &tb.flag)) {
+          for (int i = tid; i < a.N * P::kPairs; i += kConsumers) {
             float2 v = make_float2(0.0f, 0.0f);
             for (int b = first; b <= last; ++b) {
               const float2 p = __ldcg(reinterpret_cast<const float2*>(
                                           a.part + (static_cast<int64_t>(b) * 2 +
-                                                    (b == first ? 1 : 0)) * a.part_floats) +
-                                      t * Place<WK>::kPairs + at.pair);
+                                                    (b == first ? 1 : 0)) * a.part_floats) + i);
               v.x += p.x;
               v.y += p.y;
             }
-            store_out<WK>(a, t, d, v);
+            store_out<WK>(a, P::row(i), cb * S::kCols + P::col(i), v);
           }
         }
       }
@@ -816,22 +848,28 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   }
 }
 
-int64_t part_floats_of(int64_t N) { return ((N + 7) / 8) * 4 * kConsumers; }
+// Floats of a block's share of one tile: two matrices of up to four row tiles, or all tokens.
+int64_t part_floats_of(int kind, int64_t N) {
+  const int64_t cols = kind == kF32 ? Shape<kF32>::kCols
+                       : kind == kBF16 ? Shape<kBF16>::kCols : Shape<kW8>::kCols;
+  return cols * std::max<int64_t>(N, 16 * std::min<int64_t>(4, (N + 7) / 8));
+}
 
 template <int WK>
-cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const void* W2,
+cudaError_t launch(const moe_problem& p, FewArgs& a, const void* W1, const void* W2,
                    const void* W3, cudaStream_t stream) {
   CUtensorMap m1, m2, m3;
   if (!make_stream_map(&m1, W1, WK, p.F, p.D, p.E) || !make_stream_map(&m2, W2, WK, p.F, p.D, p.E) ||
       !make_stream_map(&m3, W3, WK, p.D, p.F, p.E))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(
-      few_kernel<WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+      few_kernel<WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return e;
+  a.stages = stages_for<WK>(a.N, a.E);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min(num_sms(), kMaxGrid)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem_bytes<WK>(a.N, a.E, a.stages);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
@@ -869,15 +907,14 @@ bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, u
   const uint64_t el = kind == kF32 ? 4 : kind == kBF16 ? 2 : 1;
   const cuuint64_t dims[3] = {cols, rows, count};
   const cuuint64_t strides[2] = {cols * el, cols * rows * el};
-  const cuuint32_t box[3] = {kind == kF32 ? 32u : 64u, kind == kW8 ? 128u : 64u, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / el), kBoxRows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType type = kind == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : kind == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return encode_fn()(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     kind == kW8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -885,11 +922,14 @@ bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, u
 size_t few_workspace_bytes(const moe_problem& p) {
   if (p.N < 1 || p.N > kMaxRows) return 0;
   auto up256 = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const size_t rows = static_cast<size_t>(p.N) * p.k;
-  // 8-bit layers keep H in the 16-bit layout; both fit in the larger of the two.
-  const size_t h_row = static_cast<size_t>(h_row_bytes(kBF16, p.F));
+  const int64_t R = p.N * p.k;
+  // bf16 problems may come with either weight kind: the larger of the two.
+  const int kind = p.dtype == MOE_DTYPE_F32 ? kF32 : kW8;
   return up256(sizeof(float) * kMaxSlices * p.N * p.E) + up256(sizeof(int) * 2 * kMaxGrid) +
-         up256(sizeof(float) * 2 * kMaxGrid * part_floats_of(p.N)) + up256(rows * h_row);
+         up256(sizeof(float) * 2 * kMaxGrid * part_floats_of(kind, p.N)) +
+         up256(kind == kF32 ? sizeof(float) * R * h_row_f32(p.F)
+                            : static_cast<size_t>((std::min<int64_t>(p.E, R) + R / 8) *
+                                                  h_groups(p.F) * kHGroupBytes));
 }
 
 cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors& t, void* scratch,
@@ -917,7 +957,7 @@ cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors&
   a.counters = reinterpret_cast<int*>(w);
   w += up256(sizeof(int) * 2 * kMaxGrid);
   a.part = reinterpret_cast<float*>(w);
-  a.part_floats = part_floats_of(p.N);
+  a.part_floats = part_floats_of(p.dtype == MOE_DTYPE_F32 ? kF32 : kW8, p.N);
   w += up256(sizeof(float) * 2 * kMaxGrid * a.part_floats);
   a.H = w;
   a.bar = bar;
@@ -936,7 +976,6 @@ cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors&
   const int groups = (a.N + a.tokens_per_group - 1) / a.tokens_per_group;
   const int grid = std::min(num_sms(), kMaxGrid);
   a.slices = std::max(1, std::min({grid / groups, kMaxSlices, (a.D + 31) / 32}));
-  a.x_f32 = p.dtype == MOE_DTYPE_F32;
   a.renorm = p.renormalize != 0;
   a.token_major = p.capacity_order == MOE_ORDER_TOKEN_MAJOR;
   a.renorm_kept = p.drop_policy == MOE_DROP_RENORM_KEPT;

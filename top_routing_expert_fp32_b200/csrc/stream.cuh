@@ -5,13 +5,22 @@
 //   - the work is cut into equal runs of stages, one per block, whatever the tile count
 //     (SplitK): a tile whose reduction is shared by several blocks is summed by the last of
 //     them to finish, in block order, so the result does not depend on timing;
-//   - the loads run ahead of the arithmetic by the whole ring (160 KB and more per SM, above the
+//   - a stage's rows are 256 contiguous bytes (two 128-byte boxes side by side): with 128 bytes
+//     the same loop without arithmetic read 5.5 TB/s, with 256 bytes 6.4 TB/s (2.6 GB of weights);
+//   - the loads run ahead of the arithmetic by the whole ring (128 KB or more per SM, above the
 //     44 KB per SM that 6.5 TB/s times a microsecond of latency needs), also across grid
 //     barriers: weights do not depend on what the barrier waits for.
 // 16-bit weights [k][n] (n contiguous) become the row operand of mma.m16n8k16 through transposed
 // ldmatrix (16 output columns x 16 k per instruction), the activation rows its 8 columns: one
 // instruction per 512 bytes of weights and 8 rows, far from the tensor cores' limit, where the
 // tcgen05 tiles of 64 or 128 rows would mostly multiply padding.
+//
+// Order of k. Within 32 k-rows, thread t of a quad holds the 8 consecutive values k = 8t..8t+7 of
+// an activation row (one 16-byte load), that is four pairs w = 0..3. The instructions need them in
+// four blocks; block b takes each thread's pair w = (b + t) & 3, and the transposed loads fetch
+// the matching weight rows 8t + 2w + {0, 1}: any one-to-one order of k gives the same sum, and
+// this one makes the eight weight rows of a block differ modulo 8, so the swizzled shared-memory
+// reads have no bank conflicts.
 #pragma once
 
 #include "common.cuh"
@@ -24,28 +33,39 @@ enum WeightKind { kBF16 = 0, kF32 = 1, kW8 = 2 };
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kThreads = kConsumers + 32;  // + the producer warp
-constexpr int kBoxBytes = 8192;            // one TMA box
-constexpr int kStageBytes = 2 * kBoxBytes;
-constexpr int kMaxRows = 64;               // activation rows of one product
-constexpr int kMaxGrid = 148;              // blocks (one per SM)
+constexpr int kBoxRows = 64;               // one TMA box: 64 k-rows of 128 bytes, swizzled
+constexpr int kBoxBytes = kBoxRows * 128;
+constexpr int kStageBytes = 4 * kBoxBytes;
+constexpr int kMaxStages = 6;
+constexpr int kMaxRows = 64;     // activation rows of one call
+constexpr int kTileRows = 32;    // activation rows of one product (up to four tiles of 8)
+constexpr int kMaxGrid = 148;    // blocks (one per SM)
 constexpr int kBarConsumers = 1, kBarAll = 2;  // named barriers
 
-// A box is kBoxRows k-rows by kCols output columns (128-byte rows; 64-byte rows for 8-bit
-// weights). Warp w of a stage takes box w/4 and the (w%4)-th quarter of its rows.
+// A stage is four boxes: two side by side (kCols output columns) times either two matrices with
+// the same 64 k-rows, or 128 k-rows of one matrix. Warp w takes box w/2; for 16- and 32-bit
+// weights the (w%2)-th half of its k-rows, for 8-bit weights the (w%2)-th half of its columns.
+// Either way a warp sums kSeg columns.
 template <int WK>
-struct Box;
+struct Shape;
 template <>
-struct Box<kBF16> {
-  static constexpr int kCols = 64, kRows = 64, kK16 = 1;
+struct Shape<kBF16> {
+  static constexpr int kCols = 128, kBoxCols = 64, kSeg = 64, kGroups = 1;  // 32-row groups
 };
 template <>
-struct Box<kF32> {
-  static constexpr int kCols = 32, kRows = 64, kK16 = 1;
+struct Shape<kF32> {
+  static constexpr int kCols = 64, kBoxCols = 32, kSeg = 32, kGroups = 1;
 };
 template <>
-struct Box<kW8> {
-  static constexpr int kCols = 64, kRows = 128, kK16 = 2;
+struct Shape<kW8> {
+  static constexpr int kCols = 256, kBoxCols = 128, kSeg = 64, kGroups = 2;
 };
+
+// First k-row of a warp within its box, and its first column segment within the tile.
+template <int WK>
+__device__ __forceinline__ int warp_row(int warp) {
+  return WK == kW8 ? 0 : (warp & 1) * 32;
+}
 
 // Equal runs of the `total` stages of a product over `grid` blocks: block c takes
 // [start(c), start(c+1)).
@@ -104,8 +124,8 @@ __device__ __forceinline__ uint32_t i8x2_to_bf16x2(uint32_t v) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// fp32 sums of this warp's k-quarter: kCols columns by 8*NT rows.
-//   mma kinds: v[((m * NT) + j) * 4 + c] for the 16-column group m and row tile j.
+// fp32 sums of one warp: kSeg columns by 8*NT rows.
+//   mma kinds: v[(m * NT + j) * 4 + c] for the 16-column group m and row tile j.
 //   fp32:      v[row], column = lane.
 template <int WK, int NT>
 struct Acc {
@@ -117,86 +137,114 @@ struct Acc {
   }
 };
 
-// The activation operand of one stage: NT row tiles, kK16 k-steps of 16; with SPLIT each value
-// is the sum of two bf16 terms (words 0-1 and 2-3).
+// One thread's activation values of one stage: for each 32-row group and row tile the four
+// blocks' pairs; with SPLIT each value is the sum of two bf16 terms (planes 0 and 1).
 template <int WK, int NT, bool SPLIT>
 struct Frag {
-  uint32_t r[Box<WK>::kK16][NT][SPLIT ? 4 : 2];
+  uint32_t r[Shape<WK>::kGroups][NT][SPLIT ? 2 : 1][4];
 };
 
-// acc += (this warp's quarter of the box)^T x rows. `box`: shared address of the box, `quarter`:
-// 0..3.
+// The 16 bytes of thread t (pairs w = 0..3) in block order: out[b] = pair (b + t) & 3.
+__device__ __forceinline__ void to_blocks(const uint4& v, int t, uint32_t (&out)[4]) {
+  const bool one = (t & 1) != 0, two = (t & 2) != 0;
+  const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
+                 a3 = one ? v.x : v.w;
+  out[0] = two ? a2 : a0;
+  out[1] = two ? a3 : a1;
+  out[2] = two ? a0 : a2;
+  out[3] = two ? a1 : a3;
+}
+
+// Row of a 32-row group that lane l of a transposed load addresses for block b.
+__device__ __forceinline__ uint32_t block_row(int b, int i) {
+  const int t = i >> 1;
+  return static_cast<uint32_t>(8 * t + 2 * ((b + t) & 3) + (i & 1));
+}
+
+// acc += (this warp's part of its box)^T x rows. `box`: shared address of the box.
 template <int WK, int NT, bool SPLIT>
-__device__ __forceinline__ void multiply(Acc<WK, NT>& acc, uint32_t box, int quarter, int lane,
+__device__ __forceinline__ void multiply(Acc<WK, NT>& acc, uint32_t box, int warp, int lane,
                                          const Frag<WK, NT, SPLIT>& f) {
   const int b = lane >> 3, i = lane & 7;
   if constexpr (WK == kBF16) {
-    // 8x8 blocks (columns lo/hi) x (k lo/hi) of a 16 x 16 piece, 128-byte swizzled rows.
-    const uint32_t row = box + static_cast<uint32_t>(quarter * 16 + (b >> 1) * 8 + i) * 128;
+    // Matrices of one load: (column halves lo, hi) x (blocks 2s, 2s + 1).
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      uint32_t a[4];
-      ldsm_x4_trans(row + static_cast<uint32_t>(((m * 2 + (b & 1)) ^ i) << 4), a);
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t r = block_row(2 * s + (b >> 1), i);
+      const uint32_t row = box + (static_cast<uint32_t>(warp & 1) * 32 + r) * 128;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[0][j][0], f.r[0][j][1]);
-        if constexpr (SPLIT) mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[0][j][2], f.r[0][j][3]);
+      for (int m = 0; m < 4; ++m) {
+        uint32_t a[4];
+        ldsm_x4_trans(row + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (r & 7u)) << 4), a);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+          for (int q = 0; q < (SPLIT ? 2 : 1); ++q)
+            mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[0][j][q][2 * s], f.r[0][j][q][2 * s + 1]);
+        }
       }
     }
   } else {
-    // 16-byte blocks of 8 k-rows: as 16-bit elements, a transposed 8x8 block gives each thread
-    // the bytes of columns 2g and 2g+1 at k = 2t and 2t+1; the even columns take the
-    // instruction's rows 0-7 and the odd ones rows 8-15.
-    const uint32_t row = static_cast<uint32_t>(quarter * 32 + b * 8 + i);
+    // One load takes 16 columns (bytes) of all four blocks: as 16-bit elements, a transposed
+    // 8x8 matrix gives each thread the bytes of columns 2g and 2g+1 at its pair of k; the even
+    // columns take the instruction's rows 0-7 and the odd ones rows 8-15.
+    const uint32_t r = block_row(b, i);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      uint32_t q[4];
-      ldsm_x4_trans(box + row * 64 + ((static_cast<uint32_t>(m) ^ ((row >> 1) & 3u)) << 4), q);
+    for (int g = 0; g < Shape<WK>::kGroups; ++g) {
+      const uint32_t row = box + (static_cast<uint32_t>(g) * 32 + r) * 128;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint32_t a[4];
+      for (int m = 0; m < 4; ++m) {
+        uint32_t p[4];
+        ldsm_x4_trans(row + ((static_cast<uint32_t>((warp & 1) * 4 + m) ^ (r & 7u)) << 4), p);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t v = q[2 * s + h];
-          a[2 * h] = i8x2_to_bf16x2(v & 0x00FF00FFu);
-          a[2 * h + 1] = i8x2_to_bf16x2((v >> 8) & 0x00FF00FFu);
-        }
+        for (int s = 0; s < 2; ++s) {
+          uint32_t a[4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[s][j][0], f.r[s][j][1]);
-          if constexpr (SPLIT)
-            mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[s][j][2], f.r[s][j][3]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t v = p[2 * s + h];
+            a[2 * h] = i8x2_to_bf16x2(v & 0x00FF00FFu);
+            a[2 * h + 1] = i8x2_to_bf16x2((v >> 8) & 0x00FF00FFu);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int q = 0; q < (SPLIT ? 2 : 1); ++q)
+              mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[g][j][q][2 * s], f.r[g][j][q][2 * s + 1]);
+          }
         }
       }
     }
   }
 }
 
-// fp32 weights on the CUDA cores: acc.v[r] += sum over the quarter's 16 k of W[k][lane] x_r[k].
+// fp32 weights on the CUDA cores: acc.v[r] += sum over the warp's 32 k-rows of W[k][lane] x_r[k].
 // row(r): row r's values (global memory), k0: its first k here, K: the reduction length.
 template <int NT, typename RowPtr>
-__device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, int quarter,
-                                             int lane, int n_rows, int k0, int K, RowPtr row) {
-  float w[16];
+__device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, int warp, int lane,
+                                             int n_rows, int k0, int K, RowPtr row) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t r = static_cast<uint32_t>(quarter * 16 + i);
-    const uint32_t at = box + r * 128 + (((static_cast<uint32_t>(lane) >> 2) ^ (r & 7u)) << 4) +
-                        (static_cast<uint32_t>(lane) & 3u) * 4;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at) : "memory");
-  }
+  for (int h = 0; h < 2; ++h) {
+    float w[16];
 #pragma unroll
-  for (int r = 0; r < 8 * NT; ++r) {
-    if (r < n_rows) {
-      const float* x = row(r) + k0;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t r = static_cast<uint32_t>((warp & 1) * 32 + h * 16 + i);
+      const uint32_t at = box + r * 128 + (((static_cast<uint32_t>(lane) >> 2) ^ (r & 7u)) << 4) +
+                          (static_cast<uint32_t>(lane) & 3u) * 4;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at) : "memory");
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (k0 + 4 * q < K) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(x + 4 * q));
-          acc.v[r] = fmaf(w[4 * q], v.x, acc.v[r]);
-          acc.v[r] = fmaf(w[4 * q + 1], v.y, acc.v[r]);
-          acc.v[r] = fmaf(w[4 * q + 2], v.z, acc.v[r]);
-          acc.v[r] = fmaf(w[4 * q + 3], v.w, acc.v[r]);
+    for (int r = 0; r < 8 * NT; ++r) {
+      if (r < n_rows) {
+        const float* x = row(r) + k0 + h * 16;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (k0 + h * 16 + 4 * q < K) {
+            const float4 v = *reinterpret_cast<const float4*>(x + 4 * q);
+            acc.v[r] = fmaf(w[4 * q], v.x, acc.v[r]);
+            acc.v[r] = fmaf(w[4 * q + 1], v.y, acc.v[r]);
+            acc.v[r] = fmaf(w[4 * q + 2], v.z, acc.v[r]);
+            acc.v[r] = fmaf(w[4 * q + 3], v.w, acc.v[r]);
+          }
         }
       }
     }
@@ -212,56 +260,58 @@ template <int WK, int NT>
 __device__ __forceinline__ void put_tile(float* red, const Acc<WK, NT>& acc, int j, int warp,
                                          int lane) {
   float* mine = red + warp * 8 * kRedPitch;
-  if constexpr (WK == kF32) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      float v = 0.0f;
+  for (int jj = 0; jj < NT; ++jj) {
+    if (jj != j) continue;
+    if constexpr (WK == kF32) {
 #pragma unroll
-      for (int jj = 0; jj < NT; ++jj)
-        if (jj == j) v = acc.v[8 * jj + r];
-      mine[r * kRedPitch + lane] = v;
-    }
-  } else {
-    const int g = lane >> 2, t = lane & 3;
+      for (int r = 0; r < 8; ++r) mine[r * kRedPitch + lane] = acc.v[8 * jj + r];
+    } else {
+      const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-#pragma unroll
-      for (int jj = 0; jj < NT; ++jj) {
-        if (jj == j) {
-          const float* c = &acc.v[(m * NT + jj) * 4];
-          const int lo = WK == kW8 ? 16 * m + 2 * g : 16 * m + g;
-          const int hi = WK == kW8 ? lo + 1 : lo + 8;
-          mine[(2 * t) * kRedPitch + lo] = c[0];
-          mine[(2 * t + 1) * kRedPitch + lo] = c[1];
-          mine[(2 * t) * kRedPitch + hi] = c[2];
-          mine[(2 * t + 1) * kRedPitch + hi] = c[3];
-        }
+      for (int m = 0; m < 4; ++m) {
+        const float* c = &acc.v[(m * NT + jj) * 4];
+        const int lo = WK == kW8 ? 16 * m + 2 * g : 16 * m + g;
+        const int hi = WK == kW8 ? lo + 1 : lo + 8;
+        mine[(2 * t) * kRedPitch + lo] = c[0];
+        mine[(2 * t + 1) * kRedPitch + lo] = c[1];
+        mine[(2 * t) * kRedPitch + hi] = c[2];
+        mine[(2 * t + 1) * kRedPitch + hi] = c[3];
       }
     }
   }
 }
 
-// Sum of warps [w0, w1) at (row, columns 2 pair and 2 pair + 1), in warp order.
-__device__ __forceinline__ float2 take_pair(const float* red, int w0, int w1, int row, int pair) {
+// A thread's places in an epilogue pass over 8 rows by kCols columns, two columns at a time:
+// i = tid, tid + kConsumers, ... < Places<WK>::kCount.
+template <int WK>
+struct Places {
+  static constexpr int kPairs = Shape<WK>::kCols / 2;
+  static constexpr int kCount = 8 * kPairs;
+  __device__ static int row(int i) { return i / kPairs; }
+  __device__ static int col(int i) { return 2 * (i % kPairs); }
+};
+
+// Sum, in warp order, of the warps that hold columns col and col + 1 of `row`: of the matrix
+// `branch` (0, 1) of a two-matrix stage, or of all (branch < 0).
+template <int WK>
+__device__ __forceinline__ float2 take_pair(const float* red, int branch, int row, int col) {
+  const int seg = col / Shape<WK>::kSeg, in = col % Shape<WK>::kSeg;
   float2 s = make_float2(0.0f, 0.0f);
-  for (int w = w0; w < w1; ++w) {
-    const float2 v =
-        *reinterpret_cast<const float2*>(red + (w * 8 + row) * kRedPitch + 2 * pair);
-    s.x += v.x;
-    s.y += v.y;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (branch >= 0 && half != branch) continue;
+    // 16/32-bit: segment = box of the pair, two warps each; 8-bit: segment = warp.
+#pragma unroll
+    for (int q = 0; q < (WK == kW8 ? 1 : 2); ++q) {
+      const int w = half * 4 + (WK == kW8 ? seg : seg * 2 + q);
+      const float2 v = *reinterpret_cast<const float2*>(red + (w * 8 + row) * kRedPitch + in);
+      s.x += v.x;
+      s.y += v.y;
+    }
   }
   return s;
 }
-
-// A thread's place in an epilogue pass over 8 rows by kCols columns.
-template <int WK>
-struct Place {
-  static constexpr int kPairs = Box<WK>::kCols / 2;
-  int row, pair;
-  bool active;
-  __device__ explicit Place(int tid)
-      : row(tid / kPairs), pair(tid % kPairs), active(tid < 8 * kPairs) {}
-};
 
 // All consumer threads of every block: arrive, wait until `target` arrivals (bounded). The
 // block's earlier global writes are visible to the others afterwards. False: the wait ran out.
@@ -330,10 +380,10 @@ __device__ __forceinline__ void drain(const Ring& ring, const Cursor& end, long 
   }
 }
 
-// 3-D map over stacked weights [count][rows][cols] (cols contiguous) in boxes of Box<kind>;
-// elements past the edges read as zero. Defined in few.cu.
 }  // namespace stream
 
+// 3-D map over stacked weights [count][rows][cols] (cols contiguous) of a stream::WeightKind in
+// boxes of 64 rows x 128 bytes, 128-byte swizzle; elements past the edges read as zero.
 bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, uint64_t rows,
                      uint64_t count);
 
