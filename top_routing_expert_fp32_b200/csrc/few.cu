@@ -67,7 +67,6 @@ struct FewArgs {
   uint64_t timeout_ns;
   int N, D, F, E, k;
   int tokens_per_group, slices;  // router split
-  int stages;
   bool renorm, token_major, renorm_kept;
   int act;
 };
@@ -81,6 +80,7 @@ struct Part {
 
 struct Tables {
   uint64_t full[kMaxStages];
+  uint64_t rows_full[kMaxStages];
   uint64_t empty[kMaxStages];
   float gate[kMaxRecords];
   float row_gate[kMaxRecords];
@@ -90,6 +90,7 @@ struct Tables {
   int off[kMaxE + 1];
   Part part[kMaxParts];
   int n_parts;
+  int max_rows;  // of any piece
   int flag;
   int16_t row_tok[kMaxRecords];
   int16_t pos[kMaxRecords];
@@ -97,25 +98,25 @@ struct Tables {
 };
 
 // Shared memory: the ring, the warps' sums, the column block's sums per token (first the
-// logits), the tables. The ring takes what the batch leaves, 6 stages for small ones.
+// logits), the tables. The ring takes what the batch leaves; how many stages that makes depends
+// on the rows of the largest piece, which the kernel learns from the routing.
 template <int WK>
 constexpr size_t out_bytes(int N, int E) {
-  return sizeof(float) * static_cast<size_t>(N) *
-         static_cast<size_t>(E > Shape<WK>::kCols ? E : Shape<WK>::kCols);
-}
-template <int WK>
-constexpr size_t smem_bytes(int N, int E, int stages) {
-  return 1024 + static_cast<size_t>(stages) * kStageBytes + sizeof(float) * kRedFloats +
-         out_bytes<WK>(N, E) + sizeof(Tables) + 16;
+  return (sizeof(float) * static_cast<size_t>(N) *
+              static_cast<size_t>(E > Shape<WK>::kCols ? E : Shape<WK>::kCols) + 15) & ~size_t(15);
 }
 constexpr size_t kMaxSmem = 232448;
 template <int WK>
-int stages_for(int N, int E) {
-  int s = kMaxStages;
-  while (s > 2 && smem_bytes<WK>(N, E, s) > kMaxSmem) --s;
-  return s;
+__host__ __device__ constexpr size_t ring_bytes(int N, int E) {
+  return (kMaxSmem - 1024 - sizeof(float) * kRedFloats - out_bytes<WK>(N, E) - sizeof(Tables)) &
+         ~size_t(1023);
 }
-static_assert(smem_bytes<kW8>(kMaxRows, kMaxE, 4) <= kMaxSmem, "at least four stages");
+__host__ __device__ constexpr int ring_stages(size_t bytes, int row_tiles) {
+  const int s = static_cast<int>(bytes / (kStageBytes + static_cast<size_t>(row_tiles) * kTileBytes));
+  return s < kMaxStages ? s : kMaxStages;
+}
+static_assert(ring_stages(ring_bytes<kW8>(kMaxRows, kMaxE), kTileRows / 8) >= 2, "ring of two");
+static_assert(ring_stages(ring_bytes<kBF16>(kMaxRows, kMaxE), kTileRows / 8) >= 3, "ring of three");
 
 // H. 16-bit kinds: per tile of 8 rows and 32 values of F two planes (the first and the second
 // bf16 term) of 32 threads x 16 bytes, each thread's four pairs in block order (stream.cuh):
@@ -314,6 +315,8 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
         tb.part[part + q] = {static_cast<int16_t>(e), static_cast<int16_t>(row + q * kTileRows),
                              static_cast<int16_t>(min(kTileRows, n - q * kTileRows)),
                              static_cast<int16_t>(tile + q * (kTileRows / 8))};
+      const int most = __reduce_max_sync(0xFFFFFFFFu, n);
+      if (lane == 0) tb.max_rows = e0 == 0 ? most : max(tb.max_rows, most);
       before += total & 0xFFF;
       parts += (total >> 12) & 0xFF;
       tiles += total >> 20;
@@ -379,15 +382,17 @@ struct Consumer {
   int* err;
 
   __device__ void wait_full() {
-    if (ok && !mbar_wait(&ring.full[cur.stage], cur.phase, timeout_ns)) {
+    if (ok && (!mbar_wait(&ring.full[cur.stage], cur.phase, timeout_ns) ||
+               !mbar_wait(&ring.rows_full[cur.stage], cur.phase, timeout_ns))) {
       ok = false;
       record_error(err, MOE_DEVERR_WAIT_TIMEOUT);
     }
   }
   __device__ uint32_t my_box() const {
-    return ring.base + static_cast<uint32_t>(cur.stage) * kStageBytes +
+    return smem_u32(ring.weights) + static_cast<uint32_t>(cur.stage) * kStageBytes +
            static_cast<uint32_t>(warp >> 1) * kBoxBytes;
   }
+  __device__ const uint8_t* rows() const { return ring.rows + cur.stage * ring.row_bytes; }
   __device__ void release() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.empty[cur.stage]);
@@ -396,22 +401,6 @@ struct Consumer {
 };
 
 // ---- up: stages [k0, k1) of one column tile of one piece
-
-template <int WK, int NT>
-__device__ __forceinline__ void load_x(Frag<WK, NT, false>& f,
-                                       const __nv_bfloat16* const (&row)[NT], int d0, int t,
-                                       int D) {
-#pragma unroll
-  for (int g = 0; g < Shape<WK>::kGroups; ++g) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int d = d0 + 32 * g;  // row[j] is already at 8 t
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (row[j] != nullptr && d + 8 * t < D) v = __ldg(reinterpret_cast<const uint4*>(row[j] + d));
-      to_blocks(v, t, f.r[g][j][0]);
-    }
-  }
-}
 
 // Two H values of row r of a piece: columns f, f + 1 (f even).
 template <int WK>
@@ -464,46 +453,23 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
                                         int k1, const Part pt, int fb) {
   using S = Shape<WK>;
   using P = Places<WK>;
-  const int16_t* tok = tb.row_tok + pt.row0;
   Acc<WK, NT> acc;
   acc.zero();
   const int first_row = warp_row<WK>(c.warp);
-  if constexpr (WK == kF32) {
-    const float* X = static_cast<const float*>(a.X);
-    for (int s = k0; s < k1; ++s) {
-      c.wait_full();
-      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, pt.n, s * kBoxRows + first_row, a.D,
-                       [&](int r) { return X + static_cast<int64_t>(tok[r]) * a.D; });
+  for (int s = k0; s < k1; ++s) {
+    c.wait_full();
+    const int d0 = s * kBoxRows + first_row;
+    if constexpr (WK == kF32) {
+      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, c.rows() + first_row * 4, kRowPitchF32,
+                       pt.n, d0, a.D);
       c.release();
-    }
-  } else {
-    const int t = c.lane & 3;
-    const __nv_bfloat16* row[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int r = 8 * j + (c.lane >> 2);
-      row[j] = r < pt.n ? static_cast<const __nv_bfloat16*>(a.X) +
-                              static_cast<int64_t>(tok[r]) * a.D + 8 * t
-                        : nullptr;
-    }
-    // The rows' values are loaded kAhead stages before their use: an L2 access takes longer
-    // than a stage's arithmetic.
-    constexpr int kAhead = NT * S::kGroups <= 4 ? 2 : 1;
-    Frag<WK, NT, false> f[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (k0 + u < k1) load_x<WK, NT>(f[u], row, (k0 + u) * kBoxRows + first_row, t, a.D);
-    for (int s = k0; s < k1; s += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (s + u < k1) {
-          c.wait_full();
-          multiply<WK, NT, false>(acc, c.my_box(), c.warp, c.lane, f[u]);
-          c.release();
-          if (s + u + kAhead < k1)
-            load_x<WK, NT>(f[u], row, (s + u + kAhead) * kBoxRows + first_row, t, a.D);
-        }
-      }
+    } else {
+      Weights<WK> w;
+      Frag<WK, NT, false> f;
+      w.load(c.my_box(), c.warp, c.lane);
+      f.load_rows(c.rows(), kRowPitch, first_row / 32, d0, a.D, c.lane);
+      c.release();
+      multiply<WK, NT, false>(acc, w, f);
     }
   }
 
@@ -549,28 +515,6 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
 
 // ---- down: stages [s0, s1) of one piece's part of one column block, added into outacc
 
-// row: this thread's 16 bytes of the piece's first group of each row tile (H is complete: the
-// grid barrier that ordered it lies behind).
-template <int WK, int NT>
-__device__ __forceinline__ void load_h(Frag<WK, NT, true>& f, const uint8_t* base,
-                                       int64_t tile_bytes, int g0) {
-#pragma unroll
-  for (int g = 0; g < Shape<WK>::kGroups; ++g) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint4 v = *reinterpret_cast<const uint4*>(
-            base + j * tile_bytes + static_cast<int64_t>(g0 + g) * kHGroupBytes + q * 512);
-        f.r[g][j][q][0] = v.x;
-        f.r[g][j][q][1] = v.y;
-        f.r[g][j][q][2] = v.z;
-        f.r[g][j][q][3] = v.w;
-      }
-    }
-  }
-}
-
 template <int WK, int NT>
 __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer& c, int s0, int s1,
                                          const Part pt, int cb, float* outacc) {
@@ -580,36 +524,19 @@ __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer&
   acc.zero();
   // Warps 0-3 take the stage's first 64 k-rows, warps 4-7 the others.
   const int first_row = (c.warp >> 2) * kBoxRows + warp_row<WK>(c.warp);
-  if constexpr (WK == kF32) {
-    const int64_t row_floats = h_row_f32(a.F);
-    const float* H = static_cast<const float*>(a.H) + pt.row0 * row_floats;
-    for (int s = s0; s < s1; ++s) {
-      c.wait_full();
-      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, pt.n, s * 2 * kBoxRows + first_row, a.F,
-                       [&](int r) { return H + r * row_floats; });
+  for (int s = s0; s < s1; ++s) {
+    c.wait_full();
+    if constexpr (WK == kF32) {
+      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, c.rows() + first_row * 4,
+                       2 * kBoxRows * 4, pt.n, s * 2 * kBoxRows + first_row, a.F);
       c.release();
-    }
-  } else {
-    const int64_t tile_bytes = h_groups(a.F) * kHGroupBytes;
-    const uint8_t* base =
-        static_cast<const uint8_t*>(a.H) + pt.tile * tile_bytes + c.lane * 16;
-    const int g0 = first_row / 32;
-    constexpr int kAhead = NT * S::kGroups <= 2 ? 2 : 1;
-    Frag<WK, NT, true> f[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (s0 + u < s1) load_h<WK, NT>(f[u], base, tile_bytes, (s0 + u) * 4 + g0);
-    for (int s = s0; s < s1; s += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (s + u < s1) {
-          c.wait_full();
-          multiply<WK, NT, true>(acc, c.my_box(), c.warp, c.lane, f[u]);
-          c.release();
-          if (s + u + kAhead < s1)
-            load_h<WK, NT>(f[u], base, tile_bytes, (s + u + kAhead) * 4 + g0);
-        }
-      }
+    } else {
+      Weights<WK> w;
+      Frag<WK, NT, true> f;
+      w.load(c.my_box(), c.warp, c.lane);
+      f.load_ordered(c.rows(), first_row / 32, c.lane);
+      c.release();
+      multiply<WK, NT, true>(acc, w, f);
     }
   }
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
@@ -666,18 +593,19 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* red = reinterpret_cast<float*>(smem + static_cast<size_t>(a.stages) * kStageBytes);
+  const size_t ring_size = ring_bytes<WK>(a.N, a.E);
+  float* red = reinterpret_cast<float*>(smem + ring_size);
   float* outacc = red + kRedFloats;  // the logits first, then the column block's sums
-  Tables& tb = *reinterpret_cast<Tables*>(
-      reinterpret_cast<uint8_t*>(outacc) + ((out_bytes<WK>(a.N, a.E) + 15) & ~size_t(15)));
+  Tables& tb = *reinterpret_cast<Tables*>(reinterpret_cast<uint8_t*>(outacc) +
+                                          out_bytes<WK>(a.N, a.E));
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
   const int G = static_cast<int>(gridDim.x);
 
-  Ring ring{smem_u32(smem), tb.full, tb.empty, a.stages};
   if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&tb.full[i], 1);
+      mbar_init(&tb.rows_full[i], 1);
       mbar_init(&tb.empty[i], kConsumerWarps);
     }
     fence_barrier_init();
@@ -714,60 +642,143 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   const long long d0 = me < down.grid ? down.start(me) : 0,
                   d1 = me < down.grid ? down.start(me + 1) : 0;
 
+  const int row_tiles = max(1, min(kTileRows, tb.max_rows) + 7) / 8;
+  Ring ring;
+  ring.stages = ring_stages(ring_size, row_tiles);
+  ring.row_bytes = row_tiles * kTileBytes;
+  ring.weights = smem;
+  ring.rows = smem + static_cast<size_t>(ring.stages) * kStageBytes;
+  ring.full = tb.full;
+  ring.rows_full = tb.rows_full;
+  ring.empty = tb.empty;
+
+  // Stages in order: f_up(piece, column tile, k-stage), then f_down(piece, column block, k-stage);
+  // a callback that returns false ends the walk.
+  auto walk = [&](auto f_up, auto between, auto f_down) {
+    for (long long s = u0; s < u1;) {
+      const long long tile = s / up_steps;
+      int k = static_cast<int>(s - tile * up_steps);
+      const int k_end = static_cast<int>(min(static_cast<long long>(up_steps), k + (u1 - s)));
+      const Part pt = tb.part[tile / up_cols];
+      const int fb = static_cast<int>(tile % up_cols);
+      s += k_end - k;
+      for (; k < k_end; ++k)
+        if (!f_up(pt, fb, k)) return;
+    }
+    between();
+    for (long long s = d0; s < d1;) {
+      const long long tile = s / down_steps;
+      const int in = static_cast<int>(s - tile * down_steps);
+      const int pi = in / run_steps;
+      int k = in - pi * run_steps;
+      const int k_end = static_cast<int>(min(static_cast<long long>(run_steps), k + (d1 - s)));
+      const Part pt = tb.part[pi];
+      s += k_end - k;
+      for (; k < k_end; ++k)
+        if (!f_down(pt, static_cast<int>(tile), k)) return;
+    }
+  };
+
   if (warp == kConsumerWarps) {
-    // Producer: one thread issues this block's stages of both products in order.
+    // Weight producer: one thread issues this block's stages of both products in order.
     if (lane == 0) {
       // Weights are read once; evict_first read 6.4 TB/s where the default read 6.0.
       const uint64_t policy = l2_policy(-1);
       Cursor c;
       bool good = true;
       long long issued = 0;
-      for (long long s = u0; s < u1 && good;) {
-        const long long tile = s / up_steps;
-        int k = static_cast<int>(s - tile * up_steps);
-        const int k_end = static_cast<int>(min(static_cast<long long>(up_steps), k + (u1 - s)));
-        const int e = tb.part[tile / up_cols].expert;
-        const int col = static_cast<int>(tile % up_cols) * S::kCols;
-        s += k_end - k;
-        for (; k < k_end; ++k) {
-          if (!(good = acquire_stage(ring, c, a.timeout_ns))) break;
-          uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
-          uint64_t* bar = &tb.full[c.stage];
-          const int row = k * kBoxRows;
-          tma_load_3d_hint(dst, &m1, bar, col, row, e, policy);
-          tma_load_3d_hint(dst + kBoxBytes, &m1, bar, col + S::kBoxCols, row, e, policy);
-          tma_load_3d_hint(dst + 2 * kBoxBytes, &m2, bar, col, row, e, policy);
-          tma_load_3d_hint(dst + 3 * kBoxBytes, &m2, bar, col + S::kBoxCols, row, e, policy);
-          c.next(a.stages);
-          ++issued;
-        }
-      }
-      for (long long s = d0; s < d1 && good;) {
-        const long long tile = s / down_steps;
-        const int in = static_cast<int>(s - tile * down_steps);
-        const int pi = in / run_steps;
-        int k = in - pi * run_steps;
-        const int k_end = static_cast<int>(min(static_cast<long long>(run_steps), k + (d1 - s)));
-        const int e = tb.part[pi].expert;
-        const int col = static_cast<int>(tile) * S::kCols;
-        s += k_end - k;
-        for (; k < k_end; ++k) {
-          if (!(good = acquire_stage(ring, c, a.timeout_ns))) break;
-          uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
-          uint64_t* bar = &tb.full[c.stage];
-          const int row = 2 * k * kBoxRows;
-          tma_load_3d_hint(dst, &m3, bar, col, row, e, policy);
-          tma_load_3d_hint(dst + kBoxBytes, &m3, bar, col + S::kBoxCols, row, e, policy);
-          tma_load_3d_hint(dst + 2 * kBoxBytes, &m3, bar, col, row + kBoxRows, e, policy);
-          tma_load_3d_hint(dst + 3 * kBoxBytes, &m3, bar, col + S::kBoxCols, row + kBoxRows, e,
-                           policy);
-          c.next(a.stages);
-          ++issued;
-        }
-      }
+      auto up_stage = [&](const Part& pt, int fb, int k) {
+        if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) return false;
+        uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
+        uint64_t* bar = &tb.full[c.stage];
+        const int col = fb * S::kCols, row = k * kBoxRows, e = pt.expert;
+        tma_load_3d_hint(dst, &m1, bar, col, row, e, policy);
+        tma_load_3d_hint(dst + kBoxBytes, &m1, bar, col + S::kBoxCols, row, e, policy);
+        tma_load_3d_hint(dst + 2 * kBoxBytes, &m2, bar, col, row, e, policy);
+        tma_load_3d_hint(dst + 3 * kBoxBytes, &m2, bar, col + S::kBoxCols, row, e, policy);
+        c.next(ring.stages);
+        ++issued;
+        return true;
+      };
+      auto down_stage = [&](const Part& pt, int cb, int k) {
+        if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) return false;
+        uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
+        uint64_t* bar = &tb.full[c.stage];
+        const int col = cb * S::kCols, row = 2 * k * kBoxRows, e = pt.expert;
+        tma_load_3d_hint(dst, &m3, bar, col, row, e, policy);
+        tma_load_3d_hint(dst + kBoxBytes, &m3, bar, col + S::kBoxCols, row, e, policy);
+        tma_load_3d_hint(dst + 2 * kBoxBytes, &m3, bar, col, row + kBoxRows, e, policy);
+        tma_load_3d_hint(dst + 3 * kBoxBytes, &m3, bar, col + S::kBoxCols, row + kBoxRows, e,
+                         policy);
+        c.next(ring.stages);
+        ++issued;
+        return true;
+      };
+      walk(up_stage, [] {}, down_stage);
       if (!good) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
-      drain(ring, c, issued, a.timeout_ns);
+      drain(tb.full, ring.stages, c, issued, a.timeout_ns);
     }
+    __syncwarp();
+  } else if (warp == kConsumerWarps + 1) {
+    // Row producer: the lanes copy one row (X) or one tile (H) each. H waits for the barrier.
+    Cursor c;
+    bool good = true;
+    long long issued = 0;
+    // All lanes: the stage is free and its bytes are announced.
+    auto acquire = [&](uint32_t bytes) {
+      good = mbar_wait(&tb.empty[c.stage], c.phase ^ 1u, a.timeout_ns);
+      good = __all_sync(0xFFFFFFFFu, good);
+      if (good && lane == 0) mbar_arrive_expect_tx(&tb.rows_full[c.stage], bytes);
+      __syncwarp();
+      return good;
+    };
+    auto up_rows = [&](const Part& pt, int, int k) {
+      constexpr int kEl = WK == kF32 ? 4 : 2;
+      const int d = k * kBoxRows;
+      const uint32_t bytes = static_cast<uint32_t>(min(kBoxRows, a.D - d) * kEl);
+      if (!acquire(bytes * static_cast<uint32_t>(pt.n))) return false;
+      uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
+      if (lane < pt.n)
+        bulk_g2s(dst + lane * (WK == kF32 ? kRowPitchF32 : kRowPitch),
+                 static_cast<const uint8_t*>(a.X) +
+                     (static_cast<int64_t>(tb.row_tok[pt.row0 + lane]) * a.D + d) * kEl,
+                 bytes, &tb.rows_full[c.stage]);
+      c.next(ring.stages);
+      ++issued;
+      return true;
+    };
+    auto h_ready = [&] {
+      named_bar_sync(kBarRows, kConsumers + 32);
+      fence_proxy_async_all();
+    };
+    auto down_rows = [&](const Part& pt, int, int k) {
+      uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
+      if constexpr (WK == kF32) {
+        const int f = k * 2 * kBoxRows;
+        const uint32_t bytes = static_cast<uint32_t>(min(2 * kBoxRows, a.F - f) * 4);
+        if (!acquire(bytes * static_cast<uint32_t>(pt.n))) return false;
+        if (lane < pt.n)
+          bulk_g2s(dst + lane * 2 * kBoxRows * 4,
+                   static_cast<const float*>(a.H) + (pt.row0 + lane) * h_row_f32(a.F) + f, bytes,
+                   &tb.rows_full[c.stage]);
+      } else {
+        const int tiles = (pt.n + 7) / 8;
+        if (!acquire(static_cast<uint32_t>(tiles) * kTileBytes)) return false;
+        if (lane < tiles)
+          bulk_g2s(dst + lane * kTileBytes,
+                   static_cast<const uint8_t*>(a.H) +
+                       ((pt.tile + lane) * h_groups(a.F) + k * 4) * kHGroupBytes,
+                   kTileBytes, &tb.rows_full[c.stage]);
+      }
+      c.next(ring.stages);
+      ++issued;
+      return true;
+    };
+    bool waited = false;
+    walk(up_rows, [&] { h_ready(); waited = true; }, down_rows);
+    if (!waited) h_ready();  // the consumers arrive there in any case
+    if (!good && lane == 0) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+    drain(tb.rows_full, ring.stages, c, issued, a.timeout_ns);
     __syncwarp();
   } else {
     if (me == 0) export_routing(a, tb, outacc, tid);
@@ -788,7 +799,9 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
 #undef MOE_UP
       s += k1 - k0;
     }
+    fence_proxy_async_all();  // H is read by bulk copies
     if (!grid_barrier(a.bar, 2 * G, tid, &tb.flag, a.timeout_ns, a.err)) c.ok = false;
+    named_bar_arrive(kBarRows, kConsumers + 32);
 
     for (long long s = d0; s < d1;) {
       const long long tile = s / down_steps;
@@ -856,7 +869,7 @@ int64_t part_floats_of(int kind, int64_t N) {
 }
 
 template <int WK>
-cudaError_t launch(const moe_problem& p, FewArgs& a, const void* W1, const void* W2,
+cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const void* W2,
                    const void* W3, cudaStream_t stream) {
   CUtensorMap m1, m2, m3;
   if (!make_stream_map(&m1, W1, WK, p.F, p.D, p.E) || !make_stream_map(&m2, W2, WK, p.F, p.D, p.E) ||
@@ -865,11 +878,10 @@ cudaError_t launch(const moe_problem& p, FewArgs& a, const void* W1, const void*
   cudaError_t e = cudaFuncSetAttribute(
       few_kernel<WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return e;
-  a.stages = stages_for<WK>(a.N, a.E);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min(num_sms(), kMaxGrid)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<WK>(a.N, a.E, a.stages);
+  cfg.dynamicSmemBytes = kMaxSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;

@@ -1,15 +1,20 @@
 // Weight streaming for products with few rows: a persistent block per SM reads its share of a
 // matrix through a ring of shared-memory stages filled by TMA, and multiplies it by the few
-// activation rows, which come from L2 straight into registers. What bounds such a product is
+// activation rows. What bounds such a product is
 // the one pass over the weights, so
 //   - the work is cut into equal runs of stages, one per block, whatever the tile count
 //     (SplitK): a tile whose reduction is shared by several blocks is summed by the last of
 //     them to finish, in block order, so the result does not depend on timing;
 //   - a stage's rows are 256 contiguous bytes (two 128-byte boxes side by side): with 128 bytes
 //     the same loop without arithmetic read 5.5 TB/s, with 256 bytes 6.4 TB/s (2.6 GB of weights);
-//   - the loads run ahead of the arithmetic by the whole ring (128 KB or more per SM, above the
-//     44 KB per SM that 6.5 TB/s times a microsecond of latency needs), also across grid
-//     barriers: weights do not depend on what the barrier waits for.
+//   - the loads run ahead of the arithmetic by the whole ring, also across grid barriers
+//     (weights do not depend on what the barrier waits for), but at most kInFlight stages are
+//     under way at once: 96 KB per SM cover the latency, and more only queue in the memory
+//     system, where the activation rows then queue behind them (Mixtral-shaped layer, 8 tokens,
+//     with rows loaded by the consumers: 192 KB in flight 506 us, 128 KB 455, 96 KB 423, 64 KB
+//     463);
+//   - the activation rows of a stage come through the same ring, fetched once per block by a
+//     second producer warp, so that the consumers never wait for an L2 access.
 // 16-bit weights [k][n] (n contiguous) become the row operand of mma.m16n8k16 through transposed
 // ldmatrix (16 output columns x 16 k per instruction), the activation rows its 8 columns: one
 // instruction per 512 bytes of weights and 8 rows, far from the tensor cores' limit, where the
@@ -32,15 +37,21 @@ enum WeightKind { kBF16 = 0, kF32 = 1, kW8 = 2 };
 
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kThreads = kConsumers + 32;  // + the producer warp
+constexpr int kThreads = kConsumers + 64;  // + the weight and the row producer warp
 constexpr int kBoxRows = 64;               // one TMA box: 64 k-rows of 128 bytes, swizzled
 constexpr int kBoxBytes = kBoxRows * 128;
 constexpr int kStageBytes = 4 * kBoxBytes;
 constexpr int kMaxStages = 6;
+constexpr int kInFlight = 3;               // stages of weights under way at once
+// Activation rows of a stage, per tile of 8 rows. One matrix pair: 64 k-values of the rows
+// themselves, rows kRowPitch bytes apart (no bank conflicts). One matrix: 128 k-values, 16-bit
+// ones in operand order (two planes of four 512-byte groups), fp32 plain.
+constexpr int kTileBytes = 4096;
+constexpr int kRowPitch = 144, kRowPitchF32 = 256;
 constexpr int kMaxRows = 64;     // activation rows of one call
 constexpr int kTileRows = 32;    // activation rows of one product (up to four tiles of 8)
 constexpr int kMaxGrid = 148;    // blocks (one per SM)
-constexpr int kBarConsumers = 1, kBarAll = 2;  // named barriers
+constexpr int kBarConsumers = 1, kBarAll = 2, kBarRows = 3;  // named barriers
 
 // A stage is four boxes: two side by side (kCols output columns) times either two matrices with
 // the same 64 k-rows, or 128 k-rows of one matrix. Warp w takes box w/2; for 16- and 32-bit
@@ -80,10 +91,12 @@ struct SplitK {
 };
 
 struct Ring {
-  uint32_t base;  // shared address of stage 0 (1024-byte aligned)
-  uint64_t* full;
+  uint8_t* weights;  // stage 0 (1024-byte aligned), kStageBytes each
+  uint8_t* rows;     // stage 0, row_bytes each
+  uint64_t* full;    // weights have landed
+  uint64_t* rows_full;
   uint64_t* empty;
-  int stages;
+  int stages, row_bytes;
 };
 
 struct Cursor {
@@ -106,8 +119,7 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
 
 __device__ __forceinline__ void mma_bf16(float* c, const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -137,23 +149,54 @@ struct Acc {
   }
 };
 
-// One thread's activation values of one stage: for each 32-row group and row tile the four
-// blocks' pairs; with SPLIT each value is the sum of two bf16 terms (planes 0 and 1).
+// One thread's activation values of one stage: for each 32-row group and row tile the pairs of
+// the four blocks; with SPLIT each value is the sum of two bf16 terms (planes 0 and 1).
 template <int WK, int NT, bool SPLIT>
 struct Frag {
   uint32_t r[Shape<WK>::kGroups][NT][SPLIT ? 2 : 1][4];
-};
 
-// The 16 bytes of thread t (pairs w = 0..3) in block order: out[b] = pair (b + t) & 3.
-__device__ __forceinline__ void to_blocks(const uint4& v, int t, uint32_t (&out)[4]) {
-  const bool one = (t & 1) != 0, two = (t & 2) != 0;
-  const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
-                 a3 = one ? v.x : v.w;
-  out[0] = two ? a2 : a0;
-  out[1] = two ? a3 : a1;
-  out[2] = two ? a0 : a2;
-  out[3] = two ? a1 : a3;
-}
+  // From operand order: `rows` of the stage, its first group (0..3) for this warp.
+  __device__ __forceinline__ void load_ordered(const uint8_t* rows, int group, int lane) {
+    static_assert(SPLIT, "two planes");
+#pragma unroll
+    for (int g = 0; g < Shape<WK>::kGroups; ++g)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint4 v = *reinterpret_cast<const uint4*>(rows + j * kTileBytes +
+                                                          (group + g) * 1024 + q * 512 + lane * 16);
+          r[g][j][q][0] = v.x;
+          r[g][j][q][1] = v.y;
+          r[g][j][q][2] = v.z;
+          r[g][j][q][3] = v.w;
+        }
+  }
+
+  // From plain rows: thread t of quad `lane / 4` reads the 16 bytes of its four pairs, block b
+  // takes pair (b + t) & 3. k0: the warp's first k of the stage within the reduction of K (past
+  // its end nothing was copied: zeros); `group`: the warp's first 32-value group in the rows.
+  __device__ __forceinline__ void load_rows(const uint8_t* rows, int row_pitch, int group, int k0,
+                                            int K, int lane) {
+    static_assert(!SPLIT, "one plane");
+    const int t = lane & 3;
+    const bool one = (t & 1) != 0, two = (t & 2) != 0;
+#pragma unroll
+    for (int g = 0; g < Shape<WK>::kGroups; ++g)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint4 v = *reinterpret_cast<const uint4*>(rows + (8 * j + (lane >> 2)) * row_pitch +
+                                                  (group + g) * 64 + t * 16);
+        if (k0 + 32 * g + 8 * t >= K) v = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
+                       a3 = one ? v.x : v.w;
+        r[g][j][0][0] = two ? a2 : a0;
+        r[g][j][0][1] = two ? a3 : a1;
+        r[g][j][0][2] = two ? a0 : a2;
+        r[g][j][0][3] = two ? a1 : a3;
+      }
+  }
+};
 
 // Row of a 32-row group that lane l of a transposed load addresses for block b.
 __device__ __forceinline__ uint32_t block_row(int b, int i) {
@@ -161,67 +204,88 @@ __device__ __forceinline__ uint32_t block_row(int b, int i) {
   return static_cast<uint32_t>(8 * t + 2 * ((b + t) & 3) + (i & 1));
 }
 
-// acc += (this warp's part of its box)^T x rows. `box`: shared address of the box.
-template <int WK, int NT, bool SPLIT>
-__device__ __forceinline__ void multiply(Acc<WK, NT>& acc, uint32_t box, int warp, int lane,
-                                         const Frag<WK, NT, SPLIT>& f) {
-  const int b = lane >> 3, i = lane & 7;
-  if constexpr (WK == kBF16) {
-    // Matrices of one load: (column halves lo, hi) x (blocks 2s, 2s + 1).
+// This warp's weights of one stage, as the transposed loads deliver them: registers, so that the
+// stage can be handed back before the arithmetic.
+template <int WK>
+struct Weights {
+  uint32_t r[8][4];
+  // `box`: shared address of the warp's box.
+  __device__ __forceinline__ void load(uint32_t box, int warp, int lane) {
+    const int b = lane >> 3, i = lane & 7;
+    if constexpr (WK == kBF16) {
+      // Matrices of one load: (column halves lo, hi) x (blocks 2s, 2s + 1).
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const uint32_t r = block_row(2 * s + (b >> 1), i);
-      const uint32_t row = box + (static_cast<uint32_t>(warp & 1) * 32 + r) * 128;
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t k = block_row(2 * s + (b >> 1), i);
+        const uint32_t row = box + (static_cast<uint32_t>(warp & 1) * 32 + k) * 128;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        uint32_t a[4];
-        ldsm_x4_trans(row + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (r & 7u)) << 4), a);
+        for (int m = 0; m < 4; ++m)
+          ldsm_x4_trans(row + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (k & 7u)) << 4),
+                        r[s * 4 + m]);
+      }
+    } else {
+      // One load takes 16 columns (bytes) of all four blocks of a 32-row group.
+      const uint32_t k = block_row(b, i);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t row = box + (static_cast<uint32_t>(g) * 32 + k) * 128;
 #pragma unroll
-          for (int q = 0; q < (SPLIT ? 2 : 1); ++q)
-            mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[0][j][q][2 * s], f.r[0][j][q][2 * s + 1]);
-        }
+        for (int m = 0; m < 4; ++m)
+          ldsm_x4_trans(row + ((static_cast<uint32_t>((warp & 1) * 4 + m) ^ (k & 7u)) << 4),
+                        r[g * 4 + m]);
       }
     }
+  }
+};
+
+// acc += weights^T x rows.
+template <int WK, int NT, bool SPLIT>
+__device__ __forceinline__ void multiply(Acc<WK, NT>& acc, const Weights<WK>& w,
+                                         const Frag<WK, NT, SPLIT>& f) {
+  constexpr int kPlanes = SPLIT ? 2 : 1;
+  if constexpr (WK == kBF16) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int q = 0; q < kPlanes; ++q)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            mma_bf16(&acc.v[(m * NT + j) * 4], w.r[s * 4 + m], f.r[0][j][q][2 * s],
+                     f.r[0][j][q][2 * s + 1]);
   } else {
-    // One load takes 16 columns (bytes) of all four blocks: as 16-bit elements, a transposed
-    // 8x8 matrix gives each thread the bytes of columns 2g and 2g+1 at its pair of k; the even
-    // columns take the instruction's rows 0-7 and the odd ones rows 8-15.
-    const uint32_t r = block_row(b, i);
+    // As 16-bit elements, a transposed 8x8 matrix gives each thread the bytes of columns 2g and
+    // 2g+1 at its pair of k; the even columns take the instruction's rows 0-7 and the odd ones
+    // rows 8-15.
 #pragma unroll
-    for (int g = 0; g < Shape<WK>::kGroups; ++g) {
-      const uint32_t row = box + (static_cast<uint32_t>(g) * 32 + r) * 128;
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        uint32_t p[4];
-        ldsm_x4_trans(row + ((static_cast<uint32_t>((warp & 1) * 4 + m) ^ (r & 7u)) << 4), p);
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int m = 0; m < 4; ++m) {
           uint32_t a[4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t v = p[2 * s + h];
+            const uint32_t v = w.r[g * 4 + m][2 * s + h];
             a[2 * h] = i8x2_to_bf16x2(v & 0x00FF00FFu);
             a[2 * h + 1] = i8x2_to_bf16x2((v >> 8) & 0x00FF00FFu);
           }
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
+          for (int q = 0; q < kPlanes; ++q)
 #pragma unroll
-            for (int q = 0; q < (SPLIT ? 2 : 1); ++q)
+            for (int j = 0; j < NT; ++j)
               mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[g][j][q][2 * s], f.r[g][j][q][2 * s + 1]);
-          }
         }
-      }
-    }
   }
 }
 
 // fp32 weights on the CUDA cores: acc.v[r] += sum over the warp's 32 k-rows of W[k][lane] x_r[k].
-// row(r): row r's values (global memory), k0: its first k here, K: the reduction length.
-template <int NT, typename RowPtr>
+// `rows`: the stage's rows at this warp's first k, pitch bytes apart; k0: that k within K.
+template <int NT>
 __device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, int warp, int lane,
-                                             int n_rows, int k0, int K, RowPtr row) {
+                                             const uint8_t* rows, int pitch, int n_rows, int k0,
+                                             int K) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float w[16];
@@ -235,7 +299,7 @@ __device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, i
 #pragma unroll
     for (int r = 0; r < 8 * NT; ++r) {
       if (r < n_rows) {
-        const float* x = row(r) + k0 + h * 16;
+        const float* x = reinterpret_cast<const float*>(rows + r * pitch) + h * 16;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (k0 + h * 16 + 4 * q < K) {
@@ -356,28 +420,47 @@ __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid,
   return last;
 }
 
-// Producer side of one stage: wait for it to be free, then announce its bytes.
-__device__ __forceinline__ bool acquire_stage(const Ring& ring, const Cursor& c,
-                                              uint64_t timeout_ns) {
+// Weight producer, before it fills the stage at `c` (the issued-th overall): the stage is free
+// and at most kInFlight - 1 earlier ones are still under way; then announce its bytes.
+__device__ __forceinline__ bool acquire_weights(const Ring& ring, const Cursor& c,
+                                                long long issued, uint64_t timeout_ns) {
   if (!mbar_wait(&ring.empty[c.stage], c.phase ^ 1u, timeout_ns)) return false;
+  if (issued >= kInFlight && ring.stages >= kInFlight) {
+    int s = c.stage - kInFlight;
+    uint32_t phase = c.phase;
+    if (s < 0) {
+      s += ring.stages;
+      phase ^= 1u;
+    }
+    if (!mbar_wait(&ring.full[s], phase, timeout_ns)) return false;
+  }
   mbar_arrive_expect_tx(&ring.full[c.stage], kStageBytes);
   return true;
 }
 
-// Before the block ends: every copy issued into the ring has landed (bounded).
-__device__ __forceinline__ void drain(const Ring& ring, const Cursor& end, long long issued,
-                                      uint64_t timeout_ns) {
+// Before the block ends: every copy counted on `full` has landed (bounded).
+__device__ __forceinline__ void drain(uint64_t* full, int stages, const Cursor& end,
+                                      long long issued, uint64_t timeout_ns) {
   Cursor c = end;
-  const long long n = issued < ring.stages ? issued : ring.stages;
+  const long long n = issued < stages ? issued : stages;
   for (long long i = 0; i < n; ++i) {
     if (c.stage == 0) {
-      c.stage = ring.stages - 1;
+      c.stage = stages - 1;
       c.phase ^= 1u;
     } else {
       --c.stage;
     }
-    if (!mbar_wait(&ring.full[c.stage], c.phase, timeout_ns)) return;
+    if (!mbar_wait(&full[c.stage], c.phase, timeout_ns)) return;
   }
+}
+
+// Generic-proxy writes of global memory before bulk copies of it, and the other way round.
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 }  // namespace stream
