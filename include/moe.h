@@ -357,6 +357,47 @@ moe_status moe_forward_few_w8(const moe_problem* p, const void* X, const float* 
                               uint8_t* dropped, float* prob_colsum, void* ws, size_t ws_bytes,
                               void* stream);
 
+/* ---- A projection shared by every row beside the low-rank adapters of many requests, for the
+ * dense projections around the layer (a shared expert's, an attention block's) when each
+ * request brings its own adapter:
+ *   Y[m] = addend[m] + X[m] W + scale[a] (X[m] A[a]) B[a],   a = adapter[m]
+ *   M        rows, >= 0;  K, N  the projection's widths
+ *   adapters number L of resident adapters, >= 1
+ *   rank     r, the adapters' common rank (smaller ones padded with zeros), 1..128
+ *   dtype    MOE_DTYPE_* of X, W, A, B, addend and Y
+ * Layouts: X [M,K]; W [K,N]; A [L,K,r]; B [L,r,N]; adapter [M] int32; scale [L] fp32; addend,
+ * Y [M,N]. bf16 needs K, N and r multiples of 8, fp32 multiples of 4 (else
+ * MOE_ERR_UNSUPPORTED). */
+typedef struct {
+  int64_t M;
+  int64_t K;
+  int64_t N;
+  int32_t adapters;
+  int32_t rank;
+  int32_t dtype;
+  int32_t reserved; /* must be 0 */
+} moe_lora_problem;
+
+/* Host only. Workspace bytes of moe_lora_forward (initialise its header once with
+ * moe_workspace_init, as every workspace). It grows with M: a workspace serves any problem
+ * whose size is at most its own. */
+moe_status moe_lora_workspace_size(const moe_lora_problem* p, size_t* bytes);
+
+/* adapter[m] = -1: the row takes no adapter (A and B are not read for it). A value outside
+ * [-1, L) is recorded as MOE_DEVERR_BAD_INDEX and treated as -1. scale may be NULL (1 for
+ * every adapter). addend may be NULL; it may be Y itself (Y += ...), otherwise Y must not
+ * overlap any input. Rows may come in any order; adjacent rows of one adapter share its reads.
+ *   At most 64 rows: one cooperative kernel that streams W once; X A, the adapters' part and
+ *   all sums in fp32, one rounding to the output type (one block per SM, as moe_forward_few).
+ *   More rows, bf16: X A in fp32, rounded to bf16 with its scale, and one tcgen05 product over
+ *   [X, X A] with fp32 accumulation. Its cost grows with the number of different adapters
+ *   among each 256 adjacent rows. More rows, fp32: CUDA cores.
+ * Deterministic. Pointers: device memory, 16-byte aligned (adapter, scale: 4-byte). */
+moe_status moe_lora_forward(const moe_lora_problem* p, const void* X, const void* W,
+                            const void* A, const void* B, const int32_t* adapter,
+                            const float* scale, const void* addend, void* Y, void* ws,
+                            size_t ws_bytes, void* stream);
+
 /* moe_forward with HOST activations: X_host [N,D] and out_host [N,D] are host pointers
  * (page-locked memory gives asynchronous copies), the weights and W_r/bias are device
  * pointers. Enqueues the host->device copy of X, the forward, and the device->host copy

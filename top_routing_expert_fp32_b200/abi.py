@@ -31,6 +31,7 @@ EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_workspace_size_host", "moe
            "moe_pack_w8", "moe_expert_up_w8p", "moe_expert_down_w8p", "moe_forward_w8p",
            "moe_gather_rows", "moe_forward_host_many", "moe_selftest_wait_timeout",
            "moe_balance_loss", "moe_drop_rate", "moe_forward_few", "moe_forward_few_w8",
+           "moe_lora_workspace_size", "moe_lora_forward",
            "moe_workspace_init", "moe_get_device_error", "moe_status_string", "moe_last_error",
            "moe_version")
 
@@ -42,6 +43,12 @@ class moe_problem(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("capacity_order", ctypes.c_int32), ("drop_policy", ctypes.c_int32),
                 ("routing_mode", ctypes.c_int32), ("min_capacity", ctypes.c_int64),
+                ("reserved", ctypes.c_int32)]
+
+
+class moe_lora_problem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
 
 
@@ -87,6 +94,8 @@ def _load() -> ctypes.CDLL:
         "moe_forward_w8p": [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
         "moe_forward_few": [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
         "moe_forward_few_w8": [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
+        "moe_lora_workspace_size": [ctypes.POINTER(moe_lora_problem), ctypes.POINTER(S)],
+        "moe_lora_forward": [ctypes.POINTER(moe_lora_problem), P, P, P, P, P, P, P, P, P, S, P],
         "moe_workspace_init": [P, S, P],
         "moe_get_device_error": [P, P, ctypes.POINTER(ctypes.c_int32)],
     }
@@ -304,6 +313,26 @@ def forward_host_many(p, X_host: torch.Tensor, W_r, bias, W1, W2, W3, out_host: 
     _check(lib.moe_forward_host_many(ctypes.byref(p), nb, _ptr(X_host), _ptr(W_r), _ptr(bias),
                                      _ptr(W1), _ptr(W2), _ptr(W3), _ptr(out_host), _ptr(ws),
                                      ws.numel(), _stream(stream)))
+
+
+def lora_problem(M: int, K: int, N: int, adapters: int, rank: int, dtype: int) -> moe_lora_problem:
+    return moe_lora_problem(M=M, K=K, N=N, adapters=adapters, rank=rank, dtype=dtype, reserved=0)
+
+
+def lora_workspace(p: moe_lora_problem, device="cuda") -> torch.Tensor:
+    """A device workspace for lora_forward with its header zeroed."""
+    b = ctypes.c_size_t()
+    _check(lib.moe_lora_workspace_size(ctypes.byref(p), ctypes.byref(b)))
+    ws = torch.empty(b.value, dtype=torch.uint8, device=device)
+    _check(lib.moe_workspace_init(ws.data_ptr(), ws.numel(), _stream(None)))
+    return ws
+
+
+def lora_forward(p, X, W, A, B, adapter, Y, ws, *, scale=None, addend=None, stream=None):
+    """Y[m] = addend[m] + X[m] W + scale[a] (X[m] A[a]) B[a], a = adapter[m] (-1: none)."""
+    _check(lib.moe_lora_forward(ctypes.byref(p), _ptr(X), _ptr(W), _ptr(A), _ptr(B),
+                                _ptr(adapter), _ptr(scale), _ptr(addend), _ptr(Y), _ptr(ws),
+                                ws.numel(), _stream(stream)))
 
 
 def balance_loss(p, load, prob_colsum) -> float:

@@ -86,7 +86,7 @@ int* sched_of(int* header) { return header + kSchedInt; }
 constexpr int kDispatchBarInt = 20;
 int* dispatch_bar_of(int* header) { return header + kDispatchBarInt; }
 
-// Ints 24 and 25: moe_forward_few's grid-barrier arrivals and finished count (zero at rest).
+// Ints 24 and 25: moe_forward_few's and moe_lora_forward's grid-barrier arrivals and finished count (zero at rest).
 constexpr int kFewBarInt = 24;
 int* few_bar_of(int* header) { return header + kFewBarInt; }
 
@@ -398,6 +398,34 @@ moe_status forward_impl(const moe_problem& p, const void* X, const float* W_r, c
   NvtxRange range("moe combine");
   MOE_CUDA(launch_combine(p, y, idx, gate, off, ps, dr, out, err, stream), "combine");
   return MOE_OK;
+}
+
+moe_status check_lora(const moe_lora_problem* p) {
+  if (p == nullptr) return fail(MOE_ERR_INVALID_ARG, "problem is NULL");
+  if (p->reserved != 0) return fail(MOE_ERR_INVALID_ARG, "reserved field must be 0");
+  if (p->M < 0) return fail(MOE_ERR_INVALID_ARG, "M < 0");
+  if (p->K < 1 || p->N < 1) return fail(MOE_ERR_INVALID_ARG, "K and N must be >= 1");
+  if (p->adapters < 1) return fail(MOE_ERR_INVALID_ARG, "adapters < 1");
+  if (p->rank < 1) return fail(MOE_ERR_INVALID_ARG, "rank < 1");
+  if (p->dtype != MOE_DTYPE_F32 && p->dtype != MOE_DTYPE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
+  if (p->rank > 128) return fail(MOE_ERR_UNSUPPORTED, "rank > 128");
+  if (p->M > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "M > 2^30");
+  if (p->K > (1 << 24) || p->N > (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "K or N > 2^24");
+  const int vec = p->dtype == MOE_DTYPE_BF16 ? 8 : 4;
+  if (p->K % vec != 0 || p->N % vec != 0 || p->rank % vec != 0)
+    return fail(MOE_ERR_UNSUPPORTED, p->dtype == MOE_DTYPE_BF16
+                                         ? "bf16 needs K, N and rank multiples of 8"
+                                         : "fp32 needs K, N and rank multiples of 4");
+  return MOE_OK;
+}
+
+// Header, then the scratch of the path that M takes.
+size_t lora_bytes(const moe_lora_problem& p) {
+  if (p.M == 0) return 256;
+  return 256 + align256(p.M <= kLoraFewRows         ? lora_few_workspace_bytes(p)
+                        : p.dtype == MOE_DTYPE_BF16 ? lora_sm100_workspace_bytes(p)
+                                                    : lora_f32_workspace_bytes(p));
 }
 
 moe_status few_impl(const moe_problem& p, const FewTensors& t, void* ws, cudaStream_t stream) {
@@ -720,6 +748,48 @@ moe_status moe_forward_few_w8(const moe_problem* p, const void* X, const float* 
   const FewTensors t{X,   W_r,    bias,     W1q,       W2q,  W3q,     S1,  S2,      S3,
                      out, logits, topk_idx, topk_gate, load, offsets, pos, dropped, prob_colsum};
   return few_impl(*p, t, ws, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_lora_workspace_size(const moe_lora_problem* p, size_t* bytes) {
+  MOE_TRY(check_lora(p));
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = lora_bytes(*p);
+  return MOE_OK;
+}
+
+moe_status moe_lora_forward(const moe_lora_problem* p, const void* X, const void* W,
+                            const void* A, const void* B, const int32_t* adapter,
+                            const float* scale, const void* addend, void* Y, void* ws,
+                            size_t ws_bytes, void* stream) {
+  MOE_TRY(check_lora(p));
+  MOE_TRY(need(ws, "ws", 256));
+  if (ws_bytes < lora_bytes(*p))
+    return fail(MOE_ERR_INVALID_ARG, "workspace too small: " + std::to_string(ws_bytes) + " < " +
+                                         std::to_string(lora_bytes(*p)));
+  if (p->M == 0) return MOE_OK;
+  MOE_TRY(need(X, "X"));
+  MOE_TRY(need(W, "W"));
+  MOE_TRY(need(A, "A"));
+  MOE_TRY(need(B, "B"));
+  MOE_TRY(need(adapter, "adapter", 4));
+  MOE_TRY(opt(scale, "scale", 4));
+  MOE_TRY(opt(addend, "addend"));
+  MOE_TRY(need(Y, "Y"));
+  MOE_TRY(check_sm100());
+  const LoraTensors t{X, W, A, B, adapter, scale, addend, Y};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = at<int>(ws, 0);
+  void* scratch = at<void>(ws, 256);
+  NvtxRange range("moe lora projection");
+  if (p->M <= kLoraFewRows)
+    MOE_CUDA(launch_lora_few(*p, t, scratch, err, few_bar_of(err), wait_timeout_ns(), s),
+             "projection with adapters (few rows)");
+  else if (p->dtype == MOE_DTYPE_BF16)
+    MOE_CUDA(launch_lora_sm100(*p, t, scratch, err, wait_timeout_ns(), s),
+             "projection with adapters (tcgen05)");
+  else
+    MOE_CUDA(launch_lora_f32(*p, t, scratch, err, s), "projection with adapters (fp32)");
+  return MOE_OK;
 }
 
 // Non-blocking streams per device for the host copies of moe_forward_host[_many] (created on

@@ -679,108 +679,112 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
     }
   };
 
-  if (warp == kConsumerWarps) {
-    // Weight producer: one thread issues this block's stages of both products in order.
-    if (lane == 0) {
-      // Weights are read once; evict_first read 6.4 TB/s where the default read 6.0.
-      const uint64_t policy = l2_policy(-1);
+  if (warp >= kConsumerWarps) {
+    give_registers<kProducerRegs>();
+    if (warp == kWeightWarp) {
+      // Weight producer: one thread issues this block's stages of both products in order.
+      if (lane == 0) {
+        // Weights are read once; evict_first read 6.4 TB/s where the default read 6.0.
+        const uint64_t policy = l2_policy(-1);
+        Cursor c;
+        bool good = true;
+        long long issued = 0;
+        auto up_stage = [&](const Part& pt, int fb, int k) {
+          if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) return false;
+          uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
+          uint64_t* bar = &tb.full[c.stage];
+          const int col = fb * S::kCols, row = k * kBoxRows, e = pt.expert;
+          tma_load_3d_hint(dst, &m1, bar, col, row, e, policy);
+          tma_load_3d_hint(dst + kBoxBytes, &m1, bar, col + S::kBoxCols, row, e, policy);
+          tma_load_3d_hint(dst + 2 * kBoxBytes, &m2, bar, col, row, e, policy);
+          tma_load_3d_hint(dst + 3 * kBoxBytes, &m2, bar, col + S::kBoxCols, row, e, policy);
+          c.next(ring.stages);
+          ++issued;
+          return true;
+        };
+        auto down_stage = [&](const Part& pt, int cb, int k) {
+          if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) return false;
+          uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
+          uint64_t* bar = &tb.full[c.stage];
+          const int col = cb * S::kCols, row = 2 * k * kBoxRows, e = pt.expert;
+          tma_load_3d_hint(dst, &m3, bar, col, row, e, policy);
+          tma_load_3d_hint(dst + kBoxBytes, &m3, bar, col + S::kBoxCols, row, e, policy);
+          tma_load_3d_hint(dst + 2 * kBoxBytes, &m3, bar, col, row + kBoxRows, e, policy);
+          tma_load_3d_hint(dst + 3 * kBoxBytes, &m3, bar, col + S::kBoxCols, row + kBoxRows, e,
+                           policy);
+          c.next(ring.stages);
+          ++issued;
+          return true;
+        };
+        walk(up_stage, [] {}, down_stage);
+        if (!good) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+        drain(tb.full, ring.stages, c, issued, a.timeout_ns);
+      }
+      __syncwarp();
+    } else if (warp == kRowWarp) {
+      // Row producer: the lanes copy one row (X) or one tile (H) each. H waits for the barrier.
       Cursor c;
       bool good = true;
       long long issued = 0;
-      auto up_stage = [&](const Part& pt, int fb, int k) {
-        if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) return false;
-        uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
-        uint64_t* bar = &tb.full[c.stage];
-        const int col = fb * S::kCols, row = k * kBoxRows, e = pt.expert;
-        tma_load_3d_hint(dst, &m1, bar, col, row, e, policy);
-        tma_load_3d_hint(dst + kBoxBytes, &m1, bar, col + S::kBoxCols, row, e, policy);
-        tma_load_3d_hint(dst + 2 * kBoxBytes, &m2, bar, col, row, e, policy);
-        tma_load_3d_hint(dst + 3 * kBoxBytes, &m2, bar, col + S::kBoxCols, row, e, policy);
-        c.next(ring.stages);
-        ++issued;
-        return true;
+      // All lanes: the stage is free and its bytes are announced.
+      auto acquire = [&](uint32_t bytes) {
+        good = mbar_wait(&tb.empty[c.stage], c.phase ^ 1u, a.timeout_ns);
+        good = __all_sync(0xFFFFFFFFu, good);
+        if (good && lane == 0) mbar_arrive_expect_tx(&tb.rows_full[c.stage], bytes);
+        __syncwarp();
+        return good;
       };
-      auto down_stage = [&](const Part& pt, int cb, int k) {
-        if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) return false;
-        uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
-        uint64_t* bar = &tb.full[c.stage];
-        const int col = cb * S::kCols, row = 2 * k * kBoxRows, e = pt.expert;
-        tma_load_3d_hint(dst, &m3, bar, col, row, e, policy);
-        tma_load_3d_hint(dst + kBoxBytes, &m3, bar, col + S::kBoxCols, row, e, policy);
-        tma_load_3d_hint(dst + 2 * kBoxBytes, &m3, bar, col, row + kBoxRows, e, policy);
-        tma_load_3d_hint(dst + 3 * kBoxBytes, &m3, bar, col + S::kBoxCols, row + kBoxRows, e,
-                         policy);
-        c.next(ring.stages);
-        ++issued;
-        return true;
-      };
-      walk(up_stage, [] {}, down_stage);
-      if (!good) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
-      drain(tb.full, ring.stages, c, issued, a.timeout_ns);
-    }
-    __syncwarp();
-  } else if (warp == kConsumerWarps + 1) {
-    // Row producer: the lanes copy one row (X) or one tile (H) each. H waits for the barrier.
-    Cursor c;
-    bool good = true;
-    long long issued = 0;
-    // All lanes: the stage is free and its bytes are announced.
-    auto acquire = [&](uint32_t bytes) {
-      good = mbar_wait(&tb.empty[c.stage], c.phase ^ 1u, a.timeout_ns);
-      good = __all_sync(0xFFFFFFFFu, good);
-      if (good && lane == 0) mbar_arrive_expect_tx(&tb.rows_full[c.stage], bytes);
-      __syncwarp();
-      return good;
-    };
-    auto up_rows = [&](const Part& pt, int, int k) {
-      constexpr int kEl = WK == kF32 ? 4 : 2;
-      const int d = k * kBoxRows;
-      const uint32_t bytes = static_cast<uint32_t>(min(kBoxRows, a.D - d) * kEl);
-      if (!acquire(bytes * static_cast<uint32_t>(pt.n))) return false;
-      uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
-      if (lane < pt.n)
-        bulk_g2s(dst + lane * (WK == kF32 ? kRowPitchF32 : kRowPitch),
-                 static_cast<const uint8_t*>(a.X) +
-                     (static_cast<int64_t>(tb.row_tok[pt.row0 + lane]) * a.D + d) * kEl,
-                 bytes, &tb.rows_full[c.stage]);
-      c.next(ring.stages);
-      ++issued;
-      return true;
-    };
-    auto h_ready = [&] {
-      named_bar_sync(kBarRows, kConsumers + 32);
-      fence_proxy_async_all();
-    };
-    auto down_rows = [&](const Part& pt, int, int k) {
-      uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
-      if constexpr (WK == kF32) {
-        const int f = k * 2 * kBoxRows;
-        const uint32_t bytes = static_cast<uint32_t>(min(2 * kBoxRows, a.F - f) * 4);
+      auto up_rows = [&](const Part& pt, int, int k) {
+        constexpr int kEl = WK == kF32 ? 4 : 2;
+        const int d = k * kBoxRows;
+        const uint32_t bytes = static_cast<uint32_t>(min(kBoxRows, a.D - d) * kEl);
         if (!acquire(bytes * static_cast<uint32_t>(pt.n))) return false;
+        uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
         if (lane < pt.n)
-          bulk_g2s(dst + lane * 2 * kBoxRows * 4,
-                   static_cast<const float*>(a.H) + (pt.row0 + lane) * h_row_f32(a.F) + f, bytes,
-                   &tb.rows_full[c.stage]);
-      } else {
-        const int tiles = (pt.n + 7) / 8;
-        if (!acquire(static_cast<uint32_t>(tiles) * kTileBytes)) return false;
-        if (lane < tiles)
-          bulk_g2s(dst + lane * kTileBytes,
-                   static_cast<const uint8_t*>(a.H) +
-                       ((pt.tile + lane) * h_groups(a.F) + k * 4) * kHGroupBytes,
-                   kTileBytes, &tb.rows_full[c.stage]);
-      }
-      c.next(ring.stages);
-      ++issued;
-      return true;
-    };
-    bool waited = false;
-    walk(up_rows, [&] { h_ready(); waited = true; }, down_rows);
-    if (!waited) h_ready();  // the consumers arrive there in any case
-    if (!good && lane == 0) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
-    drain(tb.rows_full, ring.stages, c, issued, a.timeout_ns);
-    __syncwarp();
+          bulk_g2s(dst + lane * (WK == kF32 ? kRowPitchF32 : kRowPitch),
+                   static_cast<const uint8_t*>(a.X) +
+                       (static_cast<int64_t>(tb.row_tok[pt.row0 + lane]) * a.D + d) * kEl,
+                   bytes, &tb.rows_full[c.stage]);
+        c.next(ring.stages);
+        ++issued;
+        return true;
+      };
+      auto h_ready = [&] {
+        named_bar_sync(kBarRows, kConsumers + 32);
+        fence_proxy_async_all();
+      };
+      auto down_rows = [&](const Part& pt, int, int k) {
+        uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
+        if constexpr (WK == kF32) {
+          const int f = k * 2 * kBoxRows;
+          const uint32_t bytes = static_cast<uint32_t>(min(2 * kBoxRows, a.F - f) * 4);
+          if (!acquire(bytes * static_cast<uint32_t>(pt.n))) return false;
+          if (lane < pt.n)
+            bulk_g2s(dst + lane * 2 * kBoxRows * 4,
+                     static_cast<const float*>(a.H) + (pt.row0 + lane) * h_row_f32(a.F) + f, bytes,
+                     &tb.rows_full[c.stage]);
+        } else {
+          const int tiles = (pt.n + 7) / 8;
+          if (!acquire(static_cast<uint32_t>(tiles) * kTileBytes)) return false;
+          if (lane < tiles)
+            bulk_g2s(dst + lane * kTileBytes,
+                     static_cast<const uint8_t*>(a.H) +
+                         ((pt.tile + lane) * h_groups(a.F) + k * 4) * kHGroupBytes,
+                     kTileBytes, &tb.rows_full[c.stage]);
+        }
+        c.next(ring.stages);
+        ++issued;
+        return true;
+      };
+      bool waited = false;
+      walk(up_rows, [&] { h_ready(); waited = true; }, down_rows);
+      if (!waited) h_ready();  // the consumers arrive there in any case
+      if (!good && lane == 0) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+      drain(tb.rows_full, ring.stages, c, issued, a.timeout_ns);
+      __syncwarp();
+    }
   } else {
+    take_registers<kConsumerRegs>();
     if (me == 0) export_routing(a, tb, outacc, tid);
     if (parts == 0) {  // a capacity of zero keeps nothing: zeros
       for (int cb = me; cb < down_cols; cb += G)
@@ -927,6 +931,19 @@ bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, u
   return encode_fn()(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_box_map_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
+                          uint64_t count, uint32_t box_rows) {
+  if (encode_fn() == nullptr) return false;
+  const cuuint64_t dims[3] = {cols, rows, count};
+  const cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -68,6 +68,11 @@ bool make_tensor_map_3d_u8(CUtensorMap* m, const void* ptr, uint64_t n, uint64_t
 bool make_tensor_map_3d_u8_sw64(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows,
                                 uint64_t E, uint32_t box_inner, uint32_t box_rows);
 
+// 3-D bf16 tensor map over stacked [count][rows][cols] (cols contiguous), box 64 columns x
+// box_rows x 1, 128-byte swizzle, out-of-range elements read as zero (few.cu).
+bool make_box_map_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
+                          uint64_t count, uint32_t box_rows);
+
 // Repack 8-bit expert weights [E][k][n] (n contiguous) into [E][n][k] (k contiguous).
 cudaError_t launch_pack_w8(const int8_t* src, int8_t* dst, int64_t E, int64_t k, int64_t n,
                            cudaStream_t stream);
@@ -172,6 +177,32 @@ struct FewTensors {
 size_t few_workspace_bytes(const moe_problem& p);
 cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors& t, void* scratch,
                        int* err, int* bar, uint64_t timeout_ns, cudaStream_t stream);
+
+// A shared projection beside per-row low-rank adapters (moe_lora_forward).
+//   few:   at most kLoraFewRows rows, one cooperative launch (lora.cu); bar as launch_few.
+//   sm100: bf16, more rows: S = X A by row groups, then one tcgen05 product (lora_sm100.cu).
+//   f32:   fp32, more rows, CUDA cores (lora_f32.cu).
+// scratch: the matching *_workspace_bytes, 256-byte aligned.
+constexpr int64_t kLoraFewRows = 64;
+struct LoraTensors {
+  const void* X;
+  const void* W;
+  const void* A;
+  const void* B;
+  const int32_t* adapter;
+  const float* scale;
+  const void* addend;
+  void* Y;
+};
+size_t lora_few_workspace_bytes(const moe_lora_problem& p);
+size_t lora_sm100_workspace_bytes(const moe_lora_problem& p);
+size_t lora_f32_workspace_bytes(const moe_lora_problem& p);
+cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, void* scratch,
+                            int* err, int* bar, uint64_t timeout_ns, cudaStream_t stream);
+cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, void* scratch,
+                              int* err, uint64_t timeout_ns, cudaStream_t stream);
+cudaError_t launch_lora_f32(const moe_lora_problem& p, const LoraTensors& t, void* scratch,
+                            int* err, cudaStream_t stream);
 
 // Failure-detection self-test: one bounded wait on a barrier nothing completes; records
 // MOE_DEVERR_WAIT_TIMEOUT in *err after timeout_ns and returns.

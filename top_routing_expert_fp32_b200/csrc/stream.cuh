@@ -37,7 +37,12 @@ enum WeightKind { kBF16 = 0, kF32 = 1, kW8 = 2 };
 
 constexpr int kConsumerWarps = 8;
 constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kThreads = kConsumers + 64;  // + the weight and the row producer warp
+constexpr int kWeightWarp = kConsumerWarps, kRowWarp = kConsumerWarps + 1;
+constexpr int kThreads = kConsumers + 128;  // + the producers' warpgroup
+// Registers: 384 threads start with 168 each (64512 in all); the producers' warpgroup hands some
+// to the consumers': 256 x 216 + 128 x 72 = 64512.
+constexpr int kConsumerRegs = 216, kProducerRegs = 72;
+static_assert(kConsumers * kConsumerRegs + 128 * kProducerRegs <= 168 * kThreads, "registers");
 constexpr int kBoxRows = 64;               // one TMA box: 64 k-rows of 128 bytes, swizzled
 constexpr int kBoxBytes = kBoxRows * 128;
 constexpr int kStageBytes = 4 * kBoxBytes;
@@ -89,6 +94,15 @@ struct SplitK {
     return static_cast<int>(((s + 1) * grid - 1) / total);
   }
 };
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 struct Ring {
   uint8_t* weights;  // stage 0 (1024-byte aligned), kStageBytes each
@@ -300,16 +314,18 @@ __device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, i
     for (int r = 0; r < 8 * NT; ++r) {
       if (r < n_rows) {
         const float* x = reinterpret_cast<const float*>(rows + r * pitch) + h * 16;
+        float s = 0.0f;  // 16 terms on their own: short chains keep the rounding error low
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (k0 + h * 16 + 4 * q < K) {
             const float4 v = *reinterpret_cast<const float4*>(x + 4 * q);
-            acc.v[r] = fmaf(w[4 * q], v.x, acc.v[r]);
-            acc.v[r] = fmaf(w[4 * q + 1], v.y, acc.v[r]);
-            acc.v[r] = fmaf(w[4 * q + 2], v.z, acc.v[r]);
-            acc.v[r] = fmaf(w[4 * q + 3], v.w, acc.v[r]);
+            s = fmaf(w[4 * q], v.x, s);
+            s = fmaf(w[4 * q + 1], v.y, s);
+            s = fmaf(w[4 * q + 2], v.z, s);
+            s = fmaf(w[4 * q + 3], v.w, s);
           }
         }
+        acc.v[r] += s;
       }
     }
   }
@@ -377,14 +393,12 @@ __device__ __forceinline__ float2 take_pair(const float* red, int branch, int ro
   return s;
 }
 
-// All consumer threads of every block: arrive, wait until `target` arrivals (bounded). The
-// block's earlier global writes are visible to the others afterwards. False: the wait ran out.
-__device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int* flag,
-                                             uint64_t timeout_ns, int* err) {
+// All consumer threads of a block: wait until `target` blocks have arrived at *bar (bounded).
+// What they wrote before is visible afterwards. False: the wait ran out.
+__device__ __forceinline__ bool grid_wait(int* bar, int target, int tid, int* flag,
+                                          uint64_t timeout_ns, int* err) {
   named_bar_sync(kBarConsumers, kConsumers);
   if (tid == 0) {
-    __threadfence();
-    atomicAdd(bar, 1);
     int ok = 1;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
@@ -401,8 +415,22 @@ __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int*
     *flag = ok;
   }
   named_bar_sync(kBarConsumers, kConsumers);
-  const bool ok = *flag != 0;
-  return ok;
+  return *flag != 0;
+}
+
+// The block's writes so far, then its arrival (all consumer threads call it).
+__device__ __forceinline__ void grid_arrive(int* bar, int tid) {
+  named_bar_sync(kBarConsumers, kConsumers);
+  if (tid == 0) {
+    __threadfence();
+    atomicAdd(bar, 1);
+  }
+}
+
+__device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int* flag,
+                                             uint64_t timeout_ns, int* err) {
+  grid_arrive(bar, tid);
+  return grid_wait(bar, target, tid, flag, timeout_ns, err);
 }
 
 // One arrival per block that shares a tile; true in the block that arrives last (its threads
