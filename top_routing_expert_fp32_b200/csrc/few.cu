@@ -935,15 +935,18 @@ bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, u
 }
 
 bool make_box_map_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
-                          uint64_t count, uint32_t box_rows) {
+                          uint64_t count, uint32_t box_cols, uint32_t box_rows) {
   if (encode_fn() == nullptr) return false;
   const cuuint64_t dims[3] = {cols, rows, count};
   const cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     box_cols == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                     : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

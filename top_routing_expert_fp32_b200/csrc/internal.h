@@ -68,10 +68,11 @@ bool make_tensor_map_3d_u8(CUtensorMap* m, const void* ptr, uint64_t n, uint64_t
 bool make_tensor_map_3d_u8_sw64(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows,
                                 uint64_t E, uint32_t box_inner, uint32_t box_rows);
 
-// 3-D bf16 tensor map over stacked [count][rows][cols] (cols contiguous), box 64 columns x
-// box_rows x 1, 128-byte swizzle, out-of-range elements read as zero (few.cu).
+// 3-D bf16 tensor map over stacked [count][rows][cols] (cols contiguous), box box_cols (16, 32 or
+// 64, swizzled over those 32, 64 or 128 bytes) x box_rows x 1, out-of-range elements read as
+// zero (few.cu).
 bool make_box_map_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
-                          uint64_t count, uint32_t box_rows);
+                          uint64_t count, uint32_t box_cols, uint32_t box_rows);
 
 // Repack 8-bit expert weights [E][k][n] (n contiguous) into [E][n][k] (k contiguous).
 cudaError_t launch_pack_w8(const int8_t* src, int8_t* dst, int64_t E, int64_t k, int64_t n,

@@ -2,17 +2,22 @@
 //   Y[m] = addend[m] + X[m] W + scale[a] (X[m] A[a]) B[a],   a = adapter[m] (-1: none)
 // for at most 64 rows, in one cooperative kernel (more rows: lora_sm100.cu, lora_f32.cu).
 //
-// What bounds it: one pass over W. W runs through the ring of stream.cuh in equal shares per
-// block, as the few-token layer's down projection does. The adapters' part hides behind it:
+// What bounds it: one pass over W (and over the used adapters). W runs through the ring of
+// stream.cuh in equal shares per block, as the few-token layer's down projection does. The
+// adapters' part hides behind it:
 //   1. Shrink. While the ring fills, the consumers compute S = X A: block (row, slice of K), a
 //      16-byte piece of an A row per thread, fp32 partial sums to L2. The block arrives at the
 //      grid barrier and goes on with W.
-//   2. Expand. Only when a tile of Y is summed does the block wait for the barrier (long since
-//      complete), add the partial S and multiply them by the adapters' B columns of the tile, in
-//      fp32 on the CUDA cores: r multiply-adds per output, a few per cent of the projection's.
+//   2. Expand, scale S B[a] for the rows of a tile, in fp32 on the CUDA cores, cut into units
+//      (4 rows x 128 columns x 16 ranks) and spread over the tile's stages: a unit's loads of B
+//      are issued in one stage and used in the next, so their latency passes under the stream.
+//      (All at the end of the tile, 48 rows of 48 adapters took 81 us where W takes 21.) A block
+//      that has a share of a tile takes the same share of its units. The barrier is waited for
+//      at the first unit.
 // S stays fp32 throughout, so the only rounding is that of Y.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "stream.cuh"
@@ -37,6 +42,7 @@ struct LoraArgs {
   void* Y;
   float* part_s;   // [slices][M][rank]
   float* part;     // [grid][2][part_floats]: sums of shared tiles
+  float* delta;    // [grid][part_floats]: adapters' part of the block's current tile
   int* counters;   // [kMaxGrid]: arrivals at shared tiles
   int* bar;        // [2] workspace header ints, zero at rest
   int* err;
@@ -128,33 +134,10 @@ __device__ void shrink(const LoraArgs& a, const LoraTables& tb, float* red, int 
   }
 }
 
-// Adds the adapter's part and the addend to two summed columns of a row and stores them.
+// Adds the addend to two columns of a row and stores them.
 template <bool F32>
-__device__ __forceinline__ void finish(const LoraArgs& a, const LoraTables& tb, const float* S,
-                                       int m, int n, float2 v) {
+__device__ __forceinline__ void finish(const LoraArgs& a, int m, int n, float2 v) {
   if (m >= a.M || n >= a.N) return;
-  const int ad = tb.adapter[m];
-  if (ad >= 0) {
-    const float* s = S + m * a.rank;
-    const int64_t base = static_cast<int64_t>(ad) * a.rank * a.N + n;
-    float2 d = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-    for (int r = 0; r < a.rank; ++r) {
-      const int64_t at = base + static_cast<int64_t>(r) * a.N;
-      float2 b;
-      if constexpr (F32) {
-        b = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.B) + at));
-      } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(
-            static_cast<const __nv_bfloat16*>(a.B) + at));
-        b = make_float2(bf16_bits_to_float(w & 0xFFFFu), bf16_bits_to_float(w >> 16));
-      }
-      d.x = fmaf(s[r], b.x, d.x);
-      d.y = fmaf(s[r], b.y, d.y);
-    }
-    v.x += d.x;
-    v.y += d.y;
-  }
   const int64_t at = static_cast<int64_t>(m) * a.N + n;
   if constexpr (F32) {
     if (a.addend != nullptr) {
@@ -173,6 +156,75 @@ __device__ __forceinline__ void finish(const LoraArgs& a, const LoraTables& tb, 
     *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.Y) + at) = pack_bf16x2(v.x, v.y);
   }
 }
+
+// The adapters' part of a tile in units: thread tid holds place i = tid + kConsumers * it of the
+// epilogue's order (row i / kPairs, two columns) for iteration it, kUnitRanks ranks at a time.
+constexpr int kUnitRanks = 16;
+
+template <int WK>
+struct Expand {
+  static constexpr bool kIsF32 = WK == kF32;
+  using P = Places<WK>;
+  using Word = typename std::conditional<kIsF32, float2, uint32_t>::type;
+  Word b[kUnitRanks];
+  float2 sum = make_float2(0.0f, 0.0f);
+  int unit = -1;  // whose words are loaded; -1: none
+
+  __device__ __forceinline__ static int chunks(int rank) {
+    return (rank + kUnitRanks - 1) / kUnitRanks;
+  }
+  __device__ __forceinline__ static int iterations(int M) {
+    return (M * P::kPairs + kConsumers - 1) / kConsumers;
+  }
+  // Loads unit u (iteration u / chunks, ranks from (u % chunks) * kUnitRanks).
+  __device__ __forceinline__ void issue(const LoraArgs& a, const LoraTables& tb, int u, int col0,
+                                        int tid) {
+    unit = u;
+    const int n_chunks = chunks(a.rank);
+    const int i = tid + kConsumers * (u / n_chunks), r0 = (u % n_chunks) * kUnitRanks;
+    const int m = P::row(i), n = col0 + P::col(i);
+    const int ad = m < a.M && n < a.N ? tb.adapter[m] : -1;
+    const int64_t base = (static_cast<int64_t>(ad) * a.rank + r0) * a.N + n;
+#pragma unroll
+    for (int r = 0; r < kUnitRanks; ++r) {
+      if constexpr (kIsF32) {
+        b[r] = make_float2(0.0f, 0.0f);
+        if (ad >= 0 && r0 + r < a.rank)
+          b[r] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.B) + base +
+                                                       static_cast<int64_t>(r) * a.N));
+      } else {
+        b[r] = 0u;
+        if (ad >= 0 && r0 + r < a.rank)
+          b[r] = __ldg(reinterpret_cast<const uint32_t*>(
+              static_cast<const __nv_bfloat16*>(a.B) + base + static_cast<int64_t>(r) * a.N));
+      }
+    }
+  }
+  // Multiplies the loaded unit by S (rows past the rank and rows without an adapter: no terms);
+  // after a place's last ranks its sum goes to `delta`.
+  __device__ __forceinline__ void complete(const LoraArgs& a, const LoraTables& tb, const float* S,
+                                           float2* delta, int tid) {
+    if (unit < 0) return;
+    const int n_chunks = chunks(a.rank), it = unit / n_chunks, r0 = (unit % n_chunks) * kUnitRanks;
+    const int i = tid + kConsumers * it, m = P::row(i);
+    if (r0 == 0) sum = make_float2(0.0f, 0.0f);
+    if (m < a.M && tb.adapter[m] >= 0) {
+      const float* s = S + m * a.rank + r0;
+#pragma unroll
+      for (int r = 0; r < kUnitRanks; ++r) {
+        if (r0 + r < a.rank) {
+          float2 v;
+          if constexpr (kIsF32) v = b[r];
+          else v = make_float2(bf16_bits_to_float(b[r] & 0xFFFFu), bf16_bits_to_float(b[r] >> 16));
+          sum.x = fmaf(s[r], v.x, sum.x);
+          sum.y = fmaf(s[r], v.y, sum.y);
+        }
+      }
+    }
+    if (r0 + kUnitRanks >= a.rank) delta[i] = sum;
+    unit = -1;
+  }
+};
 
 template <int WK, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -300,14 +352,27 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       if (have_s) return;
       have_s = true;
       if (!grid_wait(a.bar, G, tid, &tb.flag, a.timeout_ns, a.err)) ok = false;
-      for (int i = tid; i < a.M * a.rank; i += kConsumers) {
-        const int ad = tb.adapter[i / a.rank];
-        if (ad < 0) continue;
+      const int n = a.M * a.rank;
+      int per = 1;  // threads per value, over the slices
+      while (per * 2 <= a.slices && per * 2 * n <= kConsumers) per *= 2;
+      const int part = per > 1 ? tid / n : 0;
+      for (int i = per > 1 ? tid % n : tid; i < n && part < per; i += kConsumers) {
         float s = 0.0f;
+        if (tb.adapter[i / a.rank] >= 0) {
 #pragma unroll 8
-        for (int q = 0; q < a.slices; ++q)
-          s += __ldcg(a.part_s + static_cast<int64_t>(q) * a.M * a.rank + i);
-        sums[i] = a.scale != nullptr ? s * __ldg(a.scale + ad) : s;
+          for (int q = part; q < a.slices; q += per)
+            s += __ldcg(a.part_s + static_cast<int64_t>(q) * n + i);
+        }
+        if (per > 1) red[part * n + i] = s;
+        else sums[i] = s;
+      }
+      named_bar_sync(kBarConsumers, kConsumers);
+      for (int i = tid; i < n; i += kConsumers) {
+        float s = per > 1 ? 0.0f : sums[i];
+        if (per > 1)
+          for (int q = 0; q < per; ++q) s += red[q * n + i];
+        const int ad = tb.adapter[i / a.rank];
+        sums[i] = ad >= 0 && a.scale != nullptr ? s * __ldg(a.scale + ad) : s;
       }
       named_bar_sync(kBarConsumers, kConsumers);
     };
@@ -320,7 +385,24 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       const int cb = static_cast<int>(tile);
       Acc<WK, NT> acc;
       acc.zero();
+      // Units [u_begin, u_end) of the tile are this block's, due evenly over its stages.
+      Expand<WK> ex;
+      float2* delta = reinterpret_cast<float2*>(a.delta + static_cast<int64_t>(me) * a.part_floats);
+      const int iters = Expand<WK>::iterations(a.M), chunks = Expand<WK>::chunks(a.rank);
+      auto units_before = [&](int k) {  // whole iterations, so that a place has one block
+        return static_cast<int>(static_cast<long long>(iters) * k / steps) * chunks;
+      };
+      const int u_begin = units_before(k0), u_end = units_before(k1);
+      int u_next = u_begin;
       for (int k = k0; k < k1; ++k) {
+        const int due = u_begin + static_cast<int>(static_cast<long long>(u_end - u_begin) *
+                                                   (k + 1 - k0) / (k1 - k0));
+        if (ex.unit >= 0 || due - u_next > 1) take_s();
+        ex.complete(a, tb, sums, delta, tid);
+        for (; u_next < due; ++u_next) {
+          ex.complete(a, tb, sums, delta, tid);  // more than one unit a stage: one at a time
+          ex.issue(a, tb, u_next, cb * S::kCols, tid);
+        }
         if (ok && (!mbar_wait(&tb.full[cur.stage], cur.phase, a.timeout_ns) ||
                    !mbar_wait(&tb.rows_full[cur.stage], cur.phase, a.timeout_ns))) {
           ok = false;
@@ -348,6 +430,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         cur.next(ring.stages);
       }
       take_s();
+      ex.complete(a, tb, sums, delta, tid);
       const bool whole = k0 == 0 && k1 == steps;
       float2* mine = reinterpret_cast<float2*>(
           a.part + (static_cast<int64_t>(me) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
@@ -355,9 +438,16 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         put_tile<WK, NT>(red, acc, j, warp, lane);
         named_bar_sync(kBarConsumers, kConsumers);
         for (int i = tid; i < P::kCount; i += kConsumers) {
-          const float2 v = take_pair<WK>(red, -1, P::row(i), P::col(i));
-          if (whole) finish<kIsF32>(a, tb, sums, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
-          else mine[j * P::kCount + i] = v;
+          float2 v = take_pair<WK>(red, -1, P::row(i), P::col(i));
+          const int place = j * P::kCount + i;  // written by this thread, where it is a unit's
+          const int unit = place / kConsumers * chunks;
+          if (unit >= u_begin && unit < u_end) {
+            const float2 d = delta[place];
+            v.x += d.x;
+            v.y += d.y;
+          }
+          if (whole) finish<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
+          else mine[place] = v;
         }
         named_bar_sync(kBarConsumers, kConsumers);
       }
@@ -373,7 +463,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
               v.x += p.x;
               v.y += p.y;
             }
-            finish<kIsF32>(a, tb, sums, P::row(i), cb * S::kCols + P::col(i), v);
+            finish<kIsF32>(a, P::row(i), cb * S::kCols + P::col(i), v);
           }
         }
       }
@@ -397,9 +487,11 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 int64_t lora_part_floats(int64_t M) { return (M + 7) / 8 * 8 * Shape<kBF16>::kCols; }
 
-// Slices of K per row: as many blocks as there are, at least 32 k each.
+// Slices of K per row: as many blocks as there are, at least 32 k each; at most 32, since every
+// block adds them all up.
 int lora_slices(int64_t M, int64_t K) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxGrid / M, (K + 31) / 32)));
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min({kMaxGrid / M, (K + 31) / 32, static_cast<int64_t>(32)})));
 }
 
 template <int WK, int NT>
@@ -430,7 +522,7 @@ cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void*
 size_t lora_few_workspace_bytes(const moe_lora_problem& p) {
   return up256(sizeof(float) * lora_slices(p.M, p.K) * p.M * p.rank) +
          up256(sizeof(int) * kMaxGrid) +
-         up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(p.M));
+         up256(sizeof(float) * 3 * kMaxGrid * lora_part_floats(p.M));
 }
 
 cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, void* scratch,
@@ -452,6 +544,7 @@ cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, voi
   w += up256(sizeof(int) * kMaxGrid);
   a.part = reinterpret_cast<float*>(w);
   a.part_floats = lora_part_floats(p.M);
+  a.delta = a.part + 2 * kMaxGrid * a.part_floats;
   a.bar = bar;
   a.err = err;
   a.timeout_ns = timeout_ns;

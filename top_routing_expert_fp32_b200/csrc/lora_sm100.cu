@@ -8,8 +8,8 @@
 // cent of K; a tile of all-different rows costs one step of 16 per rank-16 adapter.
 //   1. shrink_kernel: S = X A. A group of 8 or 32 rows per cluster of blocks, K cut over the
 //      blocks and their warps; each warp streams (adapter of the group, piece of K) steps
-//      through its own cp.async ring into mma.m16n8k16 (ranks x rows), the fp32 sums meet
-//      through distributed shared memory. S is rounded to bf16 once, with its scale: it is a
+//      through its own TMA ring into mma.m16n8k16 (ranks x rows), the fp32 sums meet through
+//      distributed shared memory. S is rounded to bf16 once, with its scale: it is a
 //      tensor-core operand, and its rounding (2^-9 of the adapter's part) is below the output's.
 //   2. lora_gemm: the product, launched as a programmatic dependent of 1: it waits for S only when
 //      its first tile comes to the extra k-steps, so the shrink hides behind the main loop.
@@ -38,11 +38,8 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kShrinkWarps = 4;
 constexpr int kShrinkThreads = kShrinkWarps * 32;
-constexpr int kShrinkStages = 3;
 
 struct ShrinkArgs {
-  const __nv_bfloat16* X;
-  const __nv_bfloat16* A;
   const int32_t* adapter;
   const float* scale;
   __nv_bfloat16* S;   // [M][ld]
@@ -55,33 +52,44 @@ struct ShrinkArgs {
   int ld;             // columns of S, a multiple of 64
   int tile_rows;      // 128 or 256
   int cluster;        // blocks per row group
+  uint64_t timeout_ns;
 };
 
-// RT: 16-rank tiles (power of two), NT: tiles of 8 rows of a group, CK: k of a step.
+// RT: 16-rank tiles (power of two), NT: tiles of 8 rows of a group. A step is 64 k: one or two
+// boxes of A's ranks (up to 64 of them wide, swizzled over that width) and one of the rows.
 template <int RT, int NT>
 struct ShrinkShape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kRanks = 16 * RT;
-  static constexpr int kCK = RT >= 8 ? 32 : 64;
-  static constexpr int kAPitch = kRanks * 2 + 16;  // odd multiple of 16: no bank conflicts
-  static constexpr int kXPitch = kCK * 2 + 16;
-  static constexpr int kStageBytes = kCK * kAPitch + kRows * kXPitch;
+  static constexpr int kCK = 64;
+  static constexpr int kBoxRanks = kRanks < 64 ? kRanks : 64;
+  static constexpr int kABoxBytes = kCK * kBoxRanks * 2;
+  static constexpr int kABoxes = kRanks / kBoxRanks;
+  static constexpr int kStageBytes = kABoxes * kABoxBytes + kRows * kCK * 2;
+  static constexpr int kStages = RT >= 8 ? 2 : 3;
   static constexpr size_t kSumBytes = sizeof(float) * kShrinkWarps * kRows * kRanks;
-  static constexpr size_t kSmem = kSumBytes + static_cast<size_t>(kShrinkWarps) * kShrinkStages *
-                                                  kStageBytes;
+  static constexpr size_t kSmem =
+      1024 + kSumBytes + static_cast<size_t>(kShrinkWarps) * kStages * kStageBytes;
   static_assert(kSmem <= 227 * 1024 - 4096, "shared memory of a block");
+  static_assert(kStageBytes % 1024 == 0 && kSumBytes % 1024 == 0, "swizzle alignment");
+  // Shared address of the 16 bytes of ranks [8 chunk, 8 chunk + 8) of a k-row of A (the box's
+  // swizzle: 16-byte pieces exchanged by address bits 7 and up over 32, 64 or 128 bytes).
+  __device__ static uint32_t a_piece(uint32_t stage, int row, int chunk) {
+    constexpr int kPieces = kBoxRanks / 8;
+    const int box = chunk / kPieces, c = chunk % kPieces;
+    const int x = RT == 1 ? (row >> 2) & 1 : RT == 2 ? (row >> 1) & 3 : row & 7;
+    return stage + box * kABoxBytes + row * (kBoxRanks * 2) + ((c ^ x) << 4);
+  }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-
 template <int RT, int NT>
-__global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const ShrinkArgs a) {
+__global__ void __launch_bounds__(kShrinkThreads)
+shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mx,
+              const __grid_constant__ ShrinkArgs a) {
   using S = ShrinkShape<RT, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t s_full[kShrinkWarps][S::kStages];
   __shared__ int s_tile[256];   // adapters of the tile's rows
   __shared__ int s_slot[256];   // the tile's slots
   __shared__ uint32_t s_first[8];
@@ -108,12 +116,10 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const ShrinkArgs
   };
   for (int i = tid; i < a.tile_rows; i += kShrinkThreads) s_tile[i] = adapter_of(tile0 + i);
   for (int i = tid; i < static_cast<int>(S::kSumBytes / 4); i += kShrinkThreads) sums[i] = 0.0f;
-  // Ranks past the adapters' own stay zero in the rings: the copies never write there.
-  {
-    uint4* ring = reinterpret_cast<uint4*>(smem + S::kSumBytes);
-    constexpr int n = kShrinkWarps * kShrinkStages * S::kStageBytes / 16;
-    if (a.rank < S::kRanks)
-      for (int i = tid; i < n; i += kShrinkThreads) ring[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid == 0) {
+    for (int w = 0; w < kShrinkWarps; ++w)
+      for (int i = 0; i < S::kStages; ++i) mbar_init(&s_full[w][i], 1);
+    fence_barrier_init();
   }
   __syncthreads();
   // The group's items: its different adapters and the rows that have them.
@@ -141,41 +147,18 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const ShrinkArgs
   const int p1 = static_cast<int>(static_cast<int64_t>(pieces) * (rank_in_cluster + 1) / a.cluster);
   const int per_item = p1 - p0 > warp ? (p1 - p0 - warp + kShrinkWarps - 1) / kShrinkWarps : 0;
   const int total = per_item * s_items;
-  uint8_t* ring = smem + S::kSumBytes + warp * kShrinkStages * S::kStageBytes;
-  const int r8 = a.rank / 8;
+  uint8_t* ring = smem + S::kSumBytes + warp * S::kStages * S::kStageBytes;
   auto load = [&](int q) {
-    if (q < total) {
-      const int item = q / per_item;
-      const int k0 = (p0 + warp + (q - item * per_item) * kShrinkWarps) * S::kCK;
-      const uint32_t dst = smem_u32(ring + (q % kShrinkStages) * S::kStageBytes);
-      const __nv_bfloat16* src =
-          a.A + (static_cast<int64_t>(s_item[item]) * a.K + k0) * a.rank;
-      int row = lane / r8, col = lane % r8;
-      for (int i = lane; i < S::kCK * r8; i += 32) {
-        const bool in = k0 + row < a.K;
-        cp_async16(dst + row * S::kAPitch + col * 16,
-                   src + (in ? static_cast<int64_t>(row) * a.rank + col * 8 : 0), in);
-        row += 32 / r8;
-        col += 32 % r8;
-        if (col >= r8) {
-          col -= r8;
-          ++row;
-        }
-      }
-      const uint32_t xdst = dst + S::kCK * S::kAPitch;
-      const uint32_t mask = s_mask[item];
-      constexpr int x8 = S::kCK / 8;
+    if (q >= total || lane != 0) return;
+    const int item = q / per_item;
+    const int k0 = (p0 + warp + (q - item * per_item) * kShrinkWarps) * S::kCK;
+    uint8_t* dst = ring + (q % S::kStages) * S::kStageBytes;
+    uint64_t* bar = &s_full[warp][q % S::kStages];
+    mbar_arrive_expect_tx(bar, S::kStageBytes);
 #pragma unroll
-      for (int i = 0; i < S::kRows * x8 / 32; ++i) {
-        const int at = i * 32 + lane, r = at / x8, c = at % x8;
-        if ((mask >> (r & ~7)) & 0xFFu) {  // tiles of 8 rows without a row of this adapter: unread
-          const bool in = row0 + r < a.M && k0 + c * 8 < a.K;
-          cp_async16(xdst + r * S::kXPitch + c * 16,
-                     a.X + (in ? (row0 + r) * a.K + k0 + c * 8 : 0), in);
-        }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int i = 0; i < S::kABoxes; ++i)
+      tma_load_3d(dst + i * S::kABoxBytes, &ma, bar, i * S::kBoxRanks, k0, s_item[item]);
+    tma_load_2d(dst + S::kABoxes * S::kABoxBytes, &mx, bar, k0, static_cast<int>(row0));
   };
   float acc[RT][NT][4];
 #pragma unroll
@@ -184,24 +167,27 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const ShrinkArgs
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[r][j][c] = 0.0f;
-  for (int q = 0; q < kShrinkStages - 1; ++q) load(q);
+  for (int q = 0; q < S::kStages - 1; ++q) load(q);
   const int b = lane >> 3, i8 = lane & 7, t = lane & 3, g = lane >> 2;
+  bool ok = true;
   for (int q = 0; q < total; ++q) {
-    load(q + kShrinkStages - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kShrinkStages - 1) : "memory");
-    __syncwarp();
+    load(q + S::kStages - 1);
+    if (ok && !mbar_wait(&s_full[warp][q % S::kStages], (q / S::kStages) & 1, a.timeout_ns)) {
+      ok = false;
+      record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+    }
     const int item = q / per_item;
     const uint32_t mask = s_mask[item];
-    const uint8_t* at = ring + (q % kShrinkStages) * S::kStageBytes;
-    const uint8_t* xs = at + S::kCK * S::kAPitch;
+    const uint8_t* at = ring + (q % S::kStages) * S::kStageBytes;
+    const uint8_t* xs = at + S::kABoxes * S::kABoxBytes;
 #pragma unroll
     for (int kg = 0; kg < S::kCK / 32; ++kg) {
       uint32_t x[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        if (((mask >> (8 * j)) & 0xFFu) == 0) continue;
-        const uint4 v =
-            *reinterpret_cast<const uint4*>(xs + (8 * j + g) * S::kXPitch + kg * 64 + t * 16);
+        if (((mask >> (8 * j)) & 0xFFu) == 0) continue;  // no row of this adapter
+        const uint4 v = *reinterpret_cast<const uint4*>(xs + (8 * j + g) * 128 +
+                                                        (((kg * 4 + t) ^ g) << 4));
         const bool one = (t & 1) != 0, two = (t & 2) != 0;
         const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
                        a3 = one ? v.x : v.w;
@@ -212,12 +198,11 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const ShrinkArgs
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t arow = smem_u32(at) + (kg * 32 + stream::block_row(2 * s + (b >> 1), i8)) *
-                                                 S::kAPitch;
+        const int row = kg * 32 + static_cast<int>(stream::block_row(2 * s + (b >> 1), i8));
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           uint32_t w[4];
-          stream::ldsm_x4_trans(arow + (r * 2 + (b & 1)) * 16, w);
+          stream::ldsm_x4_trans(S::a_piece(smem_u32(at), row, r * 2 + (b & 1)), w);
 #pragma unroll
           for (int j = 0; j < NT; ++j)
             if (((mask >> (8 * j)) & 0xFFu) != 0)
@@ -242,7 +227,10 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const ShrinkArgs
     }
     __syncwarp();  // the stage is read before the next load overwrites it
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // (Every step issued was waited for; after a timeout the copies get another bounded wait.)
+  if (!ok)
+    for (int q = total - 1; q >= 0 && q >= total - S::kStages; --q)
+      (void)mbar_wait(&s_full[warp][q % S::kStages], (q / S::kStages) & 1, a.timeout_ns);
 
   // The tile's slots: its different adapters by first appearance.
   for (int i0 = 0; i0 < a.tile_rows; i0 += kShrinkThreads) {
@@ -344,8 +332,10 @@ struct GemmShape {
   // Lane masks of a stage's slots (at most kStageUnits).
   static constexpr int kMaskWords = kTileRows / 32;
   static constexpr int kMaskBytes = kStageUnits * kMaskWords * 4;
+  static constexpr int kIdBytes = kTileRows * 4;  // adapters of a tile's slots
   static constexpr int kSmemBytes = kStages * (kStageBytes + kMaskBytes) +
-                                    kEpiWarps * kStoreStage + 1024 /*align*/ + 512 /*barriers*/;
+                                    kEpiWarps * kStoreStage + kIdBytes + 1024 /*align*/ +
+                                    512 /*barriers*/;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   // kind::f16: D fp32, A bf16 K-major, B bf16 MN-major.
   static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
@@ -399,12 +389,14 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
   uint8_t* sB = smem + S::kStages * kABytes;
   uint8_t* sM = sB + S::kStages * S::kBBytes;  // lane masks
   uint8_t* sT = sM + S::kStages * S::kMaskBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sT + kEpiWarps * kStoreStage);
+  int* s_ids = reinterpret_cast<int*>(sT + kEpiWarps * kStoreStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sT + kEpiWarps * kStoreStage + S::kIdBytes);
   uint64_t* empty = full + S::kStages;
   uint64_t* tfull = empty + S::kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drained = tempty + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* ids_full = drained + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(ids_full + 1);
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;  // 0: the CTA that issues the MMAs
   const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
@@ -441,6 +433,7 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
       mbar_init(&tempty[i], (PAIR ? 2 : 1) * kEpiWarps);
     }
     mbar_init(drained, 1);
+    mbar_init(ids_full, 1);
     fence_barrier_init();
     prefetch_tensormap(&mx);
     prefetch_tensormap(&mw);
@@ -469,14 +462,7 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
       long long issued = 0;
       bool ok = true, s_ready = false;
       const uint64_t keep = l2_policy(1), plain = l2_policy(0);
-      int ids[kStageUnits] = {};  // adapters of a k-block's units
-      auto fetch_ids = [&](int64_t list, int u0, int slots) {
-#pragma unroll
-        for (int j = 0; j < kStageUnits; ++j) {
-          const int slot = (u0 + j) / p.units;
-          if (slot < slots) ids[j] = p.slots[list + slot];
-        }
-      };
+      uint32_t ids_phase = 0;
       for (int64_t id = unit; id < work && ok; id += n_units) {
         int64_t m_tile;
         int n0, mmas;
@@ -491,6 +477,11 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
             s_ready = true;
             slots = p.n_slots[m_tile];
             kbs = num_kb + (slots * p.units + kStageUnits - 1) / kStageUnits;
+            if (slots > 0) {  // their adapters, in whole 16-byte pieces
+              const uint32_t n = static_cast<uint32_t>(slots + 3) / 4 * 16;
+              mbar_arrive_expect_tx(ids_full, n);
+              bulk_g2s(s_ids, p.slots + m_tile * S::kTileRows, n, ids_full);
+            }
           }
           if (!mbar_wait(&empty[c.stage], c.phase ^ 1u, p.timeout_ns)) {
             record_error(p.err, MOE_DEVERR_WAIT_TIMEOUT);
@@ -536,19 +527,26 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
             const int s_col = p.units > kStageUnits ? (u0 % p.units) * kUnit : 0;
             if (PAIR) tma_load_2d_pair_hint(a_dst, &ms, bar, s_col, row0, keep);
             else tma_load_2d_hint(a_dst, &ms, &full[c.stage], s_col, row0, keep);
-            if (kb == num_kb) fetch_ids(list, u0, slots);
-#pragma unroll
-            for (int j = 0; j < kStageUnits; ++j) {
-              if (j < n) {
-                const int r0 = ((u0 + j) % p.units) * kUnit;
-                for (int i = 0; i < boxes; ++i) {
-                  uint8_t* dst = b_dst + i * kBoxBytes + j * kUnitBytes;
-                  if (PAIR) tma_load_3d_pair_hint(dst, &mb, bar, box_col(i), r0, ids[j], plain);
-                  else tma_load_3d_hint(dst, &mb, &full[c.stage], box_col(i), r0, ids[j], plain);
-                }
+            if (kb == num_kb) {
+              if (!mbar_wait(ids_full, ids_phase, p.timeout_ns)) {
+                record_error(p.err, MOE_DEVERR_WAIT_TIMEOUT);
+                ok = false;
+              }
+              ids_phase ^= 1u;
+            }
+            int slot = slot0, v = u0 % p.units;
+            for (int j = 0; j < n; ++j) {
+              const int ad = ok ? s_ids[slot] : 0;
+              for (int i = 0; i < boxes; ++i) {
+                uint8_t* dst = b_dst + i * kBoxBytes + j * kUnitBytes;
+                if (PAIR) tma_load_3d_pair_hint(dst, &mb, bar, box_col(i), v * kUnit, ad, plain);
+                else tma_load_3d_hint(dst, &mb, &full[c.stage], box_col(i), v * kUnit, ad, plain);
+              }
+              if (++v == p.units) {
+                v = 0;
+                ++slot;
               }
             }
-            fetch_ids(list, u0 + kStageUnits, slots);  // the next k-block's, ahead of its use
           }
           c.next(S::kStages);
           ++issued;
@@ -760,8 +758,12 @@ int s_cols_of(const moe_lora_problem& p) {
 }
 
 template <int RT, int NT>
-cudaError_t launch_shrink(const ShrinkArgs& a, cudaStream_t stream) {
+cudaError_t launch_shrink(const ShrinkArgs& a, const LoraTensors& t, cudaStream_t stream) {
   using S = ShrinkShape<RT, NT>;
+  CUtensorMap ma, mx;
+  if (!make_box_map_3d_bf16(&ma, t.A, a.rank, a.K, a.L, S::kBoxRanks, S::kCK) ||
+      !make_tensor_map_2d_bf16(&mx, t.X, a.K, a.M, S::kCK, S::kRows))
+    return cudaErrorInvalidValue;
   auto kernel = shrink_kernel<RT, NT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(S::kSmem));
@@ -779,16 +781,16 @@ cudaError_t launch_shrink(const ShrinkArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, ma, mx, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int NT>
-cudaError_t launch_shrink_rank(const ShrinkArgs& a, cudaStream_t stream) {
-  if (a.rank <= 16) return launch_shrink<1, NT>(a, stream);
-  if (a.rank <= 32) return launch_shrink<2, NT>(a, stream);
-  if (a.rank <= 64) return launch_shrink<4, NT>(a, stream);
-  return launch_shrink<8, NT>(a, stream);
+cudaError_t launch_shrink_rank(const ShrinkArgs& a, const LoraTensors& t, cudaStream_t stream) {
+  if (a.rank <= 16) return launch_shrink<1, NT>(a, t, stream);
+  if (a.rank <= 32) return launch_shrink<2, NT>(a, t, stream);
+  if (a.rank <= 64) return launch_shrink<4, NT>(a, t, stream);
+  return launch_shrink<8, (NT > 2 ? 2 : NT)>(a, t, stream);  // (smaller groups: shared memory)
 }
 
 template <bool PAIR, int NB>
@@ -842,8 +844,7 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
   w += up256(sizeof(uint32_t) * tiles_of(p) * tile_rows_of(p) * (tile_rows_of(p) / 32));
 
   ShrinkArgs a{};
-  a.X = static_cast<const __nv_bfloat16*>(t.X);
-  a.A = static_cast<const __nv_bfloat16*>(t.A);
+  a.timeout_ns = timeout_ns;
   a.adapter = t.adapter;
   a.scale = t.scale;
   a.S = reinterpret_cast<__nv_bfloat16*>(w);
@@ -865,14 +866,15 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
   a.cluster = 1;
   while (a.cluster < 8 && groups * a.cluster * 2 <= 2 * kSms && a.K >= 256 * a.cluster * 2)
     a.cluster *= 2;
-  cudaError_t e = small ? launch_shrink_rank<1>(a, stream) : launch_shrink_rank<4>(a, stream);
+  cudaError_t e =
+      small ? launch_shrink_rank<1>(a, t, stream) : launch_shrink_rank<4>(a, t, stream);
   if (e != cudaSuccess) return e;
 
   CUtensorMap mx, mw, ms, mb;
   if (!make_tensor_map_2d_bf16(&mx, t.X, p.K, p.M, 64, kRows) ||
       !make_tensor_map_2d_bf16(&ms, a.S, a.ld, p.M, 64, kRows) ||
-      !make_box_map_3d_bf16(&mw, t.W, p.N, p.K, 1, BK) ||
-      !make_box_map_3d_bf16(&mb, t.B, p.N, p.rank, p.adapters, kUnit))
+      !make_box_map_3d_bf16(&mw, t.W, p.N, p.K, 1, 64, BK) ||
+      !make_box_map_3d_bf16(&mb, t.B, p.N, p.rank, p.adapters, 64, kUnit))
     return cudaErrorInvalidValue;
   GemmArgs g{};
   g.n_slots = n_slots;
