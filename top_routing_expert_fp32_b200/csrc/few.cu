@@ -495,20 +495,21 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
   if (whole) return;
   const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
   if (!last_to_finish(a.counters + first, last - first + 1, c.tid, &tb.flag)) return;
+  constexpr int kMine = (P::kCount + kConsumers - 1) / kConsumers;  // places of a row tile
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
-    for (int i = c.tid; i < P::kCount; i += kConsumers) {
-      float2 h1 = make_float2(0.0f, 0.0f), h2 = h1;
-      for (int b = first; b <= last; ++b) {
-        const float2* p = reinterpret_cast<const float2*>(
-            a.part + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * a.part_floats);
-        const float2 v1 = __ldcg(p + (2 * j) * P::kCount + i);
-        const float2 v2 = __ldcg(p + (2 * j + 1) * P::kCount + i);
-        h1.x += v1.x;
-        h1.y += v1.y;
-        h2.x += v2.x;
-        h2.y += v2.y;
-      }
-      finish_h<WK>(a, tb, pt, 8 * j + P::row(i), fb * S::kCols + P::col(i), h1, h2);
+    float2 h[2][kMine];
+#pragma unroll
+    for (int branch = 0; branch < 2; ++branch) {
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) h[branch][q] = make_float2(0.0f, 0.0f);
+      add_shares(h[branch], a.part, a.part_floats, first, last, (2 * j + branch) * P::kCount + c.tid,
+                 (2 * j + branch + 1) * P::kCount);
+    }
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int i = c.tid + q * kConsumers;
+      if (i < P::kCount)
+        finish_h<WK>(a, tb, pt, 8 * j + P::row(i), fb * S::kCols + P::col(i), h[0][q], h[1][q]);
     }
   }
 }
@@ -605,7 +606,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&tb.full[i], 1);
-      mbar_init(&tb.rows_full[i], 1);
+      mbar_init(&tb.rows_full[i], 32);  // the row producer's lanes
       mbar_init(&tb.empty[i], kConsumerWarps);
     }
     fence_barrier_init();
@@ -722,29 +723,30 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       }
       __syncwarp();
     } else if (warp == kRowWarp) {
-      // Row producer: the lanes copy one row (X) or one tile (H) each. H waits for the barrier.
+      // Row producer: the kept tokens' rows of X, 16 bytes per lane and copy; then tiles of H,
+      // one bulk copy each, after the barrier that completes H.
       Cursor c;
       bool good = true;
       long long issued = 0;
-      // All lanes: the stage is free and its bytes are announced.
-      auto acquire = [&](uint32_t bytes) {
+      auto acquire = [&] {  // all lanes: the stage is free
         good = mbar_wait(&tb.empty[c.stage], c.phase ^ 1u, a.timeout_ns);
         good = __all_sync(0xFFFFFFFFu, good);
-        if (good && lane == 0) mbar_arrive_expect_tx(&tb.rows_full[c.stage], bytes);
-        __syncwarp();
         return good;
       };
       auto up_rows = [&](const Part& pt, int, int k) {
         constexpr int kEl = WK == kF32 ? 4 : 2;
-        const int d = k * kBoxRows;
-        const uint32_t bytes = static_cast<uint32_t>(min(kBoxRows, a.D - d) * kEl);
-        if (!acquire(bytes * static_cast<uint32_t>(pt.n))) return false;
-        uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
-        if (lane < pt.n)
-          bulk_g2s(dst + lane * (WK == kF32 ? kRowPitchF32 : kRowPitch),
-                   static_cast<const uint8_t*>(a.X) +
-                       (static_cast<int64_t>(tb.row_tok[pt.row0 + lane]) * a.D + d) * kEl,
-                   bytes, &tb.rows_full[c.stage]);
+        constexpr int kPieces = kBoxRows * kEl / 16;  // of a row
+        constexpr int kPitch = WK == kF32 ? kRowPitchF32 : kRowPitch;
+        if (!acquire()) return false;
+        const int d = k * kBoxRows + lane % kPieces * (16 / kEl);
+        if (d < a.D) {
+          uint8_t* dst = ring.rows + c.stage * ring.row_bytes + lane % kPieces * 16;
+          for (int r = lane / kPieces; r < pt.n; r += 32 / kPieces)
+            cp_async16(dst + r * kPitch,
+                       static_cast<const uint8_t*>(a.X) +
+                           (static_cast<int64_t>(tb.row_tok[pt.row0 + r]) * a.D + d) * kEl);
+        }
+        cp_async_arrive(&tb.rows_full[c.stage]);
         c.next(ring.stages);
         ++issued;
         return true;
@@ -754,23 +756,27 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
         fence_proxy_async_all();
       };
       auto down_rows = [&](const Part& pt, int, int k) {
+        if (!acquire()) return false;
         uint8_t* dst = ring.rows + c.stage * ring.row_bytes;
+        uint64_t* bar = &tb.rows_full[c.stage];
         if constexpr (WK == kF32) {
-          const int f = k * 2 * kBoxRows;
-          const uint32_t bytes = static_cast<uint32_t>(min(2 * kBoxRows, a.F - f) * 4);
-          if (!acquire(bytes * static_cast<uint32_t>(pt.n))) return false;
-          if (lane < pt.n)
-            bulk_g2s(dst + lane * 2 * kBoxRows * 4,
-                     static_cast<const float*>(a.H) + (pt.row0 + lane) * h_row_f32(a.F) + f, bytes,
-                     &tb.rows_full[c.stage]);
+          constexpr int kPieces = 2 * kBoxRows * 4 / 16;  // 32: a row per copy
+          const int f = k * 2 * kBoxRows + lane * 4;
+          if (f < a.F)
+            for (int r = 0; r < pt.n; ++r)
+              cp_async16(dst + r * (kPieces * 16) + lane * 16,
+                         static_cast<const float*>(a.H) + (pt.row0 + r) * h_row_f32(a.F) + f);
+          cp_async_arrive(bar);
         } else {
           const int tiles = (pt.n + 7) / 8;
-          if (!acquire(static_cast<uint32_t>(tiles) * kTileBytes)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(tiles) * kTileBytes);
+          else mbar_arrive(bar);
+          __syncwarp();
           if (lane < tiles)
             bulk_g2s(dst + lane * kTileBytes,
                      static_cast<const uint8_t*>(a.H) +
                          ((pt.tile + lane) * h_groups(a.F) + k * 4) * kHGroupBytes,
-                     kTileBytes, &tb.rows_full[c.stage]);
+                     kTileBytes, bar);
         }
         c.next(ring.stages);
         ++issued;
@@ -836,16 +842,18 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
         const int first = down.owner(tile * down_steps),
                   last = down.owner(tile * down_steps + down_steps - 1);
         if (last_to_finish(a.counters + kMaxGrid + first, last - first + 1, tid, &tb.flag)) {
-          for (int i = tid; i < a.N * P::kPairs; i += kConsumers) {
-            float2 v = make_float2(0.0f, 0.0f);
-            for (int b = first; b <= last; ++b) {
-              const float2 p = __ldcg(reinterpret_cast<const float2*>(
-                                          a.part + (static_cast<int64_t>(b) * 2 +
-                                                    (b == first ? 1 : 0)) * a.part_floats) + i);
-              v.x += p.x;
-              v.y += p.y;
+          constexpr int kChunk = 8;
+          for (int i0 = tid; i0 < a.N * P::kPairs; i0 += kChunk * kConsumers) {
+            float2 v[kChunk];
+#pragma unroll
+            for (int q = 0; q < kChunk; ++q) v[q] = make_float2(0.0f, 0.0f);
+            add_shares(v, a.part, a.part_floats, first, last, i0, a.N * P::kPairs);
+#pragma unroll
+            for (int q = 0; q < kChunk; ++q) {
+              const int i = i0 + q * kConsumers;
+              if (i < a.N * P::kPairs)
+                store_out<WK>(a, P::row(i), cb * S::kCols + P::col(i), v[q]);
             }
-            store_out<WK>(a, P::row(i), cb * S::kCols + P::col(i), v);
           }
         }
       }
@@ -918,12 +926,12 @@ EncodeTiledFn encode_fn() {
 }  // namespace
 
 bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, uint64_t rows,
-                     uint64_t count) {
+                     uint64_t count, uint32_t box_rows) {
   if (encode_fn() == nullptr) return false;
   const uint64_t el = kind == kF32 ? 4 : kind == kBF16 ? 2 : 1;
   const cuuint64_t dims[3] = {cols, rows, count};
   const cuuint64_t strides[2] = {cols * el, cols * rows * el};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / el), kBoxRows, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / el), box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType type = kind == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : kind == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

@@ -8,16 +8,16 @@
 //   1. Shrink. While the ring fills, the consumers compute S = X A: block (row, slice of K), a
 //      16-byte piece of an A row per thread, fp32 partial sums to L2. The block arrives at the
 //      grid barrier and goes on with W.
-//   2. Expand, scale S B[a] for the rows of a tile, in fp32 on the CUDA cores, cut into units
-//      (4 rows x 128 columns x 16 ranks) and spread over the tile's stages: a unit's loads of B
-//      are issued in one stage and used in the next, so their latency passes under the stream.
-//      (All at the end of the tile, 48 rows of 48 adapters took 81 us where W takes 21.) A block
-//      that has a share of a tile takes the same share of its units. The barrier is waited for
-//      at the first unit.
-// S stays fp32 throughout, so the only rounding is that of Y.
+//   2. Expand. The different adapters of the batch (slots) follow W in the same ring: a stage
+//      then holds 8 pieces of 16 ranks x the tile's columns of some B[a], and a tile's reduction
+//      is its k-stages and then those. A warp multiplies a piece into fresh registers, for the
+//      row tiles that have the adapter, and adds the sums of those rows only, so that a row
+//      never meets another adapter's values, whatever they hold. S enters as two bf16 terms (16
+//      bits of mantissa; fp32 weights: as it is). The barrier is waited for at the first such
+//      stage. (The rows' expand products on the CUDA cores, row by row out of L2, took longer
+//      than the stream: 48 rows of 48 adapters 71 us.)
 #include <algorithm>
 #include <cstdint>
-#include <type_traits>
 
 #include "internal.h"
 #include "stream.cuh"
@@ -35,14 +35,12 @@ constexpr int kRowPitch128 = 272, kRowPitch128F32 = 512;
 struct LoraArgs {
   const void* X;
   const void* A;
-  const void* B;
   const float* scale;
   const int32_t* adapter;
   const void* addend;
   void* Y;
   float* part_s;   // [slices][M][rank]
   float* part;     // [grid][2][part_floats]: sums of shared tiles
-  float* delta;    // [grid][part_floats]: adapters' part of the block's current tile
   int* counters;   // [kMaxGrid]: arrivals at shared tiles
   int* bar;        // [2] workspace header ints, zero at rest
   int* err;
@@ -55,13 +53,23 @@ struct LoraTables {
   uint64_t full[kMaxStages];
   uint64_t rows_full[kMaxStages];
   uint64_t empty[kMaxStages];
-  int adapter[kMaxRows];  // -1: none
+  uint64_t slot_rows[kMaxRows];  // rows of each slot's adapter
+  int slot[kMaxRows];            // the batch's different adapters
+  int adapter[kMaxRows];         // of each row; -1: none
+  uint32_t firsts[2];
   int flag;
 };
 
+constexpr int kPieceRanks = 16;
+constexpr int kStagePieces = 2 * kBoxRows / kPieceRanks;  // 8
+__host__ __device__ constexpr int pieces_of(int rank) {
+  return (rank + kPieceRanks - 1) / kPieceRanks;
+}
+
 constexpr size_t kMaxSmem = 232448;
-constexpr size_t s_bytes(int M, int rank) {
-  return (sizeof(float) * static_cast<size_t>(M) * rank + 15) & ~size_t(15);
+// S: whole row tiles of whole pieces, fp32 or two bf16 terms, zeros beyond M and the rank.
+__host__ __device__ constexpr size_t s_bytes(int M, int rank) {
+  return sizeof(float) * static_cast<size_t>((M + 7) / 8 * 8) * pieces_of(rank) * kPieceRanks;
 }
 __host__ __device__ constexpr size_t lora_ring_bytes(int M, int rank) {
   return (kMaxSmem - 1024 - sizeof(float) * kRedFloats - s_bytes(M, rank) - sizeof(LoraTables)) &
@@ -134,101 +142,102 @@ __device__ void shrink(const LoraArgs& a, const LoraTables& tb, float* red, int 
   }
 }
 
-// Adds the addend to two columns of a row and stores them.
+// Two columns of a row of the addend (zeros without one), and of Y. Each value is read and
+// written by one thread, the addend first, so the two may be the same array.
 template <bool F32>
-__device__ __forceinline__ void finish(const LoraArgs& a, int m, int n, float2 v) {
-  if (m >= a.M || n >= a.N) return;
+__device__ __forceinline__ float2 load_addend(const LoraArgs& a, int m, int n) {
+  if (a.addend == nullptr || m >= a.M || n >= a.N) return make_float2(0.0f, 0.0f);
   const int64_t at = static_cast<int64_t>(m) * a.N + n;
   if constexpr (F32) {
-    if (a.addend != nullptr) {
-      const float2 b = *reinterpret_cast<const float2*>(static_cast<const float*>(a.addend) + at);
-      v.x += b.x;
-      v.y += b.y;
-    }
-    *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + at) = v;
+    return *reinterpret_cast<const float2*>(static_cast<const float*>(a.addend) + at);
   } else {
-    if (a.addend != nullptr) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(
-          static_cast<const __nv_bfloat16*>(a.addend) + at);
-      v.x += bf16_bits_to_float(w & 0xFFFFu);
-      v.y += bf16_bits_to_float(w >> 16);
-    }
-    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.Y) + at) = pack_bf16x2(v.x, v.y);
+    const uint32_t w =
+        *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.addend) + at);
+    return make_float2(bf16_bits_to_float(w & 0xFFFFu), bf16_bits_to_float(w >> 16));
   }
 }
+template <bool F32>
+__device__ __forceinline__ void store_y(const LoraArgs& a, int m, int n, float2 v) {
+  if (m >= a.M || n >= a.N) return;
+  const int64_t at = static_cast<int64_t>(m) * a.N + n;
+  if constexpr (F32)
+    *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + at) = v;
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.Y) + at) = pack_bf16x2(v.x, v.y);
+}
 
-// The adapters' part of a tile in units: thread tid holds place i = tid + kConsumers * it of the
-// epilogue's order (row i / kPairs, two columns) for iteration it, kUnitRanks ranks at a time.
-constexpr int kUnitRanks = 16;
-
-template <int WK>
-struct Expand {
-  static constexpr bool kIsF32 = WK == kF32;
-  using P = Places<WK>;
-  using Word = typename std::conditional<kIsF32, float2, uint32_t>::type;
-  Word b[kUnitRanks];
-  float2 sum = make_float2(0.0f, 0.0f);
-  int unit = -1;  // whose words are loaded; -1: none
-
-  __device__ __forceinline__ static int chunks(int rank) {
-    return (rank + kUnitRanks - 1) / kUnitRanks;
-  }
-  __device__ __forceinline__ static int iterations(int M) {
-    return (M * P::kPairs + kConsumers - 1) / kConsumers;
-  }
-  // Loads unit u (iteration u / chunks, ranks from (u % chunks) * kUnitRanks).
-  __device__ __forceinline__ void issue(const LoraArgs& a, const LoraTables& tb, int u, int col0,
-                                        int tid) {
-    unit = u;
-    const int n_chunks = chunks(a.rank);
-    const int i = tid + kConsumers * (u / n_chunks), r0 = (u % n_chunks) * kUnitRanks;
-    const int m = P::row(i), n = col0 + P::col(i);
-    const int ad = m < a.M && n < a.N ? tb.adapter[m] : -1;
-    const int64_t base = (static_cast<int64_t>(ad) * a.rank + r0) * a.N + n;
+// acc += S x (this warp's two pieces of an adapters' stage). `box`: the warp's box, `piece0`: the
+// first piece of the tile's list that it holds.
+template <int WK, int NT>
+__device__ __forceinline__ void expand(Acc<WK, NT>& acc, uint32_t box, int warp, int lane,
+                                       const LoraTables& tb, const uint8_t* S, int M, int piece0,
+                                       int n_pieces, int per_slot) {
+  const int ranks = per_slot * kPieceRanks;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const int piece = piece0 + h;
+    if (piece >= n_pieces) return;
+    const int slot = piece / per_slot, r0 = (piece - slot * per_slot) * kPieceRanks;
+    const uint64_t rows = tb.slot_rows[slot];
+    const uint32_t row0 = static_cast<uint32_t>((warp & 1) * 32 + h * kPieceRanks);
+    if constexpr (WK == kF32) {
+      float w[kPieceRanks];
 #pragma unroll
-    for (int r = 0; r < kUnitRanks; ++r) {
-      if constexpr (kIsF32) {
-        b[r] = make_float2(0.0f, 0.0f);
-        if (ad >= 0 && r0 + r < a.rank)
-          b[r] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.B) + base +
-                                                       static_cast<int64_t>(r) * a.N));
-      } else {
-        b[r] = 0u;
-        if (ad >= 0 && r0 + r < a.rank)
-          b[r] = __ldg(reinterpret_cast<const uint32_t*>(
-              static_cast<const __nv_bfloat16*>(a.B) + base + static_cast<int64_t>(r) * a.N));
+      for (int i = 0; i < kPieceRanks; ++i) {
+        const uint32_t r = row0 + i;
+        const uint32_t at = box + r * 128 +
+                            (((static_cast<uint32_t>(lane) >> 2) ^ (r & 7u)) << 4) +
+                            (static_cast<uint32_t>(lane) & 3u) * 4;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at) : "memory");
       }
-    }
-  }
-  // Multiplies the loaded unit by S (rows past the rank and rows without an adapter: no terms);
-  // after a place's last ranks its sum goes to `delta`.
-  __device__ __forceinline__ void complete(const LoraArgs& a, const LoraTables& tb, const float* S,
-                                           float2* delta, int tid) {
-    if (unit < 0) return;
-    const int n_chunks = chunks(a.rank), it = unit / n_chunks, r0 = (unit % n_chunks) * kUnitRanks;
-    const int i = tid + kConsumers * it, m = P::row(i);
-    if (r0 == 0) sum = make_float2(0.0f, 0.0f);
-    if (m < a.M && tb.adapter[m] >= 0) {
-      const float* s = S + m * a.rank + r0;
 #pragma unroll
-      for (int r = 0; r < kUnitRanks; ++r) {
-        if (r0 + r < a.rank) {
-          float2 v;
-          if constexpr (kIsF32) v = b[r];
-          else v = make_float2(bf16_bits_to_float(b[r] & 0xFFFFu), bf16_bits_to_float(b[r] >> 16));
-          sum.x = fmaf(s[r], v.x, sum.x);
-          sum.y = fmaf(s[r], v.y, sum.y);
+      for (int m = 0; m < 8 * NT; ++m) {
+        if ((rows >> m) & 1ull) {
+          const float* s = reinterpret_cast<const float*>(S) + m * ranks + r0;
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kPieceRanks; ++i) sum = fmaf(w[i], s[i], sum);
+          acc.v[m] += sum;
+        }
+      }
+    } else {
+      const int b = lane >> 3, i = lane & 7, g = lane >> 2, t = lane & 3;
+      // Matrices of one load: (column halves lo, hi) x (ranks 0-7, 8-15).
+      const uint32_t r = row0 + (b >> 1) * 8 + i;
+      uint32_t w[4][4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        ldsm_x4_trans(box + r * 128 + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (r & 7u)) << 4),
+                      w[m]);
+      const uint32_t* hi = reinterpret_cast<const uint32_t*>(S);
+      const uint32_t* lo = hi + (M + 7) / 8 * 8 * ranks / 2;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const uint32_t mine = static_cast<uint32_t>(rows >> (8 * j)) & 0xFFu;
+        if (mine == 0) continue;
+        const int at = ((8 * j + g) * ranks + r0) / 2 + t;
+        const uint32_t h0 = hi[at], h1 = hi[at + 4], l0 = lo[at], l1 = lo[at + 4];
+        const bool even = (mine >> (2 * t)) & 1u, odd = (mine >> (2 * t + 1)) & 1u;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_bf16(c, w[m], h0, h1);
+          mma_bf16(c, w[m], l0, l1);
+          float* o = &acc.v[(m * NT + j) * 4];
+          o[0] += even ? c[0] : 0.0f;
+          o[1] += odd ? c[1] : 0.0f;
+          o[2] += even ? c[2] : 0.0f;
+          o[3] += odd ? c[3] : 0.0f;
         }
       }
     }
-    if (r0 + kUnitRanks >= a.rank) delta[i] = sum;
-    unit = -1;
   }
-};
+}
 
 template <int WK, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ LoraArgs a) {
+lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mb,
+                const __grid_constant__ LoraArgs a) {
   using S = Shape<WK>;
   using P = Places<WK>;
   constexpr bool kIsF32 = WK == kF32;
@@ -236,9 +245,8 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* red = reinterpret_cast<float*>(smem + lora_ring_bytes(a.M, a.rank));
-  float* sums = red + kRedFloats;  // S [M][rank], scaled
-  LoraTables& tb = *reinterpret_cast<LoraTables*>(reinterpret_cast<uint8_t*>(sums) +
-                                                  s_bytes(a.M, a.rank));
+  uint8_t* S_mem = reinterpret_cast<uint8_t*>(red + kRedFloats);  // S, scaled
+  LoraTables& tb = *reinterpret_cast<LoraTables*>(S_mem + s_bytes(a.M, a.rank));
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
   const int G = static_cast<int>(gridDim.x);
@@ -255,24 +263,63 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&tb.full[i], 1);
-      mbar_init(&tb.rows_full[i], 1);
+      mbar_init(&tb.rows_full[i], 32);  // the row producer's lanes
       mbar_init(&tb.empty[i], kConsumerWarps);
     }
     fence_barrier_init();
     a.counters[me] = 0;  // seen by the others after the grid barrier
   }
-  if (tid >= kConsumers && tid < kConsumers + a.M) {
-    const int m = tid - kConsumers, ad = a.adapter[m];
-    if (ad < -1 || ad >= a.L) record_error(a.err, MOE_DEVERR_BAD_INDEX);
-    tb.adapter[m] = ad >= 0 && ad < a.L ? ad : -1;
+  {  // The rows' adapters, and the batch's different ones by first appearance.
+    const int m = tid - kConsumers;
+    int ad = -1;
+    if (m >= 0 && m < a.M) {
+      ad = a.adapter[m];
+      if (ad < -1 || ad >= a.L) {
+        record_error(a.err, MOE_DEVERR_BAD_INDEX);
+        ad = -1;
+      }
+    }
+    if (m >= 0 && m < kMaxRows) tb.adapter[m] = ad;
+    __syncthreads();
+    uint64_t rows = 0;
+    if (ad >= 0)
+      for (int i = 0; i < a.M; ++i) rows |= static_cast<uint64_t>(tb.adapter[i] == ad) << i;
+    const bool first = ad >= 0 && (rows & ((1ull << m) - 1ull)) == 0;
+    const uint32_t f = __ballot_sync(0xFFFFFFFFu, first);
+    if (m >= 0 && m < kMaxRows && lane == 0) tb.firsts[m >> 5] = f;
+    __syncthreads();
+    if (first) {
+      const int at = __popc(f & ((1u << lane) - 1u)) + (m >= 32 ? __popc(tb.firsts[0]) : 0);
+      tb.slot[at] = ad;
+      tb.slot_rows[at] = rows;
+    }
+    // S is written where a row has an adapter; the rest of it stays zero.
+    for (int i = tid; i < static_cast<int>(s_bytes(a.M, a.rank) / 4); i += kThreads)
+      reinterpret_cast<uint32_t*>(S_mem)[i] = 0u;
   }
   __syncthreads();
 
-  const int steps = (a.K + 2 * kBoxRows - 1) / (2 * kBoxRows);
+  const int per_slot = pieces_of(a.rank);
+  const int n_pieces = (__popc(tb.firsts[0]) + __popc(tb.firsts[1])) * per_slot;
+  const int k_steps = (a.K + 2 * kBoxRows - 1) / (2 * kBoxRows);
+  const int steps = k_steps + (n_pieces + kStagePieces - 1) / kStagePieces;
   const int tiles = (a.N + S::kCols - 1) / S::kCols;
   SplitK sp{static_cast<long long>(tiles) * steps, 0};
   sp.grid = static_cast<int>(min(static_cast<long long>(G), sp.total));
   const long long s0 = me < sp.grid ? sp.start(me) : 0, s1 = me < sp.grid ? sp.start(me + 1) : 0;
+
+  // The block's stages in order: f(column tile, k-stage), until it returns false. (Divisions per
+  // tile only: a 64-bit one per stage cost the producer more than a stage's HBM time.)
+  auto walk = [&](auto f) {
+    for (long long s = s0; s < s1;) {
+      const long long tile = s / steps;
+      int k = static_cast<int>(s - tile * steps);
+      const int k_end = static_cast<int>(min(static_cast<long long>(steps), k + (s1 - s)));
+      s += k_end - k;
+      for (; k < k_end; ++k)
+        if (!f(static_cast<int>(tile), k)) return;
+    }
+  };
 
   if (warp >= kConsumerWarps) {
     give_registers<kProducerRegs>();
@@ -282,12 +329,26 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         Cursor c;
         bool good = true;
         long long issued = 0;
-        for (long long s = s0; s < s1; ++s) {
-          if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) break;
-          const int col = static_cast<int>(s / steps) * S::kCols;
-          const int row = static_cast<int>(s % steps) * 2 * kBoxRows;
+        walk([&](int tile, int k) {
+          if (!(good = acquire_weights(ring, c, issued, a.timeout_ns))) return false;
+          const int col = tile * S::kCols, row = k * 2 * kBoxRows;
           uint8_t* dst = smem + static_cast<size_t>(c.stage) * kStageBytes;
           uint64_t* bar = &tb.full[c.stage];
+          if (k >= k_steps) {
+            // 16 rows of each box per piece; the last stage's unused ones repeat the last piece,
+            // so that every stage has the same bytes.
+            int piece = (k - k_steps) * kStagePieces;
+            for (int j = 0; j < kStagePieces; ++j, ++piece) {
+              const int p = min(piece, n_pieces - 1), slot = p / per_slot;
+              uint8_t* d = dst + (j >> 2) * 2 * kBoxBytes + (j & 3) * kPieceRanks * 128;
+              const int r0 = (p - slot * per_slot) * kPieceRanks, ad = tb.slot[slot];
+              tma_load_3d_hint(d, &mb, bar, col, r0, ad, policy);
+              tma_load_3d_hint(d + kBoxBytes, &mb, bar, col + S::kBoxCols, r0, ad, policy);
+            }
+            c.next(ring.stages);
+            ++issued;
+            return true;
+          }
           tma_load_3d_hint(dst, &mw, bar, col, row, 0, policy);
           tma_load_3d_hint(dst + kBoxBytes, &mw, bar, col + S::kBoxCols, row, 0, policy);
           tma_load_3d_hint(dst + 2 * kBoxBytes, &mw, bar, col, row + kBoxRows, 0, policy);
@@ -295,59 +356,62 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
                            policy);
           c.next(ring.stages);
           ++issued;
-        }
+          return true;
+        });
         if (!good) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
         drain(tb.full, ring.stages, c, issued, a.timeout_ns);
       }
       __syncwarp();
     } else if (warp == kRowWarp) {
       constexpr int kEl = kIsF32 ? 4 : 2;
+      constexpr int kPieces = 2 * kBoxRows * kEl / 16;  // 16-byte pieces of a row
+      constexpr int kPitch = kIsF32 ? kRowPitch128F32 : kRowPitch128;
       Cursor c;
       bool good = true;
       long long issued = 0;
-      for (long long s = s0; s < s1; ++s) {
-        const int k = static_cast<int>(s % steps) * 2 * kBoxRows;
-        const uint32_t bytes = static_cast<uint32_t>(min(2 * kBoxRows, a.K - k) * kEl);
+      walk([&](int, int k_stage) {
         good = mbar_wait(&tb.empty[c.stage], c.phase ^ 1u, a.timeout_ns);
         good = __all_sync(0xFFFFFFFFu, good);
-        if (!good) break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(&tb.rows_full[c.stage], bytes * static_cast<uint32_t>(a.M));
-        __syncwarp();
-        for (int m = lane; m < a.M; m += 32)
-          bulk_g2s(ring.rows + c.stage * ring.row_bytes +
-                       m * (kIsF32 ? kRowPitch128F32 : kRowPitch128),
-                   static_cast<const uint8_t*>(a.X) + (static_cast<int64_t>(m) * a.K + k) * kEl,
-                   bytes, &tb.rows_full[c.stage]);
+        if (!good) return false;
+        const int k = k_stage * 2 * kBoxRows + lane % kPieces * (16 / kEl);
+        if (k_stage < k_steps && k < a.K) {  // (an adapters' stage has no rows to copy)
+          uint8_t* dst = ring.rows + c.stage * ring.row_bytes + lane % kPieces * 16;
+          const uint8_t* src = static_cast<const uint8_t*>(a.X) + static_cast<int64_t>(k) * kEl;
+#pragma unroll 4
+          for (int m = lane / kPieces; m < a.M; m += 32 / kPieces)
+            cp_async16(dst + m * kPitch, src + static_cast<int64_t>(m) * a.K * kEl);
+        }
+        cp_async_arrive(&tb.rows_full[c.stage]);
         c.next(ring.stages);
         ++issued;
-      }
+        return true;
+      });
       if (!good && lane == 0) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
       drain(tb.rows_full, ring.stages, c, issued, a.timeout_ns);
       __syncwarp();
-    } else if (warp >= kConsumerWarps + 2) {
-      // The remaining warps bring the adapters' columns of this block's tiles to L2 ahead of the
-      // epilogues that read them.
-      constexpr int kEl = kIsF32 ? 4 : 2;
-      for (long long s = s0; s < s1; s += steps - s % steps) {
-        const int col = static_cast<int>(s / steps) * S::kCols;
-        for (int i = tid - (kConsumers + 64); i < a.M * a.rank; i += 64) {
-          const int ad = tb.adapter[i / a.rank];
-          if (ad < 0) continue;
-          const uint8_t* p = static_cast<const uint8_t*>(a.B) +
-                             ((static_cast<int64_t>(ad) * a.rank + i % a.rank) * a.N + col) * kEl;
-          for (int q = 0; q < S::kCols * kEl; q += 128)
-            if (col * kEl + q < a.N * kEl)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(p + q) : "memory");
-        }
-      }
     }
   } else {
     take_registers<kConsumerRegs>();
     shrink<kIsF32>(a, tb, red, tid);
     grid_arrive(a.bar, tid);
     bool ok = true, have_s = false;
-    // Before the first epilogue: every block's share of S, and the counters.
+    const int ranks = per_slot * kPieceRanks;
+    auto put_s = [&](int m, int r, int ad, float s) {
+      if (ad < 0) return;
+      if (a.scale != nullptr) s *= __ldg(a.scale + ad);
+      if constexpr (kIsF32) {
+        reinterpret_cast<float*>(S_mem)[m * ranks + r] = s;
+      } else {
+        __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(S_mem) + m * ranks + r;
+        const __nv_bfloat16 h = __float2bfloat16_rn(s);
+        *hi = h;
+        // An infinite value has no remainder.
+        hi[(a.M + 7) / 8 * 8 * ranks] =
+            __float2bfloat16_rn(fabsf(s) < INFINITY ? s - __bfloat162float(h) : 0.0f);
+      }
+    };
+    // Before the first adapters' stage and the first epilogue: every block's share of S, and the
+    // counters.
     auto take_s = [&] {
       if (have_s) return;
       have_s = true;
@@ -357,24 +421,26 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       while (per * 2 <= a.slices && per * 2 * n <= kConsumers) per *= 2;
       const int part = per > 1 ? tid / n : 0;
       for (int i = per > 1 ? tid % n : tid; i < n && part < per; i += kConsumers) {
+        const int m = i / a.rank, r = i - m * a.rank, ad = tb.adapter[m];
         float s = 0.0f;
-        if (tb.adapter[i / a.rank] >= 0) {
+        if (ad >= 0) {
 #pragma unroll 8
           for (int q = part; q < a.slices; q += per)
             s += __ldcg(a.part_s + static_cast<int64_t>(q) * n + i);
         }
         if (per > 1) red[part * n + i] = s;
-        else sums[i] = s;
+        else put_s(m, r, ad, s);
       }
       named_bar_sync(kBarConsumers, kConsumers);
-      for (int i = tid; i < n; i += kConsumers) {
-        float s = per > 1 ? 0.0f : sums[i];
-        if (per > 1)
-          for (int q = 0; q < per; ++q) s += red[q * n + i];
-        const int ad = tb.adapter[i / a.rank];
-        sums[i] = ad >= 0 && a.scale != nullptr ? s * __ldg(a.scale + ad) : s;
+      if (per > 1) {
+        if (tid < n) {
+          float s = 0.0f;
+          for (int q = 0; q < per; ++q) s += red[q * n + tid];
+          const int m = tid / a.rank;
+          put_s(m, tid - m * a.rank, tb.adapter[m], s);
+        }
+        named_bar_sync(kBarConsumers, kConsumers);
       }
-      named_bar_sync(kBarConsumers, kConsumers);
     };
     Cursor cur;
     const int first_row = (warp >> 2) * kBoxRows + warp_row<WK>(warp);
@@ -385,24 +451,8 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       const int cb = static_cast<int>(tile);
       Acc<WK, NT> acc;
       acc.zero();
-      // Units [u_begin, u_end) of the tile are this block's, due evenly over its stages.
-      Expand<WK> ex;
-      float2* delta = reinterpret_cast<float2*>(a.delta + static_cast<int64_t>(me) * a.part_floats);
-      const int iters = Expand<WK>::iterations(a.M), chunks = Expand<WK>::chunks(a.rank);
-      auto units_before = [&](int k) {  // whole iterations, so that a place has one block
-        return static_cast<int>(static_cast<long long>(iters) * k / steps) * chunks;
-      };
-      const int u_begin = units_before(k0), u_end = units_before(k1);
-      int u_next = u_begin;
       for (int k = k0; k < k1; ++k) {
-        const int due = u_begin + static_cast<int>(static_cast<long long>(u_end - u_begin) *
-                                                   (k + 1 - k0) / (k1 - k0));
-        if (ex.unit >= 0 || due - u_next > 1) take_s();
-        ex.complete(a, tb, sums, delta, tid);
-        for (; u_next < due; ++u_next) {
-          ex.complete(a, tb, sums, delta, tid);  // more than one unit a stage: one at a time
-          ex.issue(a, tb, u_next, cb * S::kCols, tid);
-        }
+        if (k >= k_steps) take_s();
         if (ok && (!mbar_wait(&tb.full[cur.stage], cur.phase, a.timeout_ns) ||
                    !mbar_wait(&tb.rows_full[cur.stage], cur.phase, a.timeout_ns))) {
           ok = false;
@@ -413,7 +463,13 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
                              static_cast<uint32_t>(warp >> 1) * kBoxBytes;
         const uint8_t* rows = ring.rows + cur.stage * ring.row_bytes;
         const int at = k * 2 * kBoxRows + first_row;
-        if constexpr (kIsF32) {
+        if (k >= k_steps) {
+          expand<WK, NT>(acc, box, warp, lane, tb, S_mem, a.M,
+                         (k - k_steps) * kStagePieces + (warp >> 2) * 4 + (warp & 1) * 2, n_pieces,
+                         per_slot);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
+        } else if constexpr (kIsF32) {
           multiply_f32<NT>(acc, box, warp, lane, rows + first_row * 4, kRowPitch128F32, a.M, at,
                            a.K);
           __syncwarp();
@@ -430,40 +486,49 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         cur.next(ring.stages);
       }
       take_s();
-      ex.complete(a, tb, sums, delta, tid);
       const bool whole = k0 == 0 && k1 == steps;
       float2* mine = reinterpret_cast<float2*>(
           a.part + (static_cast<int64_t>(me) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
+      constexpr int kMine = (P::kCount + kConsumers - 1) / kConsumers;  // places of a row tile
       for (int j = 0; j < NT && 8 * j < a.M; ++j) {
+        float2 extra[kMine];  // loaded before the warps' sums meet
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+          const int i = tid + q * kConsumers;
+          extra[q] = whole ? load_addend<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i))
+                           : make_float2(0.0f, 0.0f);
+        }
         put_tile<WK, NT>(red, acc, j, warp, lane);
         named_bar_sync(kBarConsumers, kConsumers);
-        for (int i = tid; i < P::kCount; i += kConsumers) {
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+          const int i = tid + q * kConsumers;
           float2 v = take_pair<WK>(red, -1, P::row(i), P::col(i));
-          const int place = j * P::kCount + i;  // written by this thread, where it is a unit's
-          const int unit = place / kConsumers * chunks;
-          if (unit >= u_begin && unit < u_end) {
-            const float2 d = delta[place];
-            v.x += d.x;
-            v.y += d.y;
-          }
-          if (whole) finish<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
-          else mine[place] = v;
+          v.x += extra[q].x;
+          v.y += extra[q].y;
+          if (whole) store_y<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
+          else mine[j * P::kCount + i] = v;
         }
         named_bar_sync(kBarConsumers, kConsumers);
       }
       if (!whole) {
         const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
         if (last_to_finish(a.counters + first, last - first + 1, tid, &tb.flag)) {
-          for (int i = tid; i < (a.M + 7) / 8 * P::kCount; i += kConsumers) {
-            float2 v = make_float2(0.0f, 0.0f);
-            for (int b = first; b <= last; ++b) {
-              const float2 p = __ldcg(reinterpret_cast<const float2*>(
-                                          a.part + (static_cast<int64_t>(b) * 2 +
-                                                    (b == first ? 1 : 0)) * a.part_floats) + i);
-              v.x += p.x;
-              v.y += p.y;
+          constexpr int kChunk = 8;
+          const int limit = (a.M + 7) / 8 * P::kCount;
+          for (int i0 = tid; i0 < limit; i0 += kChunk * kConsumers) {
+            float2 v[kChunk];
+#pragma unroll
+            for (int q = 0; q < kChunk; ++q) {
+              const int i = i0 + q * kConsumers;
+              v[q] = load_addend<kIsF32>(a, P::row(i), cb * S::kCols + P::col(i));
             }
-            finish<kIsF32>(a, P::row(i), cb * S::kCols + P::col(i), v);
+            add_shares(v, a.part, a.part_floats, first, last, i0, limit);
+#pragma unroll
+            for (int q = 0; q < kChunk; ++q) {
+              const int i = i0 + q * kConsumers;
+              if (i < limit) store_y<kIsF32>(a, P::row(i), cb * S::kCols + P::col(i), v[q]);
+            }
           }
         }
       }
@@ -495,10 +560,12 @@ int lora_slices(int64_t M, int64_t K) {
 }
 
 template <int WK, int NT>
-cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void* W,
+cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void* W, const void* B,
                        cudaStream_t stream) {
-  CUtensorMap mw;
-  if (!make_stream_map(&mw, W, WK, p.N, p.K, 1)) return cudaErrorInvalidValue;
+  CUtensorMap mw, mb;
+  if (!make_stream_map(&mw, W, WK, p.N, p.K, 1) ||
+      !make_stream_map(&mb, B, WK, p.N, p.rank, p.adapters, kPieceRanks))
+    return cudaErrorInvalidValue;
   auto kernel = lora_few_kernel<WK, NT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kMaxSmem));
@@ -513,7 +580,7 @@ cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void*
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, mw, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, mw, mb, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -522,7 +589,7 @@ cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void*
 size_t lora_few_workspace_bytes(const moe_lora_problem& p) {
   return up256(sizeof(float) * lora_slices(p.M, p.K) * p.M * p.rank) +
          up256(sizeof(int) * kMaxGrid) +
-         up256(sizeof(float) * 3 * kMaxGrid * lora_part_floats(p.M));
+         up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(p.M));
 }
 
 cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, void* scratch,
@@ -530,7 +597,6 @@ cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, voi
   LoraArgs a{};
   a.X = t.X;
   a.A = t.A;
-  a.B = t.B;
   a.scale = t.scale;
   a.adapter = t.adapter;
   a.addend = t.addend;
@@ -544,7 +610,6 @@ cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, voi
   w += up256(sizeof(int) * kMaxGrid);
   a.part = reinterpret_cast<float*>(w);
   a.part_floats = lora_part_floats(p.M);
-  a.delta = a.part + 2 * kMaxGrid * a.part_floats;
   a.bar = bar;
   a.err = err;
   a.timeout_ns = timeout_ns;
@@ -555,17 +620,17 @@ cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, voi
   a.rank = p.rank;
   const int nt = (a.M + 7) / 8;
   if (p.dtype == MOE_DTYPE_F32) {
-    if (nt == 1) return launch_few<kF32, 1>(p, a, t.W, stream);
-    if (nt == 2) return launch_few<kF32, 2>(p, a, t.W, stream);
-    if (nt <= 4) return launch_few<kF32, 4>(p, a, t.W, stream);
-    return launch_few<kF32, 8>(p, a, t.W, stream);
+    if (nt == 1) return launch_few<kF32, 1>(p, a, t.W, t.B, stream);
+    if (nt == 2) return launch_few<kF32, 2>(p, a, t.W, t.B, stream);
+    if (nt <= 4) return launch_few<kF32, 4>(p, a, t.W, t.B, stream);
+    return launch_few<kF32, 8>(p, a, t.W, t.B, stream);
   }
-  if (nt == 1) return launch_few<kBF16, 1>(p, a, t.W, stream);
-  if (nt == 2) return launch_few<kBF16, 2>(p, a, t.W, stream);
-  if (nt == 3) return launch_few<kBF16, 3>(p, a, t.W, stream);
-  if (nt == 4) return launch_few<kBF16, 4>(p, a, t.W, stream);
-  if (nt <= 6) return launch_few<kBF16, 6>(p, a, t.W, stream);
-  return launch_few<kBF16, 8>(p, a, t.W, stream);
+  if (nt == 1) return launch_few<kBF16, 1>(p, a, t.W, t.B, stream);
+  if (nt == 2) return launch_few<kBF16, 2>(p, a, t.W, t.B, stream);
+  if (nt == 3) return launch_few<kBF16, 3>(p, a, t.W, t.B, stream);
+  if (nt == 4) return launch_few<kBF16, 4>(p, a, t.W, t.B, stream);
+  if (nt <= 6) return launch_few<kBF16, 6>(p, a, t.W, t.B, stream);
+  return launch_few<kBF16, 8>(p, a, t.W, t.B, stream);
 }
 
 }  // namespace moe

@@ -14,7 +14,9 @@
 //     with rows loaded by the consumers: 192 KB in flight 506 us, 128 KB 455, 96 KB 423, 64 KB
 //     463);
 //   - the activation rows of a stage come through the same ring, fetched once per block by a
-//     second producer warp, so that the consumers never wait for an L2 access.
+//     second producer warp, so that the consumers never wait for an L2 access. It copies them
+//     16 bytes per lane (cp.async): one bulk copy per row took about 110 cycles of the warp,
+//     more than a stage's 1424 cycles of HBM time from 13 rows on.
 // 16-bit weights [k][n] (n contiguous) become the row operand of mma.m16n8k16 through transposed
 // ldmatrix (16 output columns x 16 k per instruction), the activation rows its 8 columns: one
 // instruction per 512 bytes of weights and 8 rows, far from the tensor cores' limit, where the
@@ -448,6 +450,28 @@ __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid,
   return last;
 }
 
+// v[c] += the shares that blocks first..last hold of place i0 + c * kConsumers (< limit), in block
+// order. `part`: [grid][2][part_floats]; a tile's first block holds its share in the second
+// half. All loads of one block are independent: one L2 latency per block, not per value.
+template <int C>
+__device__ __forceinline__ void add_shares(float2 (&v)[C], const float* part, int64_t part_floats,
+                                           int first, int last, int i0, int limit) {
+  for (int b = first; b <= last; ++b) {
+    const float2* p = reinterpret_cast<const float2*>(
+        part + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * part_floats);
+    float2 w[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      w[c] = i0 + c * kConsumers < limit ? __ldcg(p + i0 + c * kConsumers)
+                                         : make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      v[c].x += w[c].x;
+      v[c].y += w[c].y;
+    }
+  }
+}
+
 // Weight producer, before it fills the stage at `c` (the issued-th overall): the stage is free
 // and at most kInFlight - 1 earlier ones are still under way; then announce its bytes.
 __device__ __forceinline__ bool acquire_weights(const Ring& ring, const Cursor& c,
@@ -482,6 +506,17 @@ __device__ __forceinline__ void drain(uint64_t* full, int stages, const Cursor& 
   }
 }
 
+// A lane's 16 bytes global -> shared, and its arrival on `bar` (initialised for 32 lanes) once its
+// copies so far have landed.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
 // Generic-proxy writes of global memory before bulk copies of it, and the other way round.
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
@@ -494,8 +529,8 @@ __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
 }  // namespace stream
 
 // 3-D map over stacked weights [count][rows][cols] (cols contiguous) of a stream::WeightKind in
-// boxes of 64 rows x 128 bytes, 128-byte swizzle; elements past the edges read as zero.
+// boxes of box_rows rows x 128 bytes, 128-byte swizzle; elements past the edges read as zero.
 bool make_stream_map(CUtensorMap* m, const void* ptr, int kind, uint64_t cols, uint64_t rows,
-                     uint64_t count);
+                     uint64_t count, uint32_t box_rows = stream::kBoxRows);
 
 }  // namespace moe
