@@ -86,7 +86,8 @@ int* sched_of(int* header) { return header + kSchedInt; }
 constexpr int kDispatchBarInt = 20;
 int* dispatch_bar_of(int* header) { return header + kDispatchBarInt; }
 
-// Ints 24 and 25: moe_forward_few's and moe_lora_forward's grid-barrier arrivals and finished count (zero at rest).
+// Ints 24 to 26: moe_forward_few's and moe_lora_forward's grid-barrier arrivals and finished
+// counts (zero at rest).
 constexpr int kFewBarInt = 24;
 int* few_bar_of(int* header) { return header + kFewBarInt; }
 

@@ -108,7 +108,7 @@ constexpr size_t out_bytes(int N, int E) {
 constexpr size_t kMaxSmem = 232448;
 template <int WK>
 __host__ __device__ constexpr size_t ring_bytes(int N, int E) {
-  return (kMaxSmem - 1024 - sizeof(float) * kRedFloats - out_bytes<WK>(N, E) - sizeof(Tables)) &
+  return (kMaxSmem - 1024 - kRedBytes - out_bytes<WK>(N, E) - sizeof(Tables)) &
          ~size_t(1023);
 }
 __host__ __device__ constexpr int ring_stages(size_t bytes, int row_tiles) {
@@ -375,7 +375,7 @@ __device__ void export_routing(const FewArgs& a, const Tables& tb, const float* 
 struct Consumer {
   Ring ring;
   Cursor cur;
-  float* red;
+  RedTurn red;
   int tid, warp, lane;
   bool ok;
   uint64_t timeout_ns;
@@ -460,7 +460,7 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
     c.wait_full();
     const int d0 = s * kBoxRows + first_row;
     if constexpr (WK == kF32) {
-      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, c.rows() + first_row * 4, kRowPitchF32,
+      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, smem_u32(c.rows()) + first_row * 4, kRowPitchF32,
                        pt.n, d0, a.D);
       c.release();
     } else {
@@ -478,11 +478,12 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
   float2* mine = reinterpret_cast<float2*>(
       a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
-    put_tile<WK, NT>(c.red, acc, j, c.warp, c.lane);
+    float* red = c.red.next();
+    put_tile<WK, NT>(red, acc, j, c.warp, c.lane);
     named_bar_sync(kBarConsumers, kConsumers);
     for (int i = c.tid; i < P::kCount; i += kConsumers) {
-      const float2 h1 = take_pair<WK>(c.red, 0, P::row(i), P::col(i));
-      const float2 h2 = take_pair<WK>(c.red, 1, P::row(i), P::col(i));
+      const float2 h1 = take_pair<WK>(red, 0, P::row(i), P::col(i));
+      const float2 h2 = take_pair<WK>(red, 1, P::row(i), P::col(i));
       if (whole) {
         finish_h<WK>(a, tb, pt, 8 * j + P::row(i), fb * S::kCols + P::col(i), h1, h2);
       } else {
@@ -490,7 +491,6 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
         mine[(2 * j + 1) * P::kCount + i] = h2;
       }
     }
-    named_bar_sync(kBarConsumers, kConsumers);
   }
   if (whole) return;
   const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
@@ -528,7 +528,7 @@ __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer&
   for (int s = s0; s < s1; ++s) {
     c.wait_full();
     if constexpr (WK == kF32) {
-      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, c.rows() + first_row * 4,
+      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, smem_u32(c.rows()) + first_row * 4,
                        2 * kBoxRows * 4, pt.n, s * 2 * kBoxRows + first_row, a.F);
       c.release();
     } else {
@@ -541,12 +541,13 @@ __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer&
     }
   }
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
-    put_tile<WK, NT>(c.red, acc, j, c.warp, c.lane);
+    float* red = c.red.next();
+    put_tile<WK, NT>(red, acc, j, c.warp, c.lane);
     named_bar_sync(kBarConsumers, kConsumers);
     for (int i = c.tid; i < P::kCount; i += kConsumers) {
       const int r = 8 * j + P::row(i);
       if (r >= pt.n) continue;
-      float2 v = take_pair<WK>(c.red, -1, P::row(i), P::col(i));
+      float2 v = take_pair<WK>(red, -1, P::row(i), P::col(i));
       if constexpr (WK == kW8) {
         const int d = cb * S::kCols + P::col(i);
         if (d < a.D) {
@@ -561,7 +562,6 @@ __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer&
       o->x += v.x;
       o->y += v.y;
     }
-    named_bar_sync(kBarConsumers, kConsumers);
   }
 }
 
@@ -596,7 +596,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const size_t ring_size = ring_bytes<WK>(a.N, a.E);
   float* red = reinterpret_cast<float*>(smem + ring_size);
-  float* outacc = red + kRedFloats;  // the logits first, then the column block's sums
+  float* outacc = red + 2 * kRedFloats;  // the logits first, then the column block's sums
   Tables& tb = *reinterpret_cast<Tables*>(reinterpret_cast<uint8_t*>(outacc) +
                                           out_bytes<WK>(a.N, a.E));
   const int tid = static_cast<int>(threadIdx.x);
@@ -797,7 +797,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
         for (int i = tid; i < a.N * P::kPairs; i += kConsumers)
           store_out<WK>(a, P::row(i), cb * S::kCols + P::col(i), make_float2(0.0f, 0.0f));
     }
-    Consumer c{ring, Cursor{}, red, tid, warp, lane, ok, a.timeout_ns, a.err};
+    Consumer c{ring, Cursor{}, RedTurn{red}, tid, warp, lane, ok, a.timeout_ns, a.err};
     for (long long s = u0; s < u1;) {
       const long long tile = s / up_steps;
       const int k0 = static_cast<int>(s - tile * up_steps);
@@ -830,6 +830,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
 #undef MOE_DOWN
         k += s1 - s0;
       }
+      named_bar_sync(kBarConsumers, kConsumers);  // the last sums are in
       const bool whole = k0 == 0 && k1 == down_steps;
       float2* mine = reinterpret_cast<float2*>(
           a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);

@@ -152,7 +152,7 @@ cudaError_t launch_combine(const moe_problem& p, const void* Y, const int32_t* i
 
 // The whole layer for at most kFewMaxTokens tokens in one cooperative launch (few.cu). W1..W3:
 // fp32 or bf16 weights, or int8 ones when S1..S3 are given; every pointer from `logits` on may
-// be NULL. scratch: few_workspace_bytes(p) bytes, 256-byte aligned; bar: two ints of the
+// be NULL. scratch: few_workspace_bytes(p) bytes, 256-byte aligned; bar: three ints of the
 // workspace header, zero at rest (returned to zero by the kernel).
 constexpr int64_t kFewMaxTokens = 64;
 struct FewTensors {

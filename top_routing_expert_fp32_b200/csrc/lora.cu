@@ -5,16 +5,15 @@
 // What bounds it: one pass over W (and over the used adapters). W runs through the ring of
 // stream.cuh in equal shares per block, as the few-token layer's down projection does. The
 // adapters' part hides behind it:
-//   1. Shrink. While the ring fills, the consumers compute S = X A: block (row, slice of K), a
-//      16-byte piece of an A row per thread, fp32 partial sums to L2. The block arrives at the
-//      grid barrier and goes on with W.
+//   1. Shrink. Beside the stream, two warps compute S = X A: block (row, slice of K), a 16-byte
+//      piece of an A row per thread, fp32 partial sums to L2. They arrive at the grid barrier,
+//      wait for it, add everybody's partial sums up in shared memory and tell the consumers.
 //   2. Expand. The different adapters of the batch (slots) follow W in the same ring: a stage
 //      then holds 8 pieces of 16 ranks x the tile's columns of some B[a], and a tile's reduction
 //      is its k-stages and then those. A warp multiplies a piece into fresh registers, for the
 //      row tiles that have the adapter, and adds the sums of those rows only, so that a row
 //      never meets another adapter's values, whatever they hold. S enters as two bf16 terms (16
-//      bits of mantissa; fp32 weights: as it is). The barrier is waited for at the first such
-//      stage. (The rows' expand products on the CUDA cores, row by row out of L2, took longer
+//      bits of mantissa; fp32 weights: as it is). (The rows' expand products on the CUDA cores, row by row out of L2, took longer
 //      than the stream: 48 rows of 48 adapters 71 us.)
 #include <algorithm>
 #include <cstdint>
@@ -42,20 +41,26 @@ struct LoraArgs {
   float* part_s;   // [slices][M][rank]
   float* part;     // [grid][2][part_floats]: sums of shared tiles
   int* counters;   // [kMaxGrid]: arrivals at shared tiles
-  int* bar;        // [2] workspace header ints, zero at rest
+  int* bar;        // [3] workspace header ints, zero at rest: blocks that started, blocks that
+                   // have their partial S out, blocks that finished
   int* err;
   int64_t part_floats;
   uint64_t timeout_ns;
   int M, K, N, L, rank, slices;
 };
 
+constexpr int kSideThreads = 64;  // the two warps that compute S
+
 struct LoraTables {
   uint64_t full[kMaxStages];
   uint64_t rows_full[kMaxStages];
   uint64_t empty[kMaxStages];
+  uint64_t s_ready;              // S is complete, the grid barrier passed
+  float scratch[kSideThreads * 8];
   uint64_t slot_rows[kMaxRows];  // rows of each slot's adapter
   int slot[kMaxRows];            // the batch's different adapters
   int adapter[kMaxRows];         // of each row; -1: none
+  float scale[kMaxRows];         // and its scale
   uint32_t firsts[2];
   int flag;
 };
@@ -72,7 +77,7 @@ __host__ __device__ constexpr size_t s_bytes(int M, int rank) {
   return sizeof(float) * static_cast<size_t>((M + 7) / 8 * 8) * pieces_of(rank) * kPieceRanks;
 }
 __host__ __device__ constexpr size_t lora_ring_bytes(int M, int rank) {
-  return (kMaxSmem - 1024 - sizeof(float) * kRedFloats - s_bytes(M, rank) - sizeof(LoraTables)) &
+  return (kMaxSmem - 1024 - kRedBytes - s_bytes(M, rank) - sizeof(LoraTables)) &
          ~size_t(1023);
 }
 // A stage's rows, whole tiles of 8.
@@ -104,41 +109,102 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
   }
 }
 
-// This block's partial S: row blockIdx.x % M over one slice of K. kVec values of a row of A per
-// thread (16 bytes).
+// The side warps' partial S of this block: row blockIdx.x % M over one slice of K; kVec values of
+// a row of A per thread (16 bytes).
 template <bool F32>
-__device__ void shrink(const LoraArgs& a, const LoraTables& tb, float* red, int tid) {
+__device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid) {
   constexpr int kVec = F32 ? 4 : 8;
   const int m = static_cast<int>(blockIdx.x) % a.M, slice = static_cast<int>(blockIdx.x) / a.M;
   if (slice >= a.slices) return;
   const int ad = tb.adapter[m];
   if (ad < 0) return;  // nobody reads this row's sums
-  const int per_row = a.rank / kVec, subs = kConsumers / per_row;
+  const int per_row = a.rank / kVec, subs = kSideThreads / per_row;
   const int chunk = (a.K + a.slices - 1) / a.slices;
   const int k0 = min(a.K, slice * chunk), k1 = min(a.K, k0 + chunk);
-  const int v = tid % per_row, sub = tid / per_row;
+  const int v = sid % per_row, sub = sid / per_row;
   float acc[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
   if (sub < subs) {
-#pragma unroll 4
+    const int64_t x0 = static_cast<int64_t>(m) * a.K;
+    const int64_t a0 = static_cast<int64_t>(ad) * a.K * a.rank + v * kVec;
+#pragma unroll 8
     for (int k = k0 + sub; k < k1; k += subs) {
-      const int64_t at = static_cast<int64_t>(m) * a.K + k;
-      const float x = F32 ? __ldg(static_cast<const float*>(a.X) + at)
-                          : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[at]);
+      const float x = F32 ? __ldg(static_cast<const float*>(a.X) + x0 + k)
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[x0 + k]);
       float w[8];
-      load8<F32>(a.A, (static_cast<int64_t>(ad) * a.K + k) * a.rank + v * kVec, w);
+      load8<F32>(a.A, a0 + static_cast<int64_t>(k) * a.rank, w);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) acc[i] = fmaf(x, w[i], acc[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) red[sub * a.rank + v * kVec + i] = acc[i];
+    for (int i = 0; i < kVec; ++i) tb.scratch[sub * a.rank + v * kVec + i] = acc[i];
   }
-  named_bar_sync(kBarConsumers, kConsumers);
-  if (tid < a.rank) {
+  named_bar_sync(kBarSide, kSideThreads);
+  for (int r = sid; r < a.rank; r += kSideThreads) {
     float s = 0.0f;
-    for (int q = 0; q < subs; ++q) s += red[q * a.rank + tid];
-    a.part_s[(static_cast<int64_t>(slice) * a.M + m) * a.rank + tid] = s;
+    for (int q = 0; q < subs; ++q) s += tb.scratch[q * a.rank + r];
+    a.part_s[(static_cast<int64_t>(slice) * a.M + m) * a.rank + r] = s;
+  }
+}
+
+// S of one row and rank, scaled, as the expand reads it.
+template <bool F32>
+__device__ __forceinline__ void put_s(const LoraArgs& a, const LoraTables& tb, uint8_t* S, int i,
+                                      float s) {
+  const int m = i / a.rank, r = i - m * a.rank, ad = tb.adapter[m];
+  const int at = m * pieces_of(a.rank) * kPieceRanks + r;
+  if (ad < 0) return;
+  s *= tb.scale[m];
+  if constexpr (F32) {
+    reinterpret_cast<float*>(S)[at] = s;
+  } else {
+    __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(S) + at;
+    const __nv_bfloat16 h = __float2bfloat16_rn(s);
+    *hi = h;
+    // An infinite value has no remainder.
+    hi[(a.M + 7) / 8 * 8 * pieces_of(a.rank) * kPieceRanks] =
+        __float2bfloat16_rn(fabsf(s) < INFINITY ? s - __bfloat162float(h) : 0.0f);
+  }
+}
+
+// The side warps, after the grid barrier: all of S from everybody's partial sums.
+template <bool F32>
+__device__ void gather_s(const LoraArgs& a, LoraTables& tb, uint8_t* S, int sid) {
+  const int n = a.M * a.rank;
+  int per = 1;  // threads per value, over the slices
+  while (per * 2 <= a.slices && per * 2 * n <= kSideThreads) per *= 2;
+  if (per > 1) {
+    float s = 0.0f;
+    const int i = sid % n, part = sid / n;
+    if (part < per) {
+#pragma unroll 8
+      for (int q = part; q < a.slices; q += per)
+        s += __ldcg(a.part_s + static_cast<int64_t>(q) * n + i);
+      tb.scratch[part * n + i] = s;
+    }
+    named_bar_sync(kBarSide, kSideThreads);
+    if (sid < n) {
+      s = 0.0f;
+      for (int q = 0; q < per; ++q) s += tb.scratch[q * n + sid];
+      put_s<F32>(a, tb, S, sid, s);
+    }
+    return;
+  }
+  constexpr int kAtOnce = 4;
+  for (int i0 = sid; i0 < n; i0 += kAtOnce * kSideThreads) {
+    float s[kAtOnce] = {};
+#pragma unroll 8
+    for (int q = 0; q < a.slices; ++q) {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int i = i0 + u * kSideThreads;
+        if (i < n) s[u] += __ldcg(a.part_s + static_cast<int64_t>(q) * n + i);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (i0 + u * kSideThreads < n) put_s<F32>(a, tb, S, i0 + u * kSideThreads, s[u]);
   }
 }
 
@@ -245,7 +311,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* red = reinterpret_cast<float*>(smem + lora_ring_bytes(a.M, a.rank));
-  uint8_t* S_mem = reinterpret_cast<uint8_t*>(red + kRedFloats);  // S, scaled
+  uint8_t* S_mem = reinterpret_cast<uint8_t*>(red + 2 * kRedFloats);  // S, scaled
   LoraTables& tb = *reinterpret_cast<LoraTables*>(S_mem + s_bytes(a.M, a.rank));
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
@@ -266,8 +332,13 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       mbar_init(&tb.rows_full[i], 32);  // the row producer's lanes
       mbar_init(&tb.empty[i], kConsumerWarps);
     }
+    mbar_init(&tb.s_ready, kSideThreads);
     fence_barrier_init();
-    a.counters[me] = 0;  // seen by the others after the grid barrier
+    // This block's counter, and word that it is zero: blocks wait for that before they share a
+    // tile, by which time all have long started.
+    a.counters[me] = 0;
+    __threadfence();
+    atomicAdd(&a.bar[0], 1);
   }
   {  // The rows' adapters, and the batch's different ones by first appearance.
     const int m = tid - kConsumers;
@@ -279,7 +350,10 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         ad = -1;
       }
     }
-    if (m >= 0 && m < kMaxRows) tb.adapter[m] = ad;
+    if (m >= 0 && m < kMaxRows) {
+      tb.adapter[m] = ad;
+      tb.scale[m] = ad >= 0 && a.scale != nullptr ? a.scale[ad] : 1.0f;
+    }
     __syncthreads();
     uint64_t rows = 0;
     if (ad >= 0)
@@ -308,17 +382,29 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   sp.grid = static_cast<int>(min(static_cast<long long>(G), sp.total));
   const long long s0 = me < sp.grid ? sp.start(me) : 0, s1 = me < sp.grid ? sp.start(me + 1) : 0;
 
-  // The block's stages in order: f(column tile, k-stage), until it returns false. (Divisions per
-  // tile only: a 64-bit one per stage cost the producer more than a stage's HBM time.)
-  auto walk = [&](auto f) {
-    for (long long s = s0; s < s1;) {
-      const long long tile = s / steps;
-      int k = static_cast<int>(s - tile * steps);
-      const int k_end = static_cast<int>(min(static_cast<long long>(steps), k + (s1 - s)));
-      s += k_end - k;
-      for (; k < k_end; ++k)
-        if (!f(static_cast<int>(tile), k)) return;
+  // The block's segments (a tile and its stages [k0, k1)) in order, the first one last: it is a
+  // tile's end, whose adapters' stages need S, and S takes a while. f returns false to stop.
+  // (Divisions per segment only: a 64-bit one per stage cost more than the stage's HBM time.)
+  auto segments = [&](auto f) {
+    if (s0 >= s1) return;
+    const long long head = min(s1, (s0 / steps + 1) * steps);  // end of the first segment
+    long long s = head;
+    while (true) {
+      const bool last = s >= s1;
+      const long long from = last ? s0 : s, tile = from / steps;
+      const long long to = last ? head : min(s1, (tile + 1) * steps);
+      if (!f(static_cast<int>(tile), static_cast<int>(from - tile * steps),
+             static_cast<int>(to - tile * steps)) || last)
+        return;
+      s = to;
     }
+  };
+  auto walk = [&](auto f) {
+    segments([&](int tile, int k0, int k1) {
+      for (int k = k0; k < k1; ++k)
+        if (!f(tile, k)) return false;
+      return true;
+    });
   };
 
   if (warp >= kConsumerWarps) {
@@ -337,13 +423,17 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
           if (k >= k_steps) {
             // 16 rows of each box per piece; the last stage's unused ones repeat the last piece,
             // so that every stage has the same bytes.
-            int piece = (k - k_steps) * kStagePieces;
-            for (int j = 0; j < kStagePieces; ++j, ++piece) {
-              const int p = min(piece, n_pieces - 1), slot = p / per_slot;
+            const int piece = (k - k_steps) * kStagePieces;
+            int slot = piece / per_slot, part = piece - slot * per_slot;
+            for (int j = 0; j < kStagePieces; ++j) {
               uint8_t* d = dst + (j >> 2) * 2 * kBoxBytes + (j & 3) * kPieceRanks * 128;
-              const int r0 = (p - slot * per_slot) * kPieceRanks, ad = tb.slot[slot];
+              const int r0 = part * kPieceRanks, ad = tb.slot[slot];
               tma_load_3d_hint(d, &mb, bar, col, r0, ad, policy);
               tma_load_3d_hint(d + kBoxBytes, &mb, bar, col + S::kBoxCols, r0, ad, policy);
+              if (piece + j + 1 < n_pieces && ++part == per_slot) {
+                part = 0;
+                ++slot;
+              }
             }
             c.next(ring.stages);
             ++issued;
@@ -389,66 +479,36 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       if (!good && lane == 0) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
       drain(tb.rows_full, ring.stages, c, issued, a.timeout_ns);
       __syncwarp();
+    } else {
+      // The side warps: S.
+      const int sid = tid - (kConsumers + 64);
+      shrink<kIsF32>(a, tb, sid);
+      named_bar_sync(kBarSide, kSideThreads);
+      if (sid == 0) {
+        __threadfence();
+        atomicAdd(&a.bar[1], 1);
+        (void)spin_until(&a.bar[1], G, a.timeout_ns, a.err);
+      }
+      named_bar_sync(kBarSide, kSideThreads);
+      gather_s<kIsF32>(a, tb, S_mem, sid);
+      mbar_arrive(&tb.s_ready);
     }
   } else {
     take_registers<kConsumerRegs>();
-    shrink<kIsF32>(a, tb, red, tid);
-    grid_arrive(a.bar, tid);
-    bool ok = true, have_s = false;
-    const int ranks = per_slot * kPieceRanks;
-    auto put_s = [&](int m, int r, int ad, float s) {
-      if (ad < 0) return;
-      if (a.scale != nullptr) s *= __ldg(a.scale + ad);
-      if constexpr (kIsF32) {
-        reinterpret_cast<float*>(S_mem)[m * ranks + r] = s;
-      } else {
-        __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(S_mem) + m * ranks + r;
-        const __nv_bfloat16 h = __float2bfloat16_rn(s);
-        *hi = h;
-        // An infinite value has no remainder.
-        hi[(a.M + 7) / 8 * 8 * ranks] =
-            __float2bfloat16_rn(fabsf(s) < INFINITY ? s - __bfloat162float(h) : 0.0f);
-      }
-    };
-    // Before the first adapters' stage and the first epilogue: every block's share of S, and the
-    // counters.
+    bool ok = true, have_s = false, all_started = false;
+    // Before the first adapters' stage: S.
     auto take_s = [&] {
       if (have_s) return;
       have_s = true;
-      if (!grid_wait(a.bar, G, tid, &tb.flag, a.timeout_ns, a.err)) ok = false;
-      const int n = a.M * a.rank;
-      int per = 1;  // threads per value, over the slices
-      while (per * 2 <= a.slices && per * 2 * n <= kConsumers) per *= 2;
-      const int part = per > 1 ? tid / n : 0;
-      for (int i = per > 1 ? tid % n : tid; i < n && part < per; i += kConsumers) {
-        const int m = i / a.rank, r = i - m * a.rank, ad = tb.adapter[m];
-        float s = 0.0f;
-        if (ad >= 0) {
-#pragma unroll 8
-          for (int q = part; q < a.slices; q += per)
-            s += __ldcg(a.part_s + static_cast<int64_t>(q) * n + i);
-        }
-        if (per > 1) red[part * n + i] = s;
-        else put_s(m, r, ad, s);
-      }
-      named_bar_sync(kBarConsumers, kConsumers);
-      if (per > 1) {
-        if (tid < n) {
-          float s = 0.0f;
-          for (int q = 0; q < per; ++q) s += red[q * n + tid];
-          const int m = tid / a.rank;
-          put_s(m, tid - m * a.rank, tb.adapter[m], s);
-        }
-        named_bar_sync(kBarConsumers, kConsumers);
+      if (ok && !mbar_wait(&tb.s_ready, 0, a.timeout_ns)) {
+        ok = false;
+        record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
       }
     };
+    RedTurn turn{red};
     Cursor cur;
     const int first_row = (warp >> 2) * kBoxRows + warp_row<WK>(warp);
-    for (long long s = s0; s < s1;) {
-      const long long tile = s / steps;
-      const int k0 = static_cast<int>(s - tile * steps);
-      const int k1 = static_cast<int>(min(static_cast<long long>(steps), k0 + (s1 - s)));
-      const int cb = static_cast<int>(tile);
+    segments([&](int cb, int k0, int k1) {
       Acc<WK, NT> acc;
       acc.zero();
       for (int k = k0; k < k1; ++k) {
@@ -470,7 +530,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
           __syncwarp();
           if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
         } else if constexpr (kIsF32) {
-          multiply_f32<NT>(acc, box, warp, lane, rows + first_row * 4, kRowPitch128F32, a.M, at,
+          multiply_f32<NT>(acc, box, warp, lane, smem_u32(rows) + first_row * 4, kRowPitch128F32, a.M, at,
                            a.K);
           __syncwarp();
           if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
@@ -485,12 +545,13 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         }
         cur.next(ring.stages);
       }
-      take_s();
       const bool whole = k0 == 0 && k1 == steps;
       float2* mine = reinterpret_cast<float2*>(
           a.part + (static_cast<int64_t>(me) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
       constexpr int kMine = (P::kCount + kConsumers - 1) / kConsumers;  // places of a row tile
-      for (int j = 0; j < NT && 8 * j < a.M; ++j) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (8 * j >= a.M) break;
         float2 extra[kMine];  // loaded before the warps' sums meet
 #pragma unroll
         for (int q = 0; q < kMine; ++q) {
@@ -498,21 +559,24 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
           extra[q] = whole ? load_addend<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i))
                            : make_float2(0.0f, 0.0f);
         }
-        put_tile<WK, NT>(red, acc, j, warp, lane);
+        float* sums = turn.next();
+        put_tile<WK, NT>(sums, acc, j, warp, lane);
         named_bar_sync(kBarConsumers, kConsumers);
 #pragma unroll
         for (int q = 0; q < kMine; ++q) {
           const int i = tid + q * kConsumers;
-          float2 v = take_pair<WK>(red, -1, P::row(i), P::col(i));
+          float2 v = take_pair<WK>(sums, -1, P::row(i), P::col(i));
           v.x += extra[q].x;
           v.y += extra[q].y;
           if (whole) store_y<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
           else mine[j * P::kCount + i] = v;
         }
-        named_bar_sync(kBarConsumers, kConsumers);
       }
       if (!whole) {
-        const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
+        const long long at = static_cast<long long>(cb) * steps;
+        const int first = sp.owner(at), last = sp.owner(at + steps - 1);
+        if (!all_started && tid == 0) (void)spin_until(&a.bar[0], G, a.timeout_ns, a.err);
+        all_started = true;  // (thread 0 counts the arrivals)
         if (last_to_finish(a.counters + first, last - first + 1, tid, &tb.flag)) {
           constexpr int kChunk = 8;
           const int limit = (a.M + 7) / 8 * P::kCount;
@@ -532,18 +596,18 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
           }
         }
       }
-      s += k1 - k0;
-    }
-    take_s();  // every block waits for the barrier, so that the counters may return to zero
+      return true;
+    });
   }
 
   // The last block out returns the barrier counters to zero for the next launch.
   __syncthreads();
   if (tid == 0) {
     __threadfence();
-    if (atomicAdd(&a.bar[1], 1) == G - 1) {
+    if (atomicAdd(&a.bar[2], 1) == G - 1) {
       atomicExch(&a.bar[0], 0);
       atomicExch(&a.bar[1], 0);
+      atomicExch(&a.bar[2], 0);
     }
   }
 }

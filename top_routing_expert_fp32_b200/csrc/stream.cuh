@@ -58,7 +58,7 @@ constexpr int kRowPitch = 144, kRowPitchF32 = 256;
 constexpr int kMaxRows = 64;     // activation rows of one call
 constexpr int kTileRows = 32;    // activation rows of one product (up to four tiles of 8)
 constexpr int kMaxGrid = 148;    // blocks (one per SM)
-constexpr int kBarConsumers = 1, kBarAll = 2, kBarRows = 3;  // named barriers
+constexpr int kBarConsumers = 1, kBarAll = 2, kBarRows = 3, kBarSide = 4;  // named barriers
 
 // A stage is four boxes: two side by side (kCols output columns) times either two matrices with
 // the same 64 k-rows, or 128 k-rows of one matrix. Warp w takes box w/2; for 16- and 32-bit
@@ -296,11 +296,21 @@ __device__ __forceinline__ void multiply(Acc<WK, NT>& acc, const Weights<WK>& w,
   }
 }
 
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // fp32 weights on the CUDA cores: acc.v[r] += sum over the warp's 32 k-rows of W[k][lane] x_r[k].
-// `rows`: the stage's rows at this warp's first k, pitch bytes apart; k0: that k within K.
+// `rows`: shared address of the stage's rows at this warp's first k, pitch bytes apart; k0: that k
+// within K.
 template <int NT>
 __device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, int warp, int lane,
-                                             const uint8_t* rows, int pitch, int n_rows, int k0,
+                                             uint32_t rows, int pitch, int n_rows, int k0,
                                              int K) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -313,30 +323,48 @@ __device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, i
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at) : "memory");
     }
 #pragma unroll
-    for (int r = 0; r < 8 * NT; ++r) {
-      if (r < n_rows) {
-        const float* x = reinterpret_cast<const float*>(rows + r * pitch) + h * 16;
-        float s = 0.0f;  // 16 terms on their own: short chains keep the rounding error low
+    for (int j = 0; j < NT; ++j) {
+      if (8 * j >= n_rows) continue;
+      // Eight rows at a time, 16 terms on their own: independent chains, and short ones, which
+      // keep the rounding error low. (Rows past the last are read from the ring and dropped.)
+      float s[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (k0 + h * 16 + 4 * q < K) {
-            const float4 v = *reinterpret_cast<const float4*>(x + 4 * q);
-            s = fmaf(w[4 * q], v.x, s);
-            s = fmaf(w[4 * q + 1], v.y, s);
-            s = fmaf(w[4 * q + 2], v.z, s);
-            s = fmaf(w[4 * q + 3], v.w, s);
+      for (int r = 0; r < 8; ++r) s[r] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (k0 + h * 16 + 4 * q < K) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float4 v = ld_shared_f4(rows + (8 * j + r) * static_cast<uint32_t>(pitch) +
+                                          h * 64 + q * 16);
+            s[r] = fmaf(w[4 * q], v.x, s[r]);
+            s[r] = fmaf(w[4 * q + 1], v.y, s[r]);
+            s[r] = fmaf(w[4 * q + 2], v.z, s[r]);
+            s[r] = fmaf(w[4 * q + 3], v.w, s[r]);
           }
         }
-        acc.v[r] += s;
       }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) acc.v[8 * j + r] += s[r];
     }
   }
 }
 
 // The warps' sums of one row tile meet in shared memory: red[warp][8 rows][kRedPitch]. The
 // pitch keeps both the fragment-shaped writes and the row-shaped reads free of bank conflicts.
+// Two such buffers in turn (RedTurn): one barrier per row tile, since a thread that writes a
+// buffer again has passed the barrier of the other one, and with it every read of this one.
 constexpr int kRedPitch = 68;
 constexpr int kRedFloats = kConsumerWarps * 8 * kRedPitch;
+constexpr size_t kRedBytes = 2 * sizeof(float) * kRedFloats;
+struct RedTurn {
+  float* base;
+  int turn = 0;
+  __device__ float* next() {
+    turn ^= 1;
+    return base + turn * kRedFloats;
+  }
+};
 
 template <int WK, int NT>
 __device__ __forceinline__ void put_tile(float* red, const Acc<WK, NT>& acc, int j, int warp,
@@ -395,44 +423,34 @@ __device__ __forceinline__ float2 take_pair(const float* red, int branch, int ro
   return s;
 }
 
-// All consumer threads of a block: wait until `target` blocks have arrived at *bar (bounded).
-// What they wrote before is visible afterwards. False: the wait ran out.
-__device__ __forceinline__ bool grid_wait(int* bar, int target, int tid, int* flag,
-                                          uint64_t timeout_ns, int* err) {
-  named_bar_sync(kBarConsumers, kConsumers);
-  if (tid == 0) {
-    int ok = 1;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-      int v;
-      asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
-      if (v >= target) break;
-      if (globaltimer_ns() - t0 > timeout_ns) {
-        ok = 0;
-        record_error(err, MOE_DEVERR_WAIT_TIMEOUT);
-        break;
-      }
+// One thread: wait until `target` blocks have arrived at *bar (bounded).
+__device__ __forceinline__ bool spin_until(int* bar, int target, uint64_t timeout_ns, int* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
+    if (v >= target) break;
+    if (globaltimer_ns() - t0 > timeout_ns) {
+      record_error(err, MOE_DEVERR_WAIT_TIMEOUT);
+      return false;
     }
-    __threadfence();
-    *flag = ok;
   }
-  named_bar_sync(kBarConsumers, kConsumers);
-  return *flag != 0;
+  __threadfence();
+  return true;
 }
 
-// The block's writes so far, then its arrival (all consumer threads call it).
-__device__ __forceinline__ void grid_arrive(int* bar, int tid) {
+// All consumer threads of every block: arrive, wait until `target` arrivals (bounded). The
+// block's earlier global writes are visible to the others afterwards. False: the wait ran out.
+__device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int* flag,
+                                             uint64_t timeout_ns, int* err) {
   named_bar_sync(kBarConsumers, kConsumers);
   if (tid == 0) {
     __threadfence();
     atomicAdd(bar, 1);
+    *flag = spin_until(bar, target, timeout_ns, err) ? 1 : 0;
   }
-}
-
-__device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int* flag,
-                                             uint64_t timeout_ns, int* err) {
-  grid_arrive(bar, tid);
-  return grid_wait(bar, target, tid, flag, timeout_ns, err);
+  named_bar_sync(kBarConsumers, kConsumers);
+  return *flag != 0;
 }
 
 // One arrival per block that shares a tile; true in the block that arrives last (its threads
