@@ -387,6 +387,7 @@ struct Consumer {
       ok = false;
       record_error(err, MOE_DEVERR_WAIT_TIMEOUT);
     }
+    __syncwarp();  // the lanes leave the wait one by one; what follows is for whole warps
   }
   __device__ uint32_t my_box() const {
     return smem_u32(ring.weights) + static_cast<uint32_t>(cur.stage) * kStageBytes +

@@ -489,6 +489,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         atomicAdd(&a.bar[1], 1);
         (void)spin_until(&a.bar[1], G, a.timeout_ns, a.err);
       }
+      __syncwarp();
       named_bar_sync(kBarSide, kSideThreads);
       gather_s<kIsF32>(a, tb, S_mem, sid);
       mbar_arrive(&tb.s_ready);
@@ -504,6 +505,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         ok = false;
         record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
       }
+      __syncwarp();
     };
     RedTurn turn{red};
     Cursor cur;
@@ -518,6 +520,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
           ok = false;
           record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
         }
+        __syncwarp();  // the lanes leave the wait one by one; what follows is for whole warps
         const uint32_t box = smem_u32(ring.weights) +
                              static_cast<uint32_t>(cur.stage) * kStageBytes +
                              static_cast<uint32_t>(warp >> 1) * kBoxBytes;
@@ -576,6 +579,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         const long long at = static_cast<long long>(cb) * steps;
         const int first = sp.owner(at), last = sp.owner(at + steps - 1);
         if (!all_started && tid == 0) (void)spin_until(&a.bar[0], G, a.timeout_ns, a.err);
+        __syncwarp();
         all_started = true;  // (thread 0 counts the arrivals)
         if (last_to_finish(a.counters + first, last - first + 1, tid, &tb.flag)) {
           constexpr int kChunk = 8;

@@ -176,6 +176,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
       ok = false;
       record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
     }
+    __syncwarp();  // the lanes leave the wait one by one; what follows is for whole warps
     const int item = q / per_item;
     const uint32_t mask = s_mask[item];
     const uint8_t* at = ring + (q % S::kStages) * S::kStageBytes;
@@ -231,6 +232,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
   if (!ok)
     for (int q = total - 1; q >= 0 && q >= total - S::kStages; --q)
       (void)mbar_wait(&s_full[warp][q % S::kStages], (q / S::kStages) & 1, a.timeout_ns);
+  __syncwarp();
 
   // The tile's slots: its different adapters by first appearance.
   for (int i0 = 0; i0 < a.tile_rows; i0 += kShrinkThreads) {

@@ -449,6 +449,7 @@ __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int*
     atomicAdd(bar, 1);
     *flag = spin_until(bar, target, timeout_ns, err) ? 1 : 0;
   }
+  __syncwarp();
   named_bar_sync(kBarConsumers, kConsumers);
   return *flag != 0;
 }
@@ -463,6 +464,7 @@ __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid,
     __threadfence();
     *flag = old == parts - 1;
   }
+  __syncwarp();
   named_bar_sync(kBarConsumers, kConsumers);
   const bool last = *flag != 0;
   return last;
