@@ -94,7 +94,9 @@ struct Tables {
   int flag;
   int16_t row_tok[kMaxRecords];
   int16_t pos[kMaxRecords];
-  uint8_t idx[kMaxRecords];
+  int16_t pos_order[kMaxRecords];
+  uint8_t idx[kMaxRecords];    // of record (t, j) at t * k + j
+  uint8_t order[kMaxRecords];  // the same in capacity order
 };
 
 // Shared memory: the ring, the warps' sums, the column block's sums per token (first the
@@ -131,10 +133,12 @@ __device__ __forceinline__ float act_value(int act, float a) {
   return activation<MOE_ACT_GELU_TANH>(a);
 }
 
-// Order-preserving integer image of a float (+0 and -0 alike), for selection by maximum.
+// Order-preserving integer image of a float (+0 and -0 alike), for selection by maximum; never 0,
+// whatever the float.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t u = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return u != 0u ? u : 1u;
 }
 
 // ------------------------------------------------------------------ router
@@ -183,6 +187,7 @@ __device__ void partial_logits(const FewArgs& a, float* red, int tid) {
     const int i = o / ep, ee = o & (ep - 1);
     if (ee < a.E) {
       float s = 0.0f;
+#pragma unroll 8
       for (int q = 0; q < subs; ++q) s += red[(i * subs + q) * ep + ee];
       a.part_logits[(static_cast<int64_t>(slice) * a.N + t0 + i) * a.E + ee] = s;
     }
@@ -207,6 +212,7 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
     if (tid < n) {
       float s = a.bias != nullptr ? a.bias[tid % a.E] : 0.0f;
       float sum = 0.0f;
+#pragma unroll 8
       for (int q = 0; q < parts; ++q) sum += red[q * n + tid];
       z[tid] = sum + s;
     }
@@ -230,20 +236,18 @@ __device__ void select_all(const FewArgs& a, Tables& tb, const float* z, int war
     const float* zt = z + t * a.E;
     const bool in0 = lane < a.E, in1 = lane + 32 < a.E;
     const float z0 = in0 ? zt[lane] : 0.0f, z1 = in1 ? zt[lane + 32] : 0.0f;
-    uint64_t k0 = in0 ? (static_cast<uint64_t>(ordered(z0)) << 32) | (0xFFFFu - lane) : 0;
-    uint64_t k1 = in1 ? (static_cast<uint64_t>(ordered(z1)) << 32) | (0xFFFFu - lane - 32) : 0;
+    // Images of the values, 0 for none: the largest by a warp reduction, its lowest lane by a
+    // ballot (experts below 32 first).
+    uint32_t k0 = in0 ? ordered(z0) : 0u, k1 = in1 ? ordered(z1) : 0u;
     float zmax = 0.0f, zsel = 0.0f;
     int mine = 0;
     for (int j = 0; j < a.k; ++j) {
-      uint64_t best = k0 > k1 ? k0 : k1;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-        best = other > best ? other : best;
-      }
-      const int e = 0xFFFF - static_cast<int>(best & 0xFFFFu);
-      if (e == lane) k0 = 0;
-      if (e == lane + 32) k1 = 0;
+      const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, k0 > k1 ? k0 : k1);
+      const uint32_t b0 = __ballot_sync(0xFFFFFFFFu, k0 == best),
+                     b1 = __ballot_sync(0xFFFFFFFFu, k1 == best);
+      const int e = b0 != 0 ? __ffs(b0) - 1 : __ffs(b1) + 31;
+      if (e == lane) k0 = 0u;
+      if (e == lane + 32) k1 = 0u;
       const float v = zt[e];
       if (j == 0) zmax = v;
       if (lane == j) {
@@ -261,6 +265,7 @@ __device__ void select_all(const FewArgs& a, Tables& tb, const float* z, int war
     }
     if (lane < a.k) {
       tb.idx[t * a.k + lane] = static_cast<uint8_t>(mine);
+      tb.order[a.token_major ? t * a.k + lane : lane * a.N + t] = static_cast<uint8_t>(mine);
       tb.gate[t * a.k + lane] = num / (a.renorm ? sel : all);
     }
     if (lane == 0) {
@@ -279,19 +284,18 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
     int base = 0;
     for (int r0 = 0; r0 < R; r0 += 32) {
       const int r = r0 + lane;  // record in capacity order
-      int at = 0;
-      bool hit = false;
-      if (r < R) {
-        at = a.token_major ? r : (r % a.N) * a.k + r / a.N;
-        hit = tb.idx[at] == e;
-      }
+      const bool hit = r < R && tb.order[r] == e;
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
-      if (hit) tb.pos[at] = static_cast<int16_t>(base + __popc(m & below));
+      if (hit) tb.pos_order[r] = static_cast<int16_t>(base + __popc(m & below));
       base += __popc(m);
     }
     if (lane == 0) tb.load[e] = base;
   }
   named_bar_sync(kBarConsumers, kConsumers);
+  for (int r = tid; r < R; r += kConsumers) {
+    const int t = r / a.k;
+    tb.pos[r] = tb.pos_order[a.token_major ? r : (r - t * a.k) * a.N + t];
+  }
   if (warp == 0) {
     int before = 0, parts = 0, tiles = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
