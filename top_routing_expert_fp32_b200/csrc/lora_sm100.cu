@@ -15,6 +15,7 @@
 //      its first tile comes to the extra k-steps, so the shrink hides behind the main loop.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "stream.cuh"
@@ -66,7 +67,7 @@ struct ShrinkShape {
   static constexpr int kABoxBytes = kCK * kBoxRanks * 2;
   static constexpr int kABoxes = kRanks / kBoxRanks;
   static constexpr int kStageBytes = kABoxes * kABoxBytes + kRows * kCK * 2;
-  static constexpr int kStages = RT >= 8 ? 2 : 3;
+  static constexpr int kStages = RT >= 8 ? 2 : RT >= 4 ? 3 : 6;
   static constexpr size_t kSumBytes = sizeof(float) * kShrinkWarps * kRows * kRanks;
   static constexpr size_t kSmem =
       1024 + kSumBytes + static_cast<size_t>(kShrinkWarps) * kStages * kStageBytes;
@@ -90,7 +91,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t s_full[kShrinkWarps][S::kStages];
-  __shared__ int s_tile[256];   // adapters of the tile's rows
+  __shared__ __align__(16) int s_tile[256];  // adapters of the tile's rows
   __shared__ int s_slot[256];   // the tile's slots
   __shared__ uint32_t s_first[8];
   __shared__ int s_item[S::kRows];
@@ -181,36 +182,47 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
     const uint32_t mask = s_mask[item];
     const uint8_t* at = ring + (q % S::kStages) * S::kStageBytes;
     const uint8_t* xs = at + S::kABoxes * S::kABoxBytes;
+    // Row tiles without a row of this adapter are left out; the usual case, all tiles, is a
+    // branch of its own, since a test per instruction keeps the loads and MMAs from overlapping.
+    uint32_t tiles = 0;
 #pragma unroll
-    for (int kg = 0; kg < S::kCK / 32; ++kg) {
-      uint32_t x[NT][4];
+    for (int j = 0; j < NT; ++j) tiles |= ((mask >> (8 * j)) & 0xFFu) != 0 ? 1u << j : 0u;
+    auto step = [&](auto all) {
+      constexpr bool kAll = decltype(all)::value;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (((mask >> (8 * j)) & 0xFFu) == 0) continue;  // no row of this adapter
-        const uint4 v = *reinterpret_cast<const uint4*>(xs + (8 * j + g) * 128 +
-                                                        (((kg * 4 + t) ^ g) << 4));
-        const bool one = (t & 1) != 0, two = (t & 2) != 0;
-        const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
-                       a3 = one ? v.x : v.w;
-        x[j][0] = two ? a2 : a0;
-        x[j][1] = two ? a3 : a1;
-        x[j][2] = two ? a0 : a2;
-        x[j][3] = two ? a1 : a3;
-      }
+      for (int kg = 0; kg < S::kCK / 32; ++kg) {
+        uint32_t x[NT][4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int row = kg * 32 + static_cast<int>(stream::block_row(2 * s + (b >> 1), i8));
+        for (int j = 0; j < NT; ++j) {
+          if (!kAll && ((tiles >> j) & 1u) == 0) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(xs + (8 * j + g) * 128 +
+                                                          (((kg * 4 + t) ^ g) << 4));
+          const bool one = (t & 1) != 0, two = (t & 2) != 0;
+          const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
+                         a3 = one ? v.x : v.w;
+          x[j][0] = two ? a2 : a0;
+          x[j][1] = two ? a3 : a1;
+          x[j][2] = two ? a0 : a2;
+          x[j][3] = two ? a1 : a3;
+        }
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          uint32_t w[4];
-          stream::ldsm_x4_trans(S::a_piece(smem_u32(at), row, r * 2 + (b & 1)), w);
+        for (int s = 0; s < 2; ++s) {
+          const int row = kg * 32 + static_cast<int>(stream::block_row(2 * s + (b >> 1), i8));
+          uint32_t w[RT][4];
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            if (((mask >> (8 * j)) & 0xFFu) != 0)
-              stream::mma_bf16(acc[r][j], w, x[j][2 * s], x[j][2 * s + 1]);
+          for (int r = 0; r < RT; ++r)
+            stream::ldsm_x4_trans(S::a_piece(smem_u32(at), row, r * 2 + (b & 1)), w[r]);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              if (kAll || ((tiles >> j) & 1u) != 0)
+                stream::mma_bf16(acc[r][j], w[r], x[j][2 * s], x[j][2 * s + 1]);
         }
       }
-    }
+    };
+    if (tiles == (1u << NT) - 1u) step(std::true_type{});
+    else step(std::false_type{});
     if (q - item * per_item == per_item - 1) {  // the item's last step: its rows' sums
       float* mine = sums + static_cast<size_t>(warp) * S::kRows * S::kRanks;
 #pragma unroll
@@ -237,13 +249,15 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
   // The tile's slots: its different adapters by first appearance.
   for (int i0 = 0; i0 < a.tile_rows; i0 += kShrinkThreads) {
     const int i = i0 + tid;
-    bool first = i < a.tile_rows && s_tile[i] >= 0;
-    if (first)
-      for (int j = i - 1; j >= 0; --j)
-        if (s_tile[j] == s_tile[i]) {
-          first = false;
-          break;
-        }
+    const int mine = i < a.tile_rows ? s_tile[i] : -1;
+    bool first = mine >= 0;
+    const int4* all = reinterpret_cast<const int4*>(s_tile);
+#pragma unroll 8
+    for (int j = 0; j < (i0 + kShrinkThreads) / 4; ++j) {  // (every earlier row, four at a time)
+      const int4 v = all[j];
+      first = first && !((v.x == mine && 4 * j < i) || (v.y == mine && 4 * j + 1 < i) ||
+                         (v.z == mine && 4 * j + 2 < i) || (v.w == mine && 4 * j + 3 < i));
+    }
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, first);
     if (lane == 0) s_first[(i0 >> 5) + warp] = m;
   }
@@ -280,20 +294,31 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
     for (int c = lane; c < a.ld / 2; c += 32) {
       uint32_t v = 0u;
       if (2 * c < a.rank && ad >= 0) {
-        float s0 = 0.0f, s1 = 0.0f;
-        for (int blk = 0; blk < a.cluster; ++blk) {
+        // All blocks' values are on their way before the first is added.
+        const uint32_t here =
+            smem_u32(sums + static_cast<size_t>(l) * S::kRanks + 2 * c);
+        float2 part[8][kShrinkWarps];
 #pragma unroll
-          for (int w = 0; w < kShrinkWarps; ++w) {
-            const uint32_t at = mapa_shared(
-                smem_u32(sums + (static_cast<size_t>(w) * S::kRows + l) * S::kRanks + 2 * c),
-                static_cast<uint32_t>(blk));
-            float v0, v1;
-            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                         : "=f"(v0), "=f"(v1)
-                         : "r"(at)
-                         : "memory");
-            s0 += v0;
-            s1 += v1;
+        for (int blk = 0; blk < 8; ++blk) {
+          if (blk < a.cluster) {
+            const uint32_t at = mapa_shared(here, static_cast<uint32_t>(blk));
+#pragma unroll
+            for (int w = 0; w < kShrinkWarps; ++w)
+              asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                           : "=f"(part[blk][w].x), "=f"(part[blk][w].y)
+                           : "r"(at + w * S::kRows * S::kRanks * 4)
+                           : "memory");
+          }
+        }
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int blk = 0; blk < 8; ++blk) {
+          if (blk < a.cluster) {
+#pragma unroll
+            for (int w = 0; w < kShrinkWarps; ++w) {
+              s0 += part[blk][w].x;
+              s1 += part[blk][w].y;
+            }
           }
         }
         v = pack_bf16x2(s0 * sc, s1 * sc);
@@ -891,12 +916,16 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
   g.N = static_cast<int>(p.N);
   g.units = units_of_rank(p.rank);
   if (use_pairs(p)) return launch_gemm<true, 4>(p, mx, mw, ms, mb, g, stream);
-  // Single CTAs: the widest tiles that still give every SM one.
+  // Single CTAs: the tile width whose rounds cost least. A k-block of a 128 x 64 NB tile loads
+  // 16 + 8 NB KB, which takes longer than its MMAs (64 bytes per clock and SM from L2).
   const int64_t m_tiles = (p.M + 127) / 128;
-  if (m_tiles * ((p.N + 255) / 256) >= kSms)
-    return launch_gemm<false, 4>(p, mx, mw, ms, mb, g, stream);
-  if (m_tiles * ((p.N + 127) / 128) >= kSms)
-    return launch_gemm<false, 2>(p, mx, mw, ms, mb, g, stream);
+  auto cost = [&](int nb) {
+    const int64_t tiles = m_tiles * ((p.N + 64 * nb - 1) / (64 * nb));
+    return (tiles + kSms - 1) / kSms * (2 + nb);
+  };
+  const int64_t c1 = cost(1), c2 = cost(2), c4 = cost(4);
+  if (c4 <= c2 && c4 <= c1) return launch_gemm<false, 4>(p, mx, mw, ms, mb, g, stream);
+  if (c2 <= c1) return launch_gemm<false, 2>(p, mx, mw, ms, mb, g, stream);
   return launch_gemm<false, 1>(p, mx, mw, ms, mb, g, stream);
 }
 
