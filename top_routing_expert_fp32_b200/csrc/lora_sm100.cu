@@ -885,13 +885,26 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
   a.L = p.adapters;
   a.rank = p.rank;
   a.tile_rows = tile_rows_of(p);
+  // Single CTAs: the tile width whose rounds cost least. A k-block of a 128 x 64 NB tile loads
+  // 16 + 8 NB KB, which takes longer than its MMAs (64 bytes per clock and SM from L2).
+  const bool pairs = use_pairs(p);
+  const int64_t m_tiles = (p.M + 127) / 128;
+  auto tiles_with = [&](int nb) { return m_tiles * ((p.N + 64 * nb - 1) / (64 * nb)); };
+  auto cost = [&](int nb) { return (tiles_with(nb) + kSms - 1) / kSms * (2 + nb); };
+  int nb = cost(2) <= cost(1) ? 2 : 1;
+  if (cost(4) <= cost(nb)) nb = 4;
+  const int64_t ctas = pairs ? kSms : std::min<int64_t>(kSms, tiles_with(nb));
+
   // Groups of 32 rows share an adapter's reads; few rows take groups of 8, whose different
   // adapters then spread over more blocks. A group's K goes over as many blocks (at most 8) as
-  // the device has left.
+  // the device has left, but where the product leaves SMs free the shrink keeps to those: a
+  // CTA of the product that waits for its SM starts late by the whole shrink (200 rows by 5000
+  // columns: 29 us with 100 blocks beside 80 CTAs, 22 us with 50).
   const bool small = p.M <= 512;
   const int64_t groups = small ? (p.M + 7) / 8 : (p.M + 31) / 32;
+  const int64_t room = kSms - ctas >= groups ? kSms - ctas : 2 * kSms;
   a.cluster = 1;
-  while (a.cluster < 8 && groups * a.cluster * 2 <= 2 * kSms && a.K >= 256 * a.cluster * 2)
+  while (a.cluster < 8 && groups * a.cluster * 2 <= room && a.K >= 256 * a.cluster * 2)
     a.cluster *= 2;
   cudaError_t e =
       small ? launch_shrink_rank<1>(a, t, stream) : launch_shrink_rank<4>(a, t, stream);
@@ -915,17 +928,9 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
   g.K = static_cast<int>(p.K);
   g.N = static_cast<int>(p.N);
   g.units = units_of_rank(p.rank);
-  if (use_pairs(p)) return launch_gemm<true, 4>(p, mx, mw, ms, mb, g, stream);
-  // Single CTAs: the tile width whose rounds cost least. A k-block of a 128 x 64 NB tile loads
-  // 16 + 8 NB KB, which takes longer than its MMAs (64 bytes per clock and SM from L2).
-  const int64_t m_tiles = (p.M + 127) / 128;
-  auto cost = [&](int nb) {
-    const int64_t tiles = m_tiles * ((p.N + 64 * nb - 1) / (64 * nb));
-    return (tiles + kSms - 1) / kSms * (2 + nb);
-  };
-  const int64_t c1 = cost(1), c2 = cost(2), c4 = cost(4);
-  if (c4 <= c2 && c4 <= c1) return launch_gemm<false, 4>(p, mx, mw, ms, mb, g, stream);
-  if (c2 <= c1) return launch_gemm<false, 2>(p, mx, mw, ms, mb, g, stream);
+  if (pairs) return launch_gemm<true, 4>(p, mx, mw, ms, mb, g, stream);
+  if (nb == 4) return launch_gemm<false, 4>(p, mx, mw, ms, mb, g, stream);
+  if (nb == 2) return launch_gemm<false, 2>(p, mx, mw, ms, mb, g, stream);
   return launch_gemm<false, 1>(p, mx, mw, ms, mb, g, stream);
 }
 

@@ -457,9 +457,9 @@ __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int*
 // One arrival per block that shares a tile; true in the block that arrives last (its threads
 // then see what the others wrote before arriving).
 __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid, int* flag) {
-  __threadfence();
   named_bar_sync(kBarConsumers, kConsumers);
   if (tid == 0) {
+    __threadfence();  // after the barrier: the whole block's writes
     const int old = atomicAdd(counter, 1);
     __threadfence();
     *flag = old == parts - 1;
