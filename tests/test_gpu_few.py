@@ -109,6 +109,7 @@ CASES = [
     _cfg("two_experts_all_rows", 57, 512, 320, 2, 2, renorm=0),
     _cfg("decode_narrow", 64, 1024, 768, 8, 2),
     _cfg("many_experts", 64, 128, 192, 64, 4, router_bias_var=2.0),
+    _cfg("most_records", 64, 72, 136, 64, 8, router_bias_var=1.0),
     _cfg("f32_smallest", 2, 4, 4, 3, 3, dtype=F32),
     _cfg("f32_tiny", 64, 64, 128, 4, 2, dtype=F32),
     _cfg("f32_odd", 5, 100, 516, 7, 2, dtype=F32, act=configs.ACT_GELU_ERF, renorm=0),
@@ -255,3 +256,22 @@ def test_agrees_with_the_whole_layer_call(abi):
     assert np.array_equal(idx.cpu().numpy(), ex["idx"])
     a, b = to_f64(out), to_f64(ref)
     assert (np.abs(a - b).max(1) <= 3 * 2.0 ** -8 * np.abs(b).max(1) + 1e-6).all()
+
+
+def test_an_expert_past_32_bit_offsets(abi):
+    # The last of 64 experts lies past 2^31 elements: the same bits as a layer of it alone.
+    D, F, E = 4096, 8448, 64
+    assert (E - 1) * D * F > 2 ** 31
+    one = inputs.make_inputs(_cfg("one", 3, D, F, 1, 1), "cuda")
+    far = [torch.zeros((E,) + tuple(w.shape[1:]), dtype=w.dtype, device="cuda")
+           for w in (one.W1, one.W2, one.W3)]
+    for w, o in zip(far, (one.W1, one.W2, one.W3)):
+        w[E - 1] = o[0]
+    bias = torch.zeros(E, device="cuda")
+    bias[E - 1] = 1e4
+    W_r = torch.zeros((D, E), device="cuda")
+    cfg = _cfg("far", 3, D, F, E, 1)
+    want, _ = _run(abi, cfg.with_(E=1), one)
+    inp = inputs.MoEInputs(one.X, W_r, bias, *far)
+    out, ex = _run(abi, cfg, inp)
+    assert (ex["idx"] == E - 1).all() and torch.equal(out, want)

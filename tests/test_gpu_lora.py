@@ -221,3 +221,18 @@ def test_layer_and_projection_together(abi):
     torch.cuda.synchronize()
     assert abi.device_error(ws) == 0 and abi.device_error(layer.ws) == 0
     c.check(out)
+
+
+@pytest.mark.parametrize("M", [4, 200])
+def test_an_adapter_past_32_bit_offsets(abi, M):
+    # The last adapter lies past 2^31 elements: the same bits as that adapter alone.
+    K, N, L, r = 14336, 256, 1216, 128
+    assert (L - 1) * K * r > 2 ** 31
+    one = Case(M, K, N, 1, r, scale=False)
+    want = one.run(abi)
+    A = torch.zeros((L, K, r), dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros((L, r, N), dtype=torch.bfloat16, device="cuda")
+    A[L - 1], B[L - 1] = one.A[0], one.B[0]
+    one.A, one.B, one.L = A, B, L
+    one.adapter = torch.full_like(one.adapter, L - 1)
+    assert torch.equal(one.run(abi), want)

@@ -19,8 +19,8 @@
 // (64 columns for fp32 weights, 256 for 8-bit ones: 256 bytes either way.)
 // Rows of an expert are its kept tokens in capacity order, read from X by index: no
 // permutation is written. More than 32 rows of an expert are two pieces, each reading the
-// expert's weights: the sums of 32 rows are what the registers hold. A tile shared by several blocks is summed by the last to finish, in
-// block order, so equal inputs give equal bits.
+// expert's weights: the sums of 32 rows are what the registers hold. A tile shared by several
+// blocks is summed by the last to finish, in block order, so equal inputs give equal bits.
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
@@ -114,7 +114,8 @@ __host__ __device__ constexpr size_t ring_bytes(int N, int E) {
          ~size_t(1023);
 }
 __host__ __device__ constexpr int ring_stages(size_t bytes, int row_tiles) {
-  const int s = static_cast<int>(bytes / (kStageBytes + static_cast<size_t>(row_tiles) * kTileBytes));
+  const int s =
+      static_cast<int>(bytes / (kStageBytes + static_cast<size_t>(row_tiles) * kTileBytes));
   return s < kMaxStages ? s : kMaxStages;
 }
 static_assert(ring_stages(ring_bytes<kW8>(kMaxRows, kMaxE), kTileRows / 8) >= 2, "ring of two");
@@ -203,7 +204,7 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
     const int l = tid % n, part = tid / n;
     if (part < parts) {
       float s = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
       for (int q = part; q < a.slices; q += parts)
         s += __ldcg(a.part_logits + static_cast<int64_t>(q) * n + l);
       red[part * n + l] = s;
@@ -219,7 +220,7 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
   } else {
     for (int l = tid; l < n; l += kConsumers) {
       float s = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
       for (int q = 0; q < a.slices; ++q)
         s += __ldcg(a.part_logits + static_cast<int64_t>(q) * n + l);
       z[l] = s + (a.bias != nullptr ? a.bias[l % a.E] : 0.0f);
@@ -890,7 +891,8 @@ template <int WK>
 cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const void* W2,
                    const void* W3, cudaStream_t stream) {
   CUtensorMap m1, m2, m3;
-  if (!make_stream_map(&m1, W1, WK, p.F, p.D, p.E) || !make_stream_map(&m2, W2, WK, p.F, p.D, p.E) ||
+  if (!make_stream_map(&m1, W1, WK, p.F, p.D, p.E) ||
+      !make_stream_map(&m2, W2, WK, p.F, p.D, p.E) ||
       !make_stream_map(&m3, W3, WK, p.D, p.F, p.E))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(
