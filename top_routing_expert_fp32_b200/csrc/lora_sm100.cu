@@ -897,12 +897,13 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
 
   // Groups of 32 rows share an adapter's reads; few rows take groups of 8, whose different
   // adapters then spread over more blocks. A group's K goes over as many blocks (at most 8) as
-  // the device has left, but where the product leaves SMs free the shrink keeps to those: a
-  // CTA of the product that waits for its SM starts late by the whole shrink (200 rows by 5000
+  // the device has left (one round of the large groups' blocks, which take an SM each: 4096 rows
+  // 358 us against 369 in two), but where the product leaves SMs free the shrink keeps to those:
+  // a CTA of the product that waits for its SM starts late by the whole shrink (200 rows by 5000
   // columns: 29 us with 100 blocks beside 80 CTAs, 22 us with 50).
   const bool small = p.M <= 512;
   const int64_t groups = small ? (p.M + 7) / 8 : (p.M + 31) / 32;
-  const int64_t room = kSms - ctas >= groups ? kSms - ctas : 2 * kSms;
+  const int64_t room = kSms - ctas >= groups ? kSms - ctas : small ? 2 * kSms : kSms;
   a.cluster = 1;
   while (a.cluster < 8 && groups * a.cluster * 2 <= room && a.K >= 256 * a.cluster * 2)
     a.cluster *= 2;
