@@ -640,10 +640,8 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   const int down_cols = (a.D + S::kCols - 1) / S::kCols;
   const int parts = tb.n_parts;
   const int down_steps = parts * run_steps;
-  SplitK up{static_cast<long long>(parts) * up_cols * up_steps, 0};
-  SplitK down{static_cast<long long>(down_cols) * down_steps, 0};
-  up.grid = static_cast<int>(min(static_cast<long long>(G), up.total));
-  down.grid = static_cast<int>(min(static_cast<long long>(G), down.total));
+  const SplitK up(static_cast<long long>(parts) * up_cols, up_steps, G);
+  const SplitK down(parts > 0 ? down_cols : 0, down_steps, G);
   const int me = static_cast<int>(blockIdx.x);
   const long long u0 = me < up.grid ? up.start(me) : 0, u1 = me < up.grid ? up.start(me + 1) : 0;
   const long long d0 = me < down.grid ? down.start(me) : 0,

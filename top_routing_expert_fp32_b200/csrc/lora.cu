@@ -378,8 +378,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   const int k_steps = (a.K + 2 * kBoxRows - 1) / (2 * kBoxRows);
   const int steps = k_steps + (n_pieces + kStagePieces - 1) / kStagePieces;
   const int tiles = (a.N + S::kCols - 1) / S::kCols;
-  SplitK sp{static_cast<long long>(tiles) * steps, 0};
-  sp.grid = static_cast<int>(min(static_cast<long long>(G), sp.total));
+  const SplitK sp(tiles, steps, G);
   const long long s0 = me < sp.grid ? sp.start(me) : 0, s1 = me < sp.grid ? sp.start(me + 1) : 0;
 
   // The block's segments (a tile and its stages [k0, k1)) in order, the first one last: it is a

@@ -85,15 +85,27 @@ __device__ __forceinline__ int warp_row(int warp) {
   return WK == kW8 ? 0 : (warp & 1) * 32;
 }
 
-// Equal runs of the `total` stages of a product over `grid` blocks: block c takes
-// [start(c), start(c+1)).
+// The stages of a product, `tiles` of `steps` each, over at most `blocks` blocks: block c takes
+// [start(c), start(c+1)). Equal runs of stages, or runs of whole tiles where those are hardly
+// longer: sharing a tile costs a block about as much as kShareStages stages (its sums to L2 and
+// back, and an arrival that everybody's writes wait for).
+constexpr int kShareStages = 4;
 struct SplitK {
-  long long total;
+  long long units;  // stages or whole tiles
+  int unit;         // stages of a unit
   int grid;
-  __device__ long long start(int c) const { return total * c / grid; }
-  // The block that takes stage s (the largest c with start(c) <= s).
+  __device__ SplitK(long long tiles, int steps, int blocks) {
+    const long long total = tiles * steps;
+    const long long whole = (tiles + blocks - 1) / blocks * steps;
+    const bool by_tile = whole <= (total + blocks - 1) / blocks + kShareStages;
+    units = by_tile ? tiles : total;
+    unit = by_tile ? steps : 1;
+    grid = static_cast<int>(units < blocks ? units : blocks);
+  }
+  __device__ long long start(int c) const { return units * c / grid * unit; }
+  // The block that takes stage s, by stages (the largest c with start(c) <= s).
   __device__ int owner(long long s) const {
-    return static_cast<int>(((s + 1) * grid - 1) / total);
+    return static_cast<int>(((s + 1) * grid - 1) / units);
   }
 };
 
