@@ -18,9 +18,10 @@
 //      over all experts in shared memory per token, which is the combine.
 // (64 columns for fp32 weights, 256 for 8-bit ones: 256 bytes either way.)
 // Rows of an expert are its kept tokens in capacity order, read from X by index: no
-// permutation is written. More than 32 rows of an expert are two pieces, each reading the
-// expert's weights: the sums of 32 rows are what the registers hold. A tile shared by several
-// blocks is summed by the last to finish, in block order, so equal inputs give equal bits.
+// permutation is written. More than 32 rows of an expert (8-bit weights: 16) are several pieces,
+// each reading the expert's weights: the sums of so many rows are what the registers hold. A
+// tile shared by several blocks is summed by the last to finish, in block order, so equal inputs
+// give equal bits.
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
@@ -36,8 +37,8 @@ using namespace stream;
 
 constexpr int kMaxRecords = kMaxRows * 8;
 constexpr int kMaxE = 64;
-// Products: an expert's kept rows in pieces of at most kTileRows.
-constexpr int kMaxParts = kMaxE + kMaxRecords / kTileRows;
+// Products: an expert's kept rows in pieces of at most Shape::kPieceRows (16 or 32).
+constexpr int kMaxParts = kMaxE + kMaxRecords / 16;
 constexpr int kMaxSlices = 64;  // pieces of D of the router's partial logits
 
 struct FewArgs {
@@ -74,7 +75,7 @@ struct FewArgs {
 struct Part {
   int16_t expert;
   int16_t row0;  // first row of the piece among all kept rows
-  int16_t n;     // rows, 1..kTileRows
+  int16_t n;     // rows, at least 1
   int16_t tile;  // its first tile of 8 rows in H
 };
 
@@ -118,8 +119,9 @@ __host__ __device__ constexpr int ring_stages(size_t bytes, int row_tiles) {
       static_cast<int>(bytes / (kStageBytes + static_cast<size_t>(row_tiles) * kTileBytes));
   return s < kMaxStages ? s : kMaxStages;
 }
-static_assert(ring_stages(ring_bytes<kW8>(kMaxRows, kMaxE), kTileRows / 8) >= 2, "ring of two");
-static_assert(ring_stages(ring_bytes<kBF16>(kMaxRows, kMaxE), kTileRows / 8) >= 3, "ring of three");
+static_assert(ring_stages(ring_bytes<kW8>(kMaxRows, kMaxE), 2) >= 2, "ring");
+static_assert(ring_stages(ring_bytes<kBF16>(kMaxRows, kMaxE), 4) >= kInFlight, "ring");
+static_assert(ring_stages(ring_bytes<kF32>(kMaxRows, kMaxE), 4) >= kInFlight, "ring");
 
 // H. 16-bit kinds: per tile of 8 rows and 32 values of F two planes (the first and the second
 // bf16 term) of 32 threads x 16 bytes, each thread's four pairs in block order (stream.cuh):
@@ -145,8 +147,9 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 // ------------------------------------------------------------------ router
 
 // This block's partial logits: tokens [t0, t1) over rows [d0, d1) of D.
-template <bool XF32>
+template <int WK>
 __device__ void partial_logits(const FewArgs& a, float* red, int tid) {
+  constexpr int kConsumers = Team<WK>::kConsumers;
   const int groups = (a.N + a.tokens_per_group - 1) / a.tokens_per_group;
   const int group = static_cast<int>(blockIdx.x) % groups;
   const int slice = static_cast<int>(blockIdx.x) / groups;
@@ -169,7 +172,7 @@ __device__ void partial_logits(const FewArgs& a, float* red, int tid) {
       for (int i = 0; i < 8; ++i) {
         if (i < nt) {
           const int64_t at = static_cast<int64_t>(t0 + i) * a.D + d;
-          const float x = XF32 ? __ldg(static_cast<const float*>(a.X) + at)
+          const float x = WK == kF32 ? __ldg(static_cast<const float*>(a.X) + at)
                                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[at]);
           acc[i] = fmaf(x, w, acc[i]);
         }
@@ -196,6 +199,7 @@ __device__ void partial_logits(const FewArgs& a, float* red, int tid) {
 }
 
 // All logits in shared memory, z[t * E + e].
+template <int kConsumers>
 __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
   const int n = a.N * a.E;
   int parts = 1;  // threads per logit
@@ -232,8 +236,9 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
 // Top-k and gates, one warp per token (the rules of select.cuh's plain top-k: descending fp32
 // logits, the lower index first among equals, gates from exp(z - max)). The selection always
 // yields k distinct experts, whatever the logits hold.
+template <int kWarps>
 __device__ void select_all(const FewArgs& a, Tables& tb, const float* z, int warp, int lane) {
-  for (int t = warp; t < a.N; t += kConsumerWarps) {
+  for (int t = warp; t < a.N; t += kWarps) {
     const float* zt = z + t * a.E;
     const bool in0 = lane < a.E, in1 = lane + 32 < a.E;
     const float z0 = in0 ? zt[lane] : 0.0f, z1 = in1 ? zt[lane + 32] : 0.0f;
@@ -278,10 +283,11 @@ __device__ void select_all(const FewArgs& a, Tables& tb, const float* z, int war
 
 // Loads, capacity positions, segment offsets, the experts with rows, and the rows' tokens and
 // gates (walkthrough 1.3, 3.1, 3.2; MoE series 2.2).
+template <int kConsumers, int kPieceRows>
 __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int lane) {
   const int R = a.N * a.k;
   const uint32_t below = (1u << lane) - 1u;
-  for (int e = warp; e < a.E; e += kConsumerWarps) {
+  for (int e = warp; e < a.E; e += kConsumers / 32) {
     int base = 0;
     for (int r0 = 0; r0 < R; r0 += 32) {
       const int r = r0 + lane;  // record in capacity order
@@ -304,22 +310,22 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
       const int n = e < a.E ? static_cast<int>(min(static_cast<int64_t>(tb.load[e]), a.capacity))
                             : 0;
       // Inclusive prefix sums over the lanes: rows, pieces and row tiles (n <= 64 a lane).
-      int sum = n | ((n + kTileRows - 1) / kTileRows) << 12 | ((n + 7) / 8) << 20;
+      int sum = n | ((n + kPieceRows - 1) / kPieceRows) << 12 | ((n + 7) / 8) << 20;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
         if (lane >= o) sum += v;
       }
       const int total = __shfl_sync(0xFFFFFFFFu, sum, 31);
-      const int np = (n + kTileRows - 1) / kTileRows, nt = (n + 7) / 8;
+      const int np = (n + kPieceRows - 1) / kPieceRows, nt = (n + 7) / 8;
       const int row = before + (sum & 0xFFF) - n;
       const int part = parts + ((sum >> 12) & 0xFF) - np;
       const int tile = tiles + (sum >> 20) - nt;
       if (e < a.E) tb.off[e] = row;
       for (int q = 0; q < np; ++q)
-        tb.part[part + q] = {static_cast<int16_t>(e), static_cast<int16_t>(row + q * kTileRows),
-                             static_cast<int16_t>(min(kTileRows, n - q * kTileRows)),
-                             static_cast<int16_t>(tile + q * (kTileRows / 8))};
+        tb.part[part + q] = {static_cast<int16_t>(e), static_cast<int16_t>(row + q * kPieceRows),
+                             static_cast<int16_t>(min(kPieceRows, n - q * kPieceRows)),
+                             static_cast<int16_t>(tile + q * (kPieceRows / 8))};
       const int most = __reduce_max_sync(0xFFFFFFFFu, n);
       if (lane == 0) tb.max_rows = e0 == 0 ? most : max(tb.max_rows, most);
       before += total & 0xFFF;
@@ -353,6 +359,7 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
   }
 }
 
+template <int kConsumers>
 __device__ void export_routing(const FewArgs& a, const Tables& tb, const float* z, int tid) {
   const int R = a.N * a.k;
   for (int r = tid; r < R; r += kConsumers) {
@@ -377,10 +384,11 @@ __device__ void export_routing(const FewArgs& a, const Tables& tb, const float* 
 
 // ------------------------------------------------------------------ consumers
 
+template <int WK>
 struct Consumer {
   Ring ring;
   Cursor cur;
-  RedTurn red;
+  RedTurn<WK> red;
   int tid, warp, lane;
   bool ok;
   uint64_t timeout_ns;
@@ -396,7 +404,7 @@ struct Consumer {
   }
   __device__ uint32_t my_box() const {
     return smem_u32(ring.weights) + static_cast<uint32_t>(cur.stage) * kStageBytes +
-           static_cast<uint32_t>(warp >> 1) * kBoxBytes;
+           static_cast<uint32_t>(box_of<WK>(warp)) * kBoxBytes;
   }
   __device__ const uint8_t* rows() const { return ring.rows + cur.stage * ring.row_bytes; }
   __device__ void release() {
@@ -454,11 +462,12 @@ __device__ __forceinline__ void finish_h(const FewArgs& a, const Tables& tb, con
 }
 
 template <int WK, int NT>
-__device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& c,
+__device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer<WK>& c,
                                         const SplitK& sp, long long tile, int steps, int k0,
                                         int k1, const Part pt, int fb) {
   using S = Shape<WK>;
   using P = Places<WK>;
+  constexpr int kConsumers = Team<WK>::kConsumers;
   Acc<WK, NT> acc;
   acc.zero();
   const int first_row = warp_row<WK>(c.warp);
@@ -466,12 +475,12 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
     c.wait_full();
     const int d0 = s * kBoxRows + first_row;
     if constexpr (WK == kF32) {
-      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, smem_u32(c.rows()) + first_row * 4, kRowPitchF32,
-                       pt.n, d0, a.D);
+      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, smem_u32(c.rows()) + first_row * 4,
+                       kRowPitchF32, pt.n, d0, a.D);
       c.release();
     } else {
       Weights<WK> w;
-      Frag<WK, NT, false> f;
+      Frag<NT, false> f;
       w.load(c.my_box(), c.warp, c.lane);
       f.load_rows(c.rows(), kRowPitch, first_row / 32, d0, a.D, c.lane);
       c.release();
@@ -497,22 +506,23 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
         mine[(2 * j + 1) * P::kCount + i] = h2;
       }
     }
+    c.red.done();
   }
   if (whole) return;
   const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
-  if (!last_to_finish(a.counters + first, last - first + 1, c.tid, &tb.flag)) return;
-  constexpr int kMine = (P::kCount + kConsumers - 1) / kConsumers;  // places of a row tile
+  if (!last_to_finish<kConsumers>(a.counters + first, last - first + 1, c.tid, &tb.flag)) return;
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
-    float2 h[2][kMine];
+    float2 h[2][P::kMine];
 #pragma unroll
     for (int branch = 0; branch < 2; ++branch) {
 #pragma unroll
-      for (int q = 0; q < kMine; ++q) h[branch][q] = make_float2(0.0f, 0.0f);
-      add_shares(h[branch], a.part, a.part_floats, first, last, (2 * j + branch) * P::kCount + c.tid,
-                 (2 * j + branch + 1) * P::kCount);
+      for (int q = 0; q < P::kMine; ++q) h[branch][q] = make_float2(0.0f, 0.0f);
+      const int at = (2 * j + branch) * P::kCount;
+      add_shares<kConsumers>(h[branch], a.part, a.part_floats, first, last, at + c.tid,
+                             at + P::kCount);
     }
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) {
+    for (int q = 0; q < P::kMine; ++q) {
       const int i = c.tid + q * kConsumers;
       if (i < P::kCount)
         finish_h<WK>(a, tb, pt, 8 * j + P::row(i), fb * S::kCols + P::col(i), h[0][q], h[1][q]);
@@ -523,14 +533,15 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer& 
 // ---- down: stages [s0, s1) of one piece's part of one column block, added into outacc
 
 template <int WK, int NT>
-__device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer& c, int s0, int s1,
+__device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer<WK>& c, int s0, int s1,
                                          const Part pt, int cb, float* outacc) {
   using S = Shape<WK>;
   using P = Places<WK>;
+  constexpr int kConsumers = Team<WK>::kConsumers;
   Acc<WK, NT> acc;
   acc.zero();
-  // Warps 0-3 take the stage's first 64 k-rows, warps 4-7 the others.
-  const int first_row = (c.warp >> 2) * kBoxRows + warp_row<WK>(c.warp);
+  // The first two boxes hold the stage's first 64 k-rows, the others the next.
+  const int first_row = (box_of<WK>(c.warp) >> 1) * kBoxRows + warp_row<WK>(c.warp);
   for (int s = s0; s < s1; ++s) {
     c.wait_full();
     if constexpr (WK == kF32) {
@@ -539,7 +550,7 @@ __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer&
       c.release();
     } else {
       Weights<WK> w;
-      Frag<WK, NT, true> f;
+      Frag<NT, true> f;
       w.load(c.my_box(), c.warp, c.lane);
       f.load_ordered(c.rows(), first_row / 32, c.lane);
       c.release();
@@ -568,6 +579,7 @@ __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer&
       o->x += v.x;
       o->y += v.y;
     }
+    c.red.done();
   }
 }
 
@@ -581,28 +593,34 @@ __device__ __forceinline__ void store_out(const FewArgs& a, int t, int d, float2
     *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) = pack_bf16x2(v.x, v.y);
 }
 
-#define MOE_FEW_ROWS(n, CALL)      \
-  do {                             \
-    if ((n) <= 8) CALL(1);         \
-    else if ((n) <= 16) CALL(2);   \
-    else if ((n) <= 24) CALL(3);   \
-    else CALL(4);                  \
+// CALL(row tiles) for n rows, where a piece has at most MAXNT row tiles.
+#define MOE_FEW_ROWS(n, CALL)                             \
+  do {                                                    \
+    if (MAXNT == 1 || (n) <= 8) CALL(1);                  \
+    else if (MAXNT == 2 || (n) <= 16) CALL(MAXNT < 2 ? 1 : 2);  \
+    else if ((n) <= 24) CALL(MAXNT < 4 ? 1 : 3);          \
+    else CALL(MAXNT < 4 ? 1 : 4);                         \
   } while (0)
 
 // ------------------------------------------------------------------ the kernel
 
-template <int WK>
-__global__ void __launch_bounds__(kThreads, 1)
+// MAXNT: row tiles of the largest possible piece (the tokens of a batch bound an expert's rows).
+// A kernel that holds only what its batch can need keeps its loops out of local memory: a spill
+// costs an L2 access here, since the ring leaves the L1 cache almost nothing.
+template <int WK, int MAXNT>
+__global__ void __launch_bounds__(Team<WK>::kThreads, 1)
 few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,
            const __grid_constant__ CUtensorMap m3, const __grid_constant__ FewArgs a) {
   using S = Shape<WK>;
   using P = Places<WK>;
+  constexpr int kConsumers = Team<WK>::kConsumers;
+  using T = Team<WK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const size_t ring_size = ring_bytes<WK>(a.N, a.E);
   float* red = reinterpret_cast<float*>(smem + ring_size);
-  float* outacc = red + 2 * kRedFloats;  // the logits first, then the column block's sums
+  float* outacc = red + kRedBytes / sizeof(float);  // the logits first, then the column block's sums
   Tables& tb = *reinterpret_cast<Tables*>(reinterpret_cast<uint8_t*>(outacc) +
                                           out_bytes<WK>(a.N, a.E));
   const int tid = static_cast<int>(threadIdx.x);
@@ -613,7 +631,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&tb.full[i], 1);
       mbar_init(&tb.rows_full[i], 32);  // the row producer's lanes
-      mbar_init(&tb.empty[i], kConsumerWarps);
+      mbar_init(&tb.empty[i], T::kWarps);
     }
     fence_barrier_init();
     // Arrivals at this block's shared tiles; seen by the others after the first grid barrier.
@@ -623,16 +641,15 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   __syncthreads();
 
   bool ok = true;
-  if (warp < kConsumerWarps) {
-    if constexpr (WK == kF32) partial_logits<true>(a, red, tid);
-    else partial_logits<false>(a, red, tid);
-    ok = grid_barrier(a.bar, G, tid, &tb.flag, a.timeout_ns, a.err);
-    sum_logits(a, outacc, red, tid);
-    select_all(a, tb, outacc, warp, lane);
+  if (warp < T::kWarps) {
+    partial_logits<WK>(a, red, tid);
+    ok = grid_barrier<kConsumers>(a.bar, G, tid, &tb.flag, a.timeout_ns, a.err);
+    sum_logits<kConsumers>(a, outacc, red, tid);
+    select_all<T::kWarps>(a, tb, outacc, warp, lane);
     named_bar_sync(kBarConsumers, kConsumers);
-    assign_rows(a, tb, tid, warp, lane);
+    assign_rows<kConsumers, S::kPieceRows>(a, tb, tid, warp, lane);
   }
-  named_bar_sync(kBarAll, kThreads);
+  named_bar_sync(kBarAll, T::kThreads);
 
   const int up_steps = (a.D + kBoxRows - 1) / kBoxRows;
   const int up_cols = (a.F + S::kCols - 1) / S::kCols;
@@ -647,7 +664,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
   const long long d0 = me < down.grid ? down.start(me) : 0,
                   d1 = me < down.grid ? down.start(me + 1) : 0;
 
-  const int row_tiles = max(1, min(kTileRows, tb.max_rows) + 7) / 8;
+  const int row_tiles = max(1, min(S::kPieceRows, tb.max_rows) + 7) / 8;
   Ring ring;
   ring.stages = ring_stages(ring_size, row_tiles);
   ring.row_bytes = row_tiles * kTileBytes;
@@ -684,9 +701,9 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
     }
   };
 
-  if (warp >= kConsumerWarps) {
-    give_registers<kProducerRegs>();
-    if (warp == kWeightWarp) {
+  if (warp >= T::kWarps) {
+    give_registers<T::kProducerRegs>();
+    if (warp == T::kWeightWarp) {
       // Weight producer: one thread issues this block's stages of both products in order.
       if (lane == 0) {
         // Weights are read once; evict_first read 6.4 TB/s where the default read 6.0.
@@ -726,7 +743,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
         drain(tb.full, ring.stages, c, issued, a.timeout_ns);
       }
       __syncwarp();
-    } else if (warp == kRowWarp) {
+    } else if (warp == T::kRowWarp) {
       // Row producer: the kept tokens' rows of X, 16 bytes per lane and copy; then tiles of H,
       // one bulk copy each, after the barrier that completes H.
       Cursor c;
@@ -794,14 +811,14 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       __syncwarp();
     }
   } else {
-    take_registers<kConsumerRegs>();
-    if (me == 0) export_routing(a, tb, outacc, tid);
+    take_registers<T::kConsumerRegs>();
+    if (me == 0) export_routing<kConsumers>(a, tb, outacc, tid);
     if (parts == 0) {  // a capacity of zero keeps nothing: zeros
       for (int cb = me; cb < down_cols; cb += G)
         for (int i = tid; i < a.N * P::kPairs; i += kConsumers)
           store_out<WK>(a, P::row(i), cb * S::kCols + P::col(i), make_float2(0.0f, 0.0f));
     }
-    Consumer c{ring, Cursor{}, RedTurn{red}, tid, warp, lane, ok, a.timeout_ns, a.err};
+    Consumer<WK> c{ring, Cursor{}, RedTurn<WK>{red}, tid, warp, lane, ok, a.timeout_ns, a.err};
     for (long long s = u0; s < u1;) {
       const long long tile = s / up_steps;
       const int k0 = static_cast<int>(s - tile * up_steps);
@@ -814,7 +831,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       s += k1 - k0;
     }
     fence_proxy_async_all();  // H is read by bulk copies
-    if (!grid_barrier(a.bar, 2 * G, tid, &tb.flag, a.timeout_ns, a.err)) c.ok = false;
+    if (!grid_barrier<kConsumers>(a.bar, 2 * G, tid, &tb.flag, a.timeout_ns, a.err)) c.ok = false;
     named_bar_arrive(kBarRows, kConsumers + 32);
 
     for (long long s = d0; s < d1;) {
@@ -846,13 +863,13 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       if (!whole) {
         const int first = down.owner(tile * down_steps),
                   last = down.owner(tile * down_steps + down_steps - 1);
-        if (last_to_finish(a.counters + kMaxGrid + first, last - first + 1, tid, &tb.flag)) {
+        if (last_to_finish<kConsumers>(a.counters + kMaxGrid + first, last - first + 1, tid, &tb.flag)) {
           constexpr int kChunk = 8;
           for (int i0 = tid; i0 < a.N * P::kPairs; i0 += kChunk * kConsumers) {
             float2 v[kChunk];
 #pragma unroll
             for (int q = 0; q < kChunk; ++q) v[q] = make_float2(0.0f, 0.0f);
-            add_shares(v, a.part, a.part_floats, first, last, i0, a.N * P::kPairs);
+            add_shares<kConsumers>(v, a.part, a.part_floats, first, last, i0, a.N * P::kPairs);
 #pragma unroll
             for (int q = 0; q < kChunk; ++q) {
               const int i = i0 + q * kConsumers;
@@ -885,7 +902,7 @@ int64_t part_floats_of(int kind, int64_t N) {
   return cols * std::max<int64_t>(N, 16 * std::min<int64_t>(4, (N + 7) / 8));
 }
 
-template <int WK>
+template <int WK, int MAXNT>
 cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const void* W2,
                    const void* W3, cudaStream_t stream) {
   CUtensorMap m1, m2, m3;
@@ -894,11 +911,11 @@ cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const
       !make_stream_map(&m3, W3, WK, p.D, p.F, p.E))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(
-      few_kernel<WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
+      few_kernel<WK, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min(num_sms(), kMaxGrid)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Team<WK>::kThreads);
   cfg.dynamicSmemBytes = kMaxSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -906,8 +923,17 @@ cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, few_kernel<WK>, m1, m2, m3, a);
+  e = cudaLaunchKernelEx(&cfg, few_kernel<WK, MAXNT>, m1, m2, m3, a);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int WK>
+cudaError_t launch_kind(const moe_problem& p, const FewArgs& a, const FewTensors& t,
+                        cudaStream_t stream) {
+  if (p.N <= 8) return launch<WK, 1>(p, a, t.W1, t.W2, t.W3, stream);
+  if (p.N <= 16 || Shape<WK>::kPieceRows == 16)
+    return launch<WK, 2>(p, a, t.W1, t.W2, t.W3, stream);
+  return launch<WK, Shape<WK>::kPieceRows / 8>(p, a, t.W1, t.W2, t.W3, stream);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1026,9 +1052,9 @@ cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors&
   a.token_major = p.capacity_order == MOE_ORDER_TOKEN_MAJOR;
   a.renorm_kept = p.drop_policy == MOE_DROP_RENORM_KEPT;
   a.act = p.activation;
-  if (t.S1 != nullptr) return launch<kW8>(p, a, t.W1, t.W2, t.W3, stream);
-  if (p.dtype == MOE_DTYPE_F32) return launch<kF32>(p, a, t.W1, t.W2, t.W3, stream);
-  return launch<kBF16>(p, a, t.W1, t.W2, t.W3, stream);
+  if (t.S1 != nullptr) return launch_kind<kW8>(p, a, t, stream);
+  if (p.dtype == MOE_DTYPE_F32) return launch_kind<kF32>(p, a, t, stream);
+  return launch_kind<kBF16>(p, a, t, stream);
 }
 
 }  // namespace moe

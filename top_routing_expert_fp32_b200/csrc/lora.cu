@@ -13,8 +13,8 @@
 //      is its k-stages and then those. A warp multiplies a piece into fresh registers, for the
 //      row tiles that have the adapter, and adds the sums of those rows only, so that a row
 //      never meets another adapter's values, whatever they hold. S enters as two bf16 terms (16
-//      bits of mantissa; fp32 weights: as it is). (The rows' expand products on the CUDA cores, row by row out of L2, took longer
-//      than the stream: 48 rows of 48 adapters 71 us.)
+//      bits of mantissa; fp32 weights: as it is). (The rows' expand products on the CUDA cores,
+//      row by row out of L2, took longer than the stream: 48 rows of 48 adapters 71 us.)
 #include <algorithm>
 #include <cstdint>
 
@@ -26,6 +26,11 @@ namespace moe {
 namespace {
 
 using namespace stream;
+
+// bf16 and fp32 weights: eight consumer warps; the two producers' neighbours compute S.
+using LoraTeam = Team<kBF16>;
+static_assert(Team<kF32>::kThreads == LoraTeam::kThreads, "one team");
+constexpr int kConsumers = LoraTeam::kConsumers, kThreads = LoraTeam::kThreads;
 
 constexpr int kMaxRank = 128;
 // 128 values of a row: bf16 with 16 bytes against bank conflicts, fp32 (read as broadcasts) plain.
@@ -311,7 +316,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* red = reinterpret_cast<float*>(smem + lora_ring_bytes(a.M, a.rank));
-  uint8_t* S_mem = reinterpret_cast<uint8_t*>(red + 2 * kRedFloats);  // S, scaled
+  uint8_t* S_mem = reinterpret_cast<uint8_t*>(red) + kRedBytes;  // S, scaled
   LoraTables& tb = *reinterpret_cast<LoraTables*>(S_mem + s_bytes(a.M, a.rank));
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
@@ -330,7 +335,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&tb.full[i], 1);
       mbar_init(&tb.rows_full[i], 32);  // the row producer's lanes
-      mbar_init(&tb.empty[i], kConsumerWarps);
+      mbar_init(&tb.empty[i], LoraTeam::kWarps);
     }
     mbar_init(&tb.s_ready, kSideThreads);
     fence_barrier_init();
@@ -406,9 +411,9 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
     });
   };
 
-  if (warp >= kConsumerWarps) {
-    give_registers<kProducerRegs>();
-    if (warp == kWeightWarp) {
+  if (warp >= LoraTeam::kWarps) {
+    give_registers<LoraTeam::kProducerRegs>();
+    if (warp == LoraTeam::kWeightWarp) {
       if (lane == 0) {
         const uint64_t policy = l2_policy(-1);
         Cursor c;
@@ -451,7 +456,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         drain(tb.full, ring.stages, c, issued, a.timeout_ns);
       }
       __syncwarp();
-    } else if (warp == kRowWarp) {
+    } else if (warp == LoraTeam::kRowWarp) {
       constexpr int kEl = kIsF32 ? 4 : 2;
       constexpr int kPieces = 2 * kBoxRows * kEl / 16;  // 16-byte pieces of a row
       constexpr int kPitch = kIsF32 ? kRowPitch128F32 : kRowPitch128;
@@ -494,7 +499,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       mbar_arrive(&tb.s_ready);
     }
   } else {
-    take_registers<kConsumerRegs>();
+    take_registers<LoraTeam::kConsumerRegs>();
     bool ok = true, have_s = false, all_started = false;
     // Before the first adapters' stage: S.
     auto take_s = [&] {
@@ -506,7 +511,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       }
       __syncwarp();
     };
-    RedTurn turn{red};
+    RedTurn<WK> turn{red};
     Cursor cur;
     const int first_row = (warp >> 2) * kBoxRows + warp_row<WK>(warp);
     segments([&](int cb, int k0, int k1) {
@@ -532,13 +537,13 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
           __syncwarp();
           if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
         } else if constexpr (kIsF32) {
-          multiply_f32<NT>(acc, box, warp, lane, smem_u32(rows) + first_row * 4, kRowPitch128F32, a.M, at,
-                           a.K);
+          multiply_f32<NT>(acc, box, warp, lane, smem_u32(rows) + first_row * 4, kRowPitch128F32,
+                           a.M, at, a.K);
           __syncwarp();
           if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
         } else {
           Weights<WK> w;
-          Frag<WK, NT, false> f;
+          Frag<NT, false> f;
           w.load(box, warp, lane);
           f.load_rows(rows, kRowPitch128, first_row / 32, at, a.K, lane);
           __syncwarp();
@@ -550,13 +555,12 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       const bool whole = k0 == 0 && k1 == steps;
       float2* mine = reinterpret_cast<float2*>(
           a.part + (static_cast<int64_t>(me) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
-      constexpr int kMine = (P::kCount + kConsumers - 1) / kConsumers;  // places of a row tile
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (8 * j >= a.M) break;
-        float2 extra[kMine];  // loaded before the warps' sums meet
+        float2 extra[P::kMine];  // loaded before the warps' sums meet
 #pragma unroll
-        for (int q = 0; q < kMine; ++q) {
+        for (int q = 0; q < P::kMine; ++q) {
           const int i = tid + q * kConsumers;
           extra[q] = whole ? load_addend<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i))
                            : make_float2(0.0f, 0.0f);
@@ -565,7 +569,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         put_tile<WK, NT>(sums, acc, j, warp, lane);
         named_bar_sync(kBarConsumers, kConsumers);
 #pragma unroll
-        for (int q = 0; q < kMine; ++q) {
+        for (int q = 0; q < P::kMine; ++q) {
           const int i = tid + q * kConsumers;
           float2 v = take_pair<WK>(sums, -1, P::row(i), P::col(i));
           v.x += extra[q].x;
@@ -580,7 +584,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         if (!all_started && tid == 0) (void)spin_until(&a.bar[0], G, a.timeout_ns, a.err);
         __syncwarp();
         all_started = true;  // (thread 0 counts the arrivals)
-        if (last_to_finish(a.counters + first, last - first + 1, tid, &tb.flag)) {
+        if (last_to_finish<kConsumers>(a.counters + first, last - first + 1, tid, &tb.flag)) {
           constexpr int kChunk = 8;
           const int limit = (a.M + 7) / 8 * P::kCount;
           for (int i0 = tid; i0 < limit; i0 += kChunk * kConsumers) {
@@ -590,7 +594,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
               const int i = i0 + q * kConsumers;
               v[q] = load_addend<kIsF32>(a, P::row(i), cb * S::kCols + P::col(i));
             }
-            add_shares(v, a.part, a.part_floats, first, last, i0, limit);
+            add_shares<kConsumers>(v, a.part, a.part_floats, first, last, i0, limit);
 #pragma unroll
             for (int q = 0; q < kChunk; ++q) {
               const int i = i0 + q * kConsumers;

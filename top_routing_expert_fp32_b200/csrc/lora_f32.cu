@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   if (ad < 0) return;
   const int per_row = rank / 4, subs = kShrinkThreads / per_row;
-  const int v = static_cast<int>(threadIdx.x) % per_row, sub = static_cast<int>(threadIdx.x) / per_row;
+  const int tid = static_cast<int>(threadIdx.x), v = tid % per_row, sub = tid / per_row;
   if (sub < subs) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = sub; k0 < K; k0 += subs * kRun) {
@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kThreads)
       xs[k + 3][r] = x.w;
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k0 + tr < K && n0 + tc * 4 < N)
-        w = __ldg(reinterpret_cast<const float4*>(W + static_cast<int64_t>(k0 + tr) * N + n0 + tc * 4));
+        w = __ldg(reinterpret_cast<const float4*>(W + static_cast<int64_t>(k0 + tr) * N + n0 +
+                                                  tc * 4));
       *reinterpret_cast<float4*>(&ws[tr][tc * 4]) = w;
     }
     __syncthreads();

@@ -718,9 +718,10 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int at = 8 * v + 2 * x;
-                ra[at] = __float_as_uint(__uint_as_float(ra[at]) + bf16_bits_to_float(ew[x] & 0xFFFFu));
-                ra[at + 1] =
-                    __float_as_uint(__uint_as_float(ra[at + 1]) + bf16_bits_to_float(ew[x] >> 16));
+                const float e0 = bf16_bits_to_float(ew[x] & 0xFFFFu);
+                const float e1 = bf16_bits_to_float(ew[x] >> 16);
+                ra[at] = __float_as_uint(__uint_as_float(ra[at]) + e0);
+                ra[at + 1] = __float_as_uint(__uint_as_float(ra[at + 1]) + e1);
               }
             }
           }

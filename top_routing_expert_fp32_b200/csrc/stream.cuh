@@ -37,14 +37,6 @@ namespace stream {
 
 enum WeightKind { kBF16 = 0, kF32 = 1, kW8 = 2 };
 
-constexpr int kConsumerWarps = 8;
-constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kWeightWarp = kConsumerWarps, kRowWarp = kConsumerWarps + 1;
-constexpr int kThreads = kConsumers + 128;  // + the producers' warpgroup
-// Registers: 384 threads start with 168 each (64512 in all); the producers' warpgroup hands some
-// to the consumers': 256 x 216 + 128 x 72 = 64512.
-constexpr int kConsumerRegs = 216, kProducerRegs = 72;
-static_assert(kConsumers * kConsumerRegs + 128 * kProducerRegs <= 168 * kThreads, "registers");
 constexpr int kBoxRows = 64;               // one TMA box: 64 k-rows of 128 bytes, swizzled
 constexpr int kBoxBytes = kBoxRows * 128;
 constexpr int kStageBytes = 4 * kBoxBytes;
@@ -56,33 +48,60 @@ constexpr int kInFlight = 3;               // stages of weights under way at onc
 constexpr int kTileBytes = 4096;
 constexpr int kRowPitch = 144, kRowPitchF32 = 256;
 constexpr int kMaxRows = 64;     // activation rows of one call
-constexpr int kTileRows = 32;    // activation rows of one product (up to four tiles of 8)
 constexpr int kMaxGrid = 148;    // blocks (one per SM)
 constexpr int kBarConsumers = 1, kBarAll = 2, kBarRows = 3, kBarSide = 4;  // named barriers
 
 // A stage is four boxes: two side by side (kCols output columns) times either two matrices with
-// the same 64 k-rows, or 128 k-rows of one matrix. Warp w takes box w/2; for 16- and 32-bit
-// weights the (w%2)-th half of its k-rows, for 8-bit weights the (w%2)-th half of its columns.
-// Either way a warp sums kSeg columns.
+// the same 64 k-rows, or 128 k-rows of one matrix. A box's warps each take 32 of its k-rows and a
+// segment of kSeg columns: two warps for 16- and 32-bit weights, four for 8-bit ones, whose
+// conversion to bf16 is what their warps spend their time on (Mixtral-shaped layer, 8 tokens: 300 us
+// with 8 warps, 245 with 16). kPieceRows: activation rows of one
+// product (tiles of 8); more are multiplied in a second pass over the weights. It is what the
+// registers hold without spilling: a spill costs an L2 access here, since the ring leaves the L1
+// cache almost nothing (8-bit weights, 32 tokens: 1300 us with pieces of 32 rows, 359 us of 16).
 template <int WK>
 struct Shape;
 template <>
 struct Shape<kBF16> {
-  static constexpr int kCols = 128, kBoxCols = 64, kSeg = 64, kGroups = 1;  // 32-row groups
+  static constexpr int kCols = 128, kBoxCols = 64, kSeg = 64, kBoxWarps = 2, kPieceRows = 32;
 };
 template <>
 struct Shape<kF32> {
-  static constexpr int kCols = 64, kBoxCols = 32, kSeg = 32, kGroups = 1;
+  static constexpr int kCols = 64, kBoxCols = 32, kSeg = 32, kBoxWarps = 2, kPieceRows = 32;
 };
 template <>
 struct Shape<kW8> {
-  static constexpr int kCols = 256, kBoxCols = 128, kSeg = 64, kGroups = 2;
+  static constexpr int kCols = 256, kBoxCols = 128, kSeg = 64, kBoxWarps = 4, kPieceRows = 16;
 };
 
-// First k-row of a warp within its box, and its first column segment within the tile.
+// The block: consumer warps, then a warpgroup whose first two warps produce weights and rows. The
+// register file is shared out again after the start: the producers' warpgroup hands some of its
+// registers to the consumers (threads x registers at the start = the two parts' sum).
+template <int WK>
+struct Team {
+  static constexpr int kWarps = 4 * Shape<WK>::kBoxWarps;
+  static constexpr int kConsumers = kWarps * 32;
+  static constexpr int kWeightWarp = kWarps, kRowWarp = kWarps + 1;
+  static constexpr int kThreads = kConsumers + 128;
+  static constexpr int kStartRegs = kWarps == 8 ? 168 : 96;
+  static constexpr int kConsumerRegs = kWarps == 8 ? 216 : 104;
+  static constexpr int kProducerRegs = kWarps == 8 ? 72 : 64;
+  static_assert(kConsumers * kConsumerRegs + 128 * kProducerRegs <= kStartRegs * kThreads &&
+                kStartRegs * kThreads <= 65536, "registers");
+};
+
+// A consumer warp's box, its first k-row there (0 or 32) and its segment of the box's columns.
+template <int WK>
+__device__ __forceinline__ int box_of(int warp) {
+  return warp / Shape<WK>::kBoxWarps;
+}
 template <int WK>
 __device__ __forceinline__ int warp_row(int warp) {
-  return WK == kW8 ? 0 : (warp & 1) * 32;
+  return (WK == kW8 ? (warp >> 1) & 1 : warp & 1) * 32;
+}
+template <int WK>
+__device__ __forceinline__ int warp_seg(int warp) {
+  return WK == kW8 ? warp & 1 : 0;
 }
 
 // The stages of a product, `tiles` of `steps` each, over at most `blocks` blocks: block c takes
@@ -153,15 +172,26 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two int8 values in the low bytes of the two halves -> two bf16, exactly. For a byte b,
-// bf16 0x4300 | (b & 127) is 128 + (b & 127) and 0x4300 | (b & 128) is 128 or, for negative b,
+// (v & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_difference(uint32_t x, uint32_t y) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
+  return d;
+}
+// Four int8 values -> bf16, exactly: bytes 0 and 2 to `even`, bytes 1 and 3 to `odd`. For a byte
+// b, bf16 0x4300 | (b & 127) is 128 + (b & 127) and 0x4300 | (b & 128) is 128 or, for negative b,
 // 256; their difference is b.
-__device__ __forceinline__ uint32_t i8x2_to_bf16x2(uint32_t v) {
-  const uint32_t lo = (v & 0x007F007Fu) | 0x43004300u;
-  const uint32_t hi = (v & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&hi));
-  return *reinterpret_cast<const uint32_t*>(&d);
+__device__ __forceinline__ void i8x4_to_bf16(uint32_t v, uint32_t& even, uint32_t& odd) {
+  const uint32_t u = v >> 8;
+  even = bf16x2_difference(and_or(v, 0x007F007Fu, 0x43004300u),
+                           and_or(v, 0x00800080u, 0x43004300u));
+  odd = bf16x2_difference(and_or(u, 0x007F007Fu, 0x43004300u),
+                          and_or(u, 0x00800080u, 0x43004300u));
 }
 
 // fp32 sums of one warp: kSeg columns by 8*NT rows.
@@ -177,52 +207,48 @@ struct Acc {
   }
 };
 
-// One thread's activation values of one stage: for each 32-row group and row tile the pairs of
-// the four blocks; with SPLIT each value is the sum of two bf16 terms (planes 0 and 1).
-template <int WK, int NT, bool SPLIT>
+// One thread's activation values of 32 k: for each row tile the pairs of the four blocks; with
+// SPLIT each value is the sum of two bf16 terms (planes 0 and 1).
+template <int NT, bool SPLIT>
 struct Frag {
-  uint32_t r[Shape<WK>::kGroups][NT][SPLIT ? 2 : 1][4];
+  uint32_t r[NT][SPLIT ? 2 : 1][4];
 
-  // From operand order: `rows` of the stage, its first group (0..3) for this warp.
+  // From operand order: `rows` of the stage, 32-value group 0..3.
   __device__ __forceinline__ void load_ordered(const uint8_t* rows, int group, int lane) {
     static_assert(SPLIT, "two planes");
 #pragma unroll
-    for (int g = 0; g < Shape<WK>::kGroups; ++g)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint4 v = *reinterpret_cast<const uint4*>(rows + j * kTileBytes +
-                                                          (group + g) * 1024 + q * 512 + lane * 16);
-          r[g][j][q][0] = v.x;
-          r[g][j][q][1] = v.y;
-          r[g][j][q][2] = v.z;
-          r[g][j][q][3] = v.w;
-        }
+      for (int q = 0; q < 2; ++q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(rows + j * kTileBytes + group * 1024 +
+                                                        q * 512 + lane * 16);
+        r[j][q][0] = v.x;
+        r[j][q][1] = v.y;
+        r[j][q][2] = v.z;
+        r[j][q][3] = v.w;
+      }
   }
 
   // From plain rows: thread t of quad `lane / 4` reads the 16 bytes of its four pairs, block b
-  // takes pair (b + t) & 3. k0: the warp's first k of the stage within the reduction of K (past
-  // its end nothing was copied: zeros); `group`: the warp's first 32-value group in the rows.
+  // takes pair (b + t) & 3. `group`: 32-value group in the rows; k0: its first k within the
+  // reduction of K (past its end nothing was copied: zeros).
   __device__ __forceinline__ void load_rows(const uint8_t* rows, int row_pitch, int group, int k0,
                                             int K, int lane) {
     static_assert(!SPLIT, "one plane");
     const int t = lane & 3;
     const bool one = (t & 1) != 0, two = (t & 2) != 0;
 #pragma unroll
-    for (int g = 0; g < Shape<WK>::kGroups; ++g)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint4 v = *reinterpret_cast<const uint4*>(rows + (8 * j + (lane >> 2)) * row_pitch +
-                                                  (group + g) * 64 + t * 16);
-        if (k0 + 32 * g + 8 * t >= K) v = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
-                       a3 = one ? v.x : v.w;
-        r[g][j][0][0] = two ? a2 : a0;
-        r[g][j][0][1] = two ? a3 : a1;
-        r[g][j][0][2] = two ? a0 : a2;
-        r[g][j][0][3] = two ? a1 : a3;
-      }
+    for (int j = 0; j < NT; ++j) {
+      uint4 v = *reinterpret_cast<const uint4*>(rows + (8 * j + (lane >> 2)) * row_pitch +
+                                                group * 64 + t * 16);
+      if (k0 + 8 * t >= K) v = make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
+                     a3 = one ? v.x : v.w;
+      r[j][0][0] = two ? a2 : a0;
+      r[j][0][1] = two ? a3 : a1;
+      r[j][0][2] = two ? a0 : a2;
+      r[j][0][3] = two ? a1 : a3;
+    }
   }
 };
 
@@ -232,36 +258,33 @@ __device__ __forceinline__ uint32_t block_row(int b, int i) {
   return static_cast<uint32_t>(8 * t + 2 * ((b + t) & 3) + (i & 1));
 }
 
-// This warp's weights of one stage, as the transposed loads deliver them: registers, so that the
+// A warp's weights of one stage, as the transposed loads deliver them: registers, so that the
 // stage can be handed back before the arithmetic.
 template <int WK>
 struct Weights {
-  uint32_t r[8][4];
+  uint32_t r[WK == kBF16 ? 8 : 4][4];
   // `box`: shared address of the warp's box.
   __device__ __forceinline__ void load(uint32_t box, int warp, int lane) {
     const int b = lane >> 3, i = lane & 7;
+    const uint32_t rows = box + static_cast<uint32_t>(warp_row<WK>(warp)) * 128;
     if constexpr (WK == kBF16) {
       // Matrices of one load: (column halves lo, hi) x (blocks 2s, 2s + 1).
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const uint32_t k = block_row(2 * s + (b >> 1), i);
-        const uint32_t row = box + (static_cast<uint32_t>(warp & 1) * 32 + k) * 128;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          ldsm_x4_trans(row + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (k & 7u)) << 4),
+          ldsm_x4_trans(rows + k * 128 + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (k & 7u)) << 4),
                         r[s * 4 + m]);
       }
     } else {
-      // One load takes 16 columns (bytes) of all four blocks of a 32-row group.
+      // One load takes 16 columns (bytes) of all four blocks.
       const uint32_t k = block_row(b, i);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t row = box + (static_cast<uint32_t>(g) * 32 + k) * 128;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          ldsm_x4_trans(row + ((static_cast<uint32_t>((warp & 1) * 4 + m) ^ (k & 7u)) << 4),
-                        r[g * 4 + m]);
-      }
+      for (int m = 0; m < 4; ++m)
+        ldsm_x4_trans(rows + k * 128 +
+                          ((static_cast<uint32_t>(warp_seg<WK>(warp) * 4 + m) ^ (k & 7u)) << 4),
+                      r[m]);
     }
   }
 };
@@ -269,42 +292,35 @@ struct Weights {
 // acc += weights^T x rows.
 template <int WK, int NT, bool SPLIT>
 __device__ __forceinline__ void multiply(Acc<WK, NT>& acc, const Weights<WK>& w,
-                                         const Frag<WK, NT, SPLIT>& f) {
+                                         const Frag<NT, SPLIT>& f) {
   constexpr int kPlanes = SPLIT ? 2 : 1;
-  if constexpr (WK == kBF16) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+  for (int s = 0; s < 2; ++s) {
+    if constexpr (WK == kBF16) {
 #pragma unroll
       for (int q = 0; q < kPlanes; ++q)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int m = 0; m < 4; ++m)
-            mma_bf16(&acc.v[(m * NT + j) * 4], w.r[s * 4 + m], f.r[0][j][q][2 * s],
-                     f.r[0][j][q][2 * s + 1]);
-  } else {
-    // As 16-bit elements, a transposed 8x8 matrix gives each thread the bytes of columns 2g and
-    // 2g+1 at its pair of k; the even columns take the instruction's rows 0-7 and the odd ones
-    // rows 8-15.
+            mma_bf16(&acc.v[(m * NT + j) * 4], w.r[s * 4 + m], f.r[j][q][2 * s],
+                     f.r[j][q][2 * s + 1]);
+    } else {
+      // As 16-bit elements, a transposed 8x8 matrix gives each thread the bytes of columns 2g and
+      // 2g+1 at its pair of k; the even columns take the instruction's rows 0-7 and the odd ones
+      // rows 8-15.
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
+      for (int m = 0; m < 4; ++m) {
+        uint32_t a[4];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int h = 0; h < 2; ++h) i8x4_to_bf16(w.r[m][2 * s + h], a[2 * h], a[2 * h + 1]);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          uint32_t a[4];
+        for (int q = 0; q < kPlanes; ++q)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t v = w.r[g * 4 + m][2 * s + h];
-            a[2 * h] = i8x2_to_bf16x2(v & 0x00FF00FFu);
-            a[2 * h + 1] = i8x2_to_bf16x2((v >> 8) & 0x00FF00FFu);
-          }
-#pragma unroll
-          for (int q = 0; q < kPlanes; ++q)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[g][j][q][2 * s], f.r[g][j][q][2 * s + 1]);
-        }
+          for (int j = 0; j < NT; ++j)
+            mma_bf16(&acc.v[(m * NT + j) * 4], a, f.r[j][q][2 * s], f.r[j][q][2 * s + 1]);
+      }
+    }
   }
 }
 
@@ -364,17 +380,21 @@ __device__ __forceinline__ void multiply_f32(Acc<kF32, NT>& acc, uint32_t box, i
 
 // The warps' sums of one row tile meet in shared memory: red[warp][8 rows][kRedPitch]. The
 // pitch keeps both the fragment-shaped writes and the row-shaped reads free of bank conflicts.
-// Two such buffers in turn (RedTurn): one barrier per row tile, since a thread that writes a
-// buffer again has passed the barrier of the other one, and with it every read of this one.
+// With eight warps two such buffers in turn: one barrier per row tile, since a thread that writes
+// a buffer again has passed the barrier of the other one, and with it every read of this one.
+// Sixteen warps have one buffer of the same bytes and a second barrier after the reads.
 constexpr int kRedPitch = 68;
-constexpr int kRedFloats = kConsumerWarps * 8 * kRedPitch;
-constexpr size_t kRedBytes = 2 * sizeof(float) * kRedFloats;
+constexpr size_t kRedBytes = 16 * 8 * kRedPitch * sizeof(float);
+template <int WK>
 struct RedTurn {
   float* base;
   int turn = 0;
   __device__ float* next() {
-    turn ^= 1;
-    return base + turn * kRedFloats;
+    if (Team<WK>::kWarps == 8) turn ^= 1;
+    return base + turn * (8 * 8 * kRedPitch);
+  }
+  __device__ void done() {
+    if (Team<WK>::kWarps != 8) named_bar_sync(kBarConsumers, Team<WK>::kConsumers);
   }
 };
 
@@ -410,6 +430,7 @@ template <int WK>
 struct Places {
   static constexpr int kPairs = Shape<WK>::kCols / 2;
   static constexpr int kCount = 8 * kPairs;
+  static constexpr int kMine = (kCount + Team<WK>::kConsumers - 1) / Team<WK>::kConsumers;
   __device__ static int row(int i) { return i / kPairs; }
   __device__ static int col(int i) { return 2 * (i % kPairs); }
 };
@@ -418,15 +439,15 @@ struct Places {
 // `branch` (0, 1) of a two-matrix stage, or of all (branch < 0).
 template <int WK>
 __device__ __forceinline__ float2 take_pair(const float* red, int branch, int row, int col) {
-  const int seg = col / Shape<WK>::kSeg, in = col % Shape<WK>::kSeg;
+  const int box = col / Shape<WK>::kBoxCols, seg = col % Shape<WK>::kBoxCols / Shape<WK>::kSeg;
+  const int in = col % Shape<WK>::kSeg;
   float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (branch >= 0 && half != branch) continue;
-    // 16/32-bit: segment = box of the pair, two warps each; 8-bit: segment = warp.
 #pragma unroll
-    for (int q = 0; q < (WK == kW8 ? 1 : 2); ++q) {
-      const int w = half * 4 + (WK == kW8 ? seg : seg * 2 + q);
+    for (int q = 0; q < 2; ++q) {  // the two halves of the box's k-rows
+      const int w = (half * 2 + box) * Shape<WK>::kBoxWarps + (WK == kW8 ? q * 2 + seg : q);
       const float2 v = *reinterpret_cast<const float2*>(red + (w * 8 + row) * kRedPitch + in);
       s.x += v.x;
       s.y += v.y;
@@ -453,6 +474,7 @@ __device__ __forceinline__ bool spin_until(int* bar, int target, uint64_t timeou
 
 // All consumer threads of every block: arrive, wait until `target` arrivals (bounded). The
 // block's earlier global writes are visible to the others afterwards. False: the wait ran out.
+template <int kConsumers>
 __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int* flag,
                                              uint64_t timeout_ns, int* err) {
   named_bar_sync(kBarConsumers, kConsumers);
@@ -468,6 +490,7 @@ __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int*
 
 // One arrival per block that shares a tile; true in the block that arrives last (its threads
 // then see what the others wrote before arriving).
+template <int kConsumers>
 __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid, int* flag) {
   named_bar_sync(kBarConsumers, kConsumers);
   if (tid == 0) {
@@ -485,7 +508,7 @@ __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid,
 // v[c] += the shares that blocks first..last hold of place i0 + c * kConsumers (< limit), in block
 // order. `part`: [grid][2][part_floats]; a tile's first block holds its share in the second
 // half. All loads of one block are independent: one L2 latency per block, not per value.
-template <int C>
+template <int kConsumers, int C>
 __device__ __forceinline__ void add_shares(float2 (&v)[C], const float* part, int64_t part_floats,
                                            int first, int last, int i0, int limit) {
   for (int b = first; b <= last; ++b) {
