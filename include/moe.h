@@ -139,8 +139,8 @@ moe_status moe_capacity(const moe_problem* p, int64_t* C);
  * all of them). The workspace holds the device error word, scratch counters, the router's
  * bf16 operand (bf16 X with more than 16 experts: the three bf16 terms of W_r, written by each
  * router call) and, for moe_forward, the intermediate buffers (routing results, X_perm, H,
- * Y), and for problems of at most MOE_FEW_MAX_TOKENS tokens moe_forward_few's partial sums and
- * intermediate activations. */
+ * Y) or, in their place, moe_forward_few's partial sums and intermediate activations. It grows
+ * with N: a workspace also serves the same problem with fewer tokens, for every entry point. */
 moe_status moe_workspace_size(const moe_problem* p, size_t* bytes);
 
 /* Router + softmax + top-k + gates (Grok-1 book 5.2, 5.2.3; walkthrough 1.1, 1.2;
@@ -330,18 +330,21 @@ moe_status moe_forward_ex(const moe_problem* p, const void* X, const float* W_r,
 /* ---- The layer for a few tokens (token-by-token generation): one launch for the whole layer. */
 #define MOE_FEW_MAX_TOKENS 64
 /* moe_forward for N <= MOE_FEW_MAX_TOKENS in one cooperative kernel: the same layer, arguments
- * and optional exports, with the experts' weights streamed once through the SMs instead of
- * tiles of 128 rows (Grok-1 book 5.2, 5.3.5; LLMs-from-scratch 12.1, 12.2; walkthrough 1.1-3.2).
+ * and optional exports, with the experts' weights streamed through the SMs instead of tiles of
+ * 128 rows (Grok-1 book 5.2, 5.3.5; LLMs-from-scratch 12.1, 12.2; walkthrough 1.1-3.2): once for
+ * an expert that keeps up to 32 tokens, again for every 32 more (8-bit weights: 16).
  * Differences from moe_forward:
  *   - Logits are fp32 sums in another order, so a selection decided by a gap of a few fp32
  *     roundings may differ; everything after the logits follows the same rules.
  *   - The intermediate activations H keep 16 bits of mantissa (two bf16 terms) and the k
- *     contributions are summed in fp32 without rounding Y: the output is rounded once.
+ *     contributions are summed in fp32 without rounding Y: the output is rounded once. (Weights
+ *     must be finite: an infinite one may give NaN where moe_forward gives infinity.)
  *   - Nothing of moe_forward's intermediates (row_token, X_perm, H, Y) is written.
  * More than 64 tokens: MOE_ERR_UNSUPPORTED. Needs routing_mode = TOPK. out must not overlap any
  * input. The kernel needs every SM of the device to itself at once (a cooperative launch of one
  * block per SM): it starts when the SMs have room, and the device must not be shared with a
- * kernel that never ends. Workspace: moe_workspace_size bytes. Deterministic. */
+ * kernel that never ends. Workspace: moe_workspace_size bytes; calls that may run at the same time
+ * need one each. Deterministic. */
 moe_status moe_forward_few(const moe_problem* p, const void* X, const float* W_r,
                            const float* bias, const void* W1, const void* W2, const void* W3,
                            void* out, float* logits, int32_t* topk_idx, float* topk_gate,
@@ -379,16 +382,17 @@ typedef struct {
 } moe_lora_problem;
 
 /* Host only. Workspace bytes of moe_lora_forward (initialise its header once with
- * moe_workspace_init, as every workspace). It grows with M: a workspace serves any problem
- * whose size is at most its own. */
+ * moe_workspace_init, as every workspace). It grows with M: a workspace also serves the same
+ * problem with fewer rows. Calls that may run at the same time need one each. */
 moe_status moe_lora_workspace_size(const moe_lora_problem* p, size_t* bytes);
 
 /* adapter[m] = -1: the row takes no adapter (A and B are not read for it). A value outside
  * [-1, L) is recorded as MOE_DEVERR_BAD_INDEX and treated as -1. scale may be NULL (1 for
  * every adapter). addend may be NULL; it may be Y itself (Y += ...), otherwise Y must not
  * overlap any input. Rows may come in any order; adjacent rows of one adapter share its reads.
- *   At most 64 rows: one cooperative kernel that streams W once; X A, the adapters' part and
- *   all sums in fp32, one rounding to the output type (one block per SM, as moe_forward_few).
+ *   At most 64 rows: one cooperative kernel that streams W once (one block per SM, as
+ *   moe_forward_few); X A and all sums in fp32, for bf16 scale (X A) as two bf16 terms (16 bits
+ *   of mantissa) in the product with B (which must be finite), one rounding to the output type.
  *   More rows, bf16: X A in fp32, rounded to bf16 with its scale, and one tcgen05 product over
  *   [X, X A] with fp32 accumulation. Its cost grows with the number of different adapters
  *   among each 256 adjacent rows. More rows, fp32: CUDA cores.

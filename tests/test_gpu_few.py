@@ -212,6 +212,67 @@ def test_graph_replay_and_other_stream(abi):
     assert abi.device_error(ws) == 0
 
 
+def test_two_streams_at_once(abi):
+    # Calls on two streams, one of high priority, with a workspace each and other kernels beside
+    # them: every call's own result, no wait that runs out.
+    cfg = _cfg("pair", 5, 512, 1024, 8, 2)
+    inp = inputs.make_inputs(cfg, "cuda")
+    want, _ = _run(abi, cfg, inp)
+    p = abi.problem(cfg)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(priority=-1)]
+    ws = [abi.workspace(p) for _ in streams]
+    outs = [[torch.empty_like(inp.X) for _ in range(20)] for _ in streams]
+    big = [torch.randn((2048, 2048), device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, w, out, b in zip(streams, ws, outs, big):
+            with torch.cuda.stream(s):
+                b.mul_(0.5)
+                abi.forward_few(p, inp.X, inp.W_r, inp.bias, inp.W1, inp.W2, inp.W3, out[i], w)
+    torch.cuda.synchronize()
+    assert all(abi.device_error(w) == 0 for w in ws)
+    assert all(torch.equal(o, want) for out in outs for o in out)
+
+
+def test_a_larger_batch_s_workspace(abi):
+    # One workspace for a server's largest batch, used by both forms of the layer in turn.
+    cfg = _cfg("largest", 200, 128, 256, 8, 2)
+    small = cfg.with_(N=20)
+    ws = abi.workspace(abi.problem(cfg))
+    inp, few = inputs.make_inputs(cfg, "cuda"), inputs.make_inputs(small, "cuda")
+    want, _ = _run(abi, small, few)
+    p = abi.problem(cfg)
+    alone, out = torch.empty_like(inp.X), torch.empty_like(inp.X)
+    abi.forward(p, inp.X, inp.W_r, inp.bias, inp.W1, inp.W2, inp.W3, alone, ws)
+    for _ in range(2):
+        got, _ = _run(abi, small, few, ws=ws)
+        assert torch.equal(got, want)
+        abi.forward(p, inp.X, inp.W_r, inp.bias, inp.W1, inp.W2, inp.W3, out, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, alone)
+
+
+def test_activations_past_the_bf16_range(abi):
+    # h = 3.394e38 lies between the largest bf16 (3.3895e38) and the largest fp32 value, and rounds
+    # to an infinite bf16 term: infinity, not NaN. GELU of a large value is the value itself.
+    cfg = _cfg("edge", 1, 8, 8, 1, 1, act=configs.ACT_GELU_ERF)
+    X = torch.zeros((1, 8), dtype=torch.bfloat16, device="cuda")
+    X[0, 0] = 1.0
+    X[0, 1] = 2.0 ** -10
+    W1 = torch.zeros((1, 8, 8), dtype=torch.bfloat16, device="cuda")
+    W2, W3 = torch.zeros_like(W1), torch.zeros_like(W1)
+    W1[0, 0, 0] = 2.0 ** 64
+    # x W2 = 2^64 (1 - 2^-9 + 2^-12), exact in fp32.
+    W2[0, 0, 0] = 255.0 / 256 * 2.0 ** 64
+    W2[0, 1, 0] = (2.0 ** -9 + 2.0 ** -12) * 2.0 ** 74
+    W3[0, 0] = 1.0
+    h = 2.0 ** 64 * float(W2[0, 0, 0].float() + W2[0, 1, 0].float() * 2.0 ** -10)
+    assert torch.finfo(torch.bfloat16).max < h < torch.finfo(torch.float32).max
+    W_r = torch.zeros((8, 1), device="cuda")
+    out, _ = _run(abi, cfg, inputs.MoEInputs(X, W_r, None, W1, W2, W3))
+    assert (out == float("inf")).all()
+
+
 def test_a_nan_token_leaves_the_others_alone(abi):
     # Non-finite inputs are unsupported, but a bad token must not reach the other rows.
     cfg = _cfg("nan", 12, 72, 104, 2, 1)

@@ -198,6 +198,35 @@ def test_graph_replay_and_other_stream(abi, M):
     assert abi.device_error(ws) == 0
 
 
+@pytest.mark.parametrize("M", [4, 200])
+def test_two_streams_at_once(abi, M):
+    # Calls on two streams, one of high priority, with a workspace each: every call's own result.
+    c = Case(M, 1024, 2048, 5, 16)
+    want = c.run(abi)
+    p = abi.lora_problem(c.M, c.K, c.N, c.L, c.r, c.dtype)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(priority=-1)]
+    ws = [abi.lora_workspace(p) for _ in streams]
+    outs = [[torch.empty_like(want) for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, w, out in zip(streams, ws, outs):
+            with torch.cuda.stream(s):
+                abi.lora_forward(p, c.X, c.W, c.A, c.B, c.adapter, out[i], w, scale=c.scale)
+    torch.cuda.synchronize()
+    assert all(abi.device_error(w) == 0 for w in ws)
+    assert all(torch.equal(o, want) for out in outs for o in out)
+
+
+def test_a_larger_batch_s_workspace(abi):
+    # One workspace for a server's largest batch, whatever path a batch takes.
+    big, small = Case(300, 256, 384, 3, 16), Case(20, 256, 384, 3, 16, seed=1)
+    want, want_small = big.run(abi), small.run(abi)
+    ws = abi.lora_workspace(abi.lora_problem(300, 256, 384, 3, 16, BF16))
+    for _ in range(2):
+        assert torch.equal(small.run(abi, ws=ws), want_small)
+        assert torch.equal(big.run(abi, ws=ws), want)
+
+
 def test_no_rows(abi):
     c = Case(0, 64, 64, 2, 8)
     assert c.run(abi, Y=torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")).numel() == 0

@@ -76,3 +76,12 @@ def test_workspace_grows_with_the_rows(abi):
     for dtype in (configs.DTYPE_BF16, configs.DTYPE_F32):
         sizes = [_size(abi, _p(abi, M=m, dtype=dtype, K=4096))[1] for m in (65, 128, 700, 4096)]
         assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(dtype=configs.DTYPE_F32), dict(K=14336, rank=128),
+                                dict(N=4096)])
+def test_a_workspace_serves_every_smaller_batch(abi, kw):
+    sizes = [_size(abi, _p(abi, M=m, **kw))[1]
+             for m in (0, 1, 3, 4, 5, 8, 9, 31, 32, 37, 63, 64, 65, 127, 128, 129, 256, 511, 512,
+                       1000, 2304, 2305, 2560, 4096, 18432, 18433, 20000)]
+    assert sizes == sorted(sizes)

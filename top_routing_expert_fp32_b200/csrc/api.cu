@@ -1,6 +1,7 @@
 // C ABI of the MoE FFN forward library (declared in include/moe.h): argument validation,
 // workspace layout, and the enqueueing of the kernels in the pages' order
 // (route -> dispatch -> expert FFN -> combine).
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -128,7 +129,10 @@ Layout make_layout(const moe_problem& p) {
   L.xperm = take(es * R * static_cast<size_t>(p.D));
   L.h = take(es * R * static_cast<size_t>(p.F));
   L.y = take(es * R * static_cast<size_t>(p.D));
-  L.few = take(few_workspace_bytes(p));
+  // moe_forward_few's scratch shares the intermediates' place. Larger batches count it too (for 64
+  // tokens), so that a workspace also serves every smaller batch.
+  L.few = L.idx;
+  o = std::max(o, align256(L.few + few_workspace_bytes(p)));
   L.total = o;
   L.xin = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
   L.xout = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
@@ -421,12 +425,15 @@ moe_status check_lora(const moe_lora_problem* p) {
   return MOE_OK;
 }
 
-// Header, then the scratch of the path that M takes.
+// Header, then the scratch of the path that M takes, and at least what fewer rows take, so that a
+// workspace also serves every smaller batch.
 size_t lora_bytes(const moe_lora_problem& p) {
   if (p.M == 0) return 256;
-  return 256 + align256(p.M <= kLoraFewRows         ? lora_few_workspace_bytes(p)
-                        : p.dtype == MOE_DTYPE_BF16 ? lora_sm100_workspace_bytes(p)
-                                                    : lora_f32_workspace_bytes(p));
+  size_t scratch = lora_few_workspace_bytes(p);
+  if (p.M > kLoraFewRows)
+    scratch = std::max(scratch, p.dtype == MOE_DTYPE_BF16 ? lora_sm100_workspace_bytes(p)
+                                                          : lora_f32_workspace_bytes(p));
+  return 256 + align256(scratch);
 }
 
 moe_status few_impl(const moe_problem& p, const FewTensors& t, void* ws, cudaStream_t stream) {

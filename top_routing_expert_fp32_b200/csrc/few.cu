@@ -433,9 +433,9 @@ __device__ __forceinline__ void store_h(const FewArgs& a, const Part& pt, int r,
     const uint32_t hi = pack_bf16x2(h0, h1);
     const float r0 = h0 - bf16_bits_to_float(hi & 0xFFFFu);
     const float r1 = h1 - bf16_bits_to_float(hi >> 16);
-    // An infinite value has no remainder.
+    // A value that is infinite, or becomes so in bf16, has no remainder.
     w[0] = hi;
-    w[128] = pack_bf16x2(fabsf(h0) < INFINITY ? r0 : 0.0f, fabsf(h1) < INFINITY ? r1 : 0.0f);
+    w[128] = pack_bf16x2(fabsf(r0) < INFINITY ? r0 : 0.0f, fabsf(r1) < INFINITY ? r1 : 0.0f);
   }
 }
 
@@ -533,8 +533,8 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer<W
 // ---- down: stages [s0, s1) of one piece's part of one column block, added into outacc
 
 template <int WK, int NT>
-__device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer<WK>& c, int s0, int s1,
-                                         const Part pt, int cb, float* outacc) {
+__device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer<WK>& c, int s0,
+                                         int s1, const Part pt, int cb, float* outacc) {
   using S = Shape<WK>;
   using P = Places<WK>;
   constexpr int kConsumers = Team<WK>::kConsumers;
@@ -620,7 +620,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const size_t ring_size = ring_bytes<WK>(a.N, a.E);
   float* red = reinterpret_cast<float*>(smem + ring_size);
-  float* outacc = red + kRedBytes / sizeof(float);  // the logits first, then the column block's sums
+  float* outacc = red + kRedBytes / sizeof(float);  // first logits, then the column block's sums
   Tables& tb = *reinterpret_cast<Tables*>(reinterpret_cast<uint8_t*>(outacc) +
                                           out_bytes<WK>(a.N, a.E));
   const int tid = static_cast<int>(threadIdx.x);
@@ -863,7 +863,8 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       if (!whole) {
         const int first = down.owner(tile * down_steps),
                   last = down.owner(tile * down_steps + down_steps - 1);
-        if (last_to_finish<kConsumers>(a.counters + kMaxGrid + first, last - first + 1, tid, &tb.flag)) {
+        if (last_to_finish<kConsumers>(a.counters + kMaxGrid + first, last - first + 1, tid,
+                                       &tb.flag)) {
           constexpr int kChunk = 8;
           for (int i0 = tid; i0 < a.N * P::kPairs; i0 += kChunk * kConsumers) {
             float2 v[kChunk];
@@ -911,7 +912,8 @@ cudaError_t launch(const moe_problem& p, const FewArgs& a, const void* W1, const
       !make_stream_map(&m3, W3, WK, p.D, p.F, p.E))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(
-      few_kernel<WK, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
+      few_kernel<WK, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min(num_sms(), kMaxGrid)));
@@ -992,13 +994,14 @@ bool make_box_map_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64
 
 // Workspace of moe_forward_few: partial logits, counters, shared-tile sums, H.
 size_t few_workspace_bytes(const moe_problem& p) {
-  if (p.N < 1 || p.N > kMaxRows) return 0;
+  if (p.N < 1) return 0;
+  const int64_t N = std::min<int64_t>(p.N, kMaxRows);
   auto up256 = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const int64_t R = p.N * p.k;
+  const int64_t R = N * p.k;
   // bf16 problems may come with either weight kind: the larger of the two.
   const int kind = p.dtype == MOE_DTYPE_F32 ? kF32 : kW8;
-  return up256(sizeof(float) * kMaxSlices * p.N * p.E) + up256(sizeof(int) * 2 * kMaxGrid) +
-         up256(sizeof(float) * 2 * kMaxGrid * part_floats_of(kind, p.N)) +
+  return up256(sizeof(float) * kMaxSlices * N * p.E) + up256(sizeof(int) * 2 * kMaxGrid) +
+         up256(sizeof(float) * 2 * kMaxGrid * part_floats_of(kind, N)) +
          up256(kind == kF32 ? sizeof(float) * R * h_row_f32(p.F)
                             : static_cast<size_t>((std::min<int64_t>(p.E, R) + R / 8) *
                                                   h_groups(p.F) * kHGroupBytes));

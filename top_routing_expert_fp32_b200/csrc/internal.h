@@ -175,7 +175,7 @@ struct FewTensors {
   uint8_t* dropped;
   float* colsum;
 };
-size_t few_workspace_bytes(const moe_problem& p);
+size_t few_workspace_bytes(const moe_problem& p);  // more tokens: as kFewMaxTokens
 cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors& t, void* scratch,
                        int* err, int* bar, uint64_t timeout_ns, cudaStream_t stream);
 
@@ -195,7 +195,7 @@ struct LoraTensors {
   const void* addend;
   void* Y;
 };
-size_t lora_few_workspace_bytes(const moe_lora_problem& p);
+size_t lora_few_workspace_bytes(const moe_lora_problem& p);  // more rows: as kLoraFewRows
 size_t lora_sm100_workspace_bytes(const moe_lora_problem& p);
 size_t lora_f32_workspace_bytes(const moe_lora_problem& p);
 cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, void* scratch,

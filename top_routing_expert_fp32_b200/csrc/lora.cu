@@ -114,13 +114,12 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
   }
 }
 
-// The side warps' partial S of this block: row blockIdx.x % M over one slice of K; kVec values of
-// a row of A per thread (16 bytes).
+// The side warps' partial S of one row and slice of K (item: row + M * slice); kVec values of a row
+// of A per thread (16 bytes).
 template <bool F32>
-__device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid) {
+__device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid, int item) {
   constexpr int kVec = F32 ? 4 : 8;
-  const int m = static_cast<int>(blockIdx.x) % a.M, slice = static_cast<int>(blockIdx.x) / a.M;
-  if (slice >= a.slices) return;
+  const int m = item % a.M, slice = item / a.M;
   const int ad = tb.adapter[m];
   if (ad < 0) return;  // nobody reads this row's sums
   const int per_row = a.rank / kVec, subs = kSideThreads / per_row;
@@ -167,9 +166,10 @@ __device__ __forceinline__ void put_s(const LoraArgs& a, const LoraTables& tb, u
     __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(S) + at;
     const __nv_bfloat16 h = __float2bfloat16_rn(s);
     *hi = h;
-    // An infinite value has no remainder.
+    // A value that is infinite, or becomes so in bf16, has no remainder.
+    const float rest = s - __bfloat162float(h);
     hi[(a.M + 7) / 8 * 8 * pieces_of(a.rank) * kPieceRanks] =
-        __float2bfloat16_rn(fabsf(s) < INFINITY ? s - __bfloat162float(h) : 0.0f);
+        __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
   }
 }
 
@@ -486,8 +486,10 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
     } else {
       // The side warps: S.
       const int sid = tid - (kConsumers + 64);
-      shrink<kIsF32>(a, tb, sid);
-      named_bar_sync(kBarSide, kSideThreads);
+      for (int item = me; item < a.M * a.slices; item += G) {  // one, where there are SMs enough
+        shrink<kIsF32>(a, tb, sid, item);
+        named_bar_sync(kBarSide, kSideThreads);
+      }
       if (sid == 0) {
         __threadfence();
         atomicAdd(&a.bar[1], 1);
@@ -658,9 +660,9 @@ cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void*
 }  // namespace
 
 size_t lora_few_workspace_bytes(const moe_lora_problem& p) {
-  return up256(sizeof(float) * lora_slices(p.M, p.K) * p.M * p.rank) +
-         up256(sizeof(int) * kMaxGrid) +
-         up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(p.M));
+  const int64_t M = std::min<int64_t>(p.M, kMaxRows);
+  return up256(sizeof(float) * kMaxGrid * p.rank) +  // slices x rows
+         up256(sizeof(int) * kMaxGrid) + up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(M));
 }
 
 cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, void* scratch,
@@ -672,11 +674,10 @@ cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, voi
   a.adapter = t.adapter;
   a.addend = t.addend;
   a.Y = t.Y;
-  const int max_slices = lora_slices(p.M, p.K);  // what the workspace holds
-  a.slices = std::max(1, std::min<int>(max_slices, std::min(num_sms(), kMaxGrid) / p.M));
+  a.slices = lora_slices(p.M, p.K);
   uint8_t* w = static_cast<uint8_t*>(scratch);
   a.part_s = reinterpret_cast<float*>(w);
-  w += up256(sizeof(float) * max_slices * p.M * p.rank);
+  w += up256(sizeof(float) * kMaxGrid * p.rank);
   a.counters = reinterpret_cast<int*>(w);
   w += up256(sizeof(int) * kMaxGrid);
   a.part = reinterpret_cast<float*>(w);

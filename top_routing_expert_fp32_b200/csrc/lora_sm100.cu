@@ -10,7 +10,8 @@
 //      blocks and their warps; each warp streams (adapter of the group, piece of K) steps
 //      through its own TMA ring into mma.m16n8k16 (ranks x rows), the fp32 sums meet through
 //      distributed shared memory. S is rounded to bf16 once, with its scale: it is a
-//      tensor-core operand, and its rounding (2^-9 of the adapter's part) is below the output's.
+//      tensor-core operand, and its rounding (2^-8 of the adapter's part) is no larger than the
+//      output's own.
 //   2. lora_gemm: the product, launched as a programmatic dependent of 1: it waits for S only when
 //      its first tile comes to the extra k-steps, so the shrink hides behind the main loop.
 #include <algorithm>
