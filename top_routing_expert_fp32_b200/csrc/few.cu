@@ -165,18 +165,28 @@ __device__ void partial_logits(const FewArgs& a, float* red, int tid) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
   if (e < a.E) {
-#pragma unroll 8
-    for (int d = d0 + sl; d < d1; d += subs) {
-      const float w = __ldg(a.W_r + static_cast<int64_t>(d) * a.E + e);
+    constexpr int kAtOnce = WK == kW8 ? 2 : 4;  // rows of W_r whose loads are on their way at once
+    for (int d = d0 + sl; d < d1; d += kAtOnce * subs) {
+      float w[kAtOnce], x[kAtOnce][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i < nt) {
-          const int64_t at = static_cast<int64_t>(t0 + i) * a.D + d;
-          const float x = WK == kF32 ? __ldg(static_cast<const float*>(a.X) + at)
-                               : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[at]);
-          acc[i] = fmaf(x, w, acc[i]);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int du = d + u * subs;
+        const bool in = du < d1;
+        w[u] = in ? __ldg(a.W_r + static_cast<int64_t>(du) * a.E + e) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[u][i] = 0.0f;
+          if (in && i < nt) {
+            const int64_t at = static_cast<int64_t>(t0 + i) * a.D + du;
+            x[u][i] = WK == kF32 ? __ldg(static_cast<const float*>(a.X) + at)
+                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[at]);
+          }
         }
       }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(x[u][i], w[u], acc[i]);
     }
   }
   for (int i = 0; i < nt; ++i) {  // sum the row interleave in order
@@ -206,13 +216,8 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
   while (parts < a.slices && parts * 2 * n <= kConsumers) parts *= 2;
   if (parts > 1) {
     const int l = tid % n, part = tid / n;
-    if (part < parts) {
-      float s = 0.0f;
-#pragma unroll 16
-      for (int q = part; q < a.slices; q += parts)
-        s += __ldcg(a.part_logits + static_cast<int64_t>(q) * n + l);
-      red[part * n + l] = s;
-    }
+    if (part < parts)
+      red[part * n + l] = sum_partials<8>(a.part_logits + l, n, part, parts, a.slices);
     named_bar_sync(kBarConsumers, kConsumers);
     if (tid < n) {
       float s = a.bias != nullptr ? a.bias[tid % a.E] : 0.0f;
@@ -223,10 +228,7 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
     }
   } else {
     for (int l = tid; l < n; l += kConsumers) {
-      float s = 0.0f;
-#pragma unroll 16
-      for (int q = 0; q < a.slices; ++q)
-        s += __ldcg(a.part_logits + static_cast<int64_t>(q) * n + l);
+      const float s = sum_partials<16>(a.part_logits + l, n, 0, 1, a.slices);
       z[l] = s + (a.bias != nullptr ? a.bias[l % a.E] : 0.0f);
     }
   }
@@ -865,7 +867,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
                   last = down.owner(tile * down_steps + down_steps - 1);
         if (last_to_finish<kConsumers>(a.counters + kMaxGrid + first, last - first + 1, tid,
                                        &tb.flag)) {
-          constexpr int kChunk = 8;
+          constexpr int kChunk = WK == kW8 ? 4 : 8;
           for (int i0 = tid; i0 < a.N * P::kPairs; i0 += kChunk * kConsumers) {
             float2 v[kChunk];
 #pragma unroll

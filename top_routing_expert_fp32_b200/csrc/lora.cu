@@ -97,17 +97,15 @@ __host__ __device__ constexpr int lora_stages(int M, int rank, bool f32) {
 static_assert(lora_stages(kMaxRows, kMaxRank, false) >= kInFlight, "ring");
 static_assert(lora_stages(kMaxRows, kMaxRank, true) >= 2, "ring");
 
+// 16 bytes: four fp32 or eight bf16 values.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
-  if constexpr (F32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  } else {
-    const uint4 a =
-        __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void unpack16(const uint4& a, float* v) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
       v[2 * i] = bf16_bits_to_float(w[i] & 0xFFFFu);
       v[2 * i + 1] = bf16_bits_to_float(w[i] >> 16);
     }
@@ -132,14 +130,32 @@ __device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid, int item) {
   if (sub < subs) {
     const int64_t x0 = static_cast<int64_t>(m) * a.K;
     const int64_t a0 = static_cast<int64_t>(ad) * a.K * a.rank + v * kVec;
-#pragma unroll 8
-    for (int k = k0 + sub; k < k1; k += subs) {
-      const float x = F32 ? __ldg(static_cast<const float*>(a.X) + x0 + k)
-                          : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[x0 + k]);
-      float w[8];
-      load8<F32>(a.A, a0 + static_cast<int64_t>(k) * a.rank, w);
+    // Four k at a time, all their loads on their way before the first product: beside the stream a
+    // load takes about 2 us (a row of 4096: the partial sums were out after 9.8 us one by one, 4.6
+    // so), and the side warps' registers hold four.
+    constexpr int kAtOnce = 4;
+    for (int k = k0 + sub; k < k1; k += kAtOnce * subs) {
+      float x[kAtOnce];
+      uint4 w[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(x, w[i], acc[i]);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int at = k + u * subs;
+        if (at < k1) {
+          x[u] = F32 ? __ldg(static_cast<const float*>(a.X) + x0 + at)
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.X)[x0 + at]);
+          w[u] = __ldg(reinterpret_cast<const uint4*>(
+              static_cast<const uint8_t*>(a.A) +
+              (a0 + static_cast<int64_t>(at) * a.rank) * (F32 ? 4 : 2)));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (k + u * subs >= k1) break;
+        float v8[kVec];
+        unpack16<F32>(w[u], v8);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] = fmaf(x[u], v8[i], acc[i]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) tb.scratch[sub * a.rank + v * kVec + i] = acc[i];
@@ -147,6 +163,7 @@ __device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid, int item) {
   named_bar_sync(kBarSide, kSideThreads);
   for (int r = sid; r < a.rank; r += kSideThreads) {
     float s = 0.0f;
+#pragma unroll 4
     for (int q = 0; q < subs; ++q) s += tb.scratch[q * a.rank + r];
     a.part_s[(static_cast<int64_t>(slice) * a.M + m) * a.rank + r] = s;
   }
@@ -180,32 +197,34 @@ __device__ void gather_s(const LoraArgs& a, LoraTables& tb, uint8_t* S, int sid)
   int per = 1;  // threads per value, over the slices
   while (per * 2 <= a.slices && per * 2 * n <= kSideThreads) per *= 2;
   if (per > 1) {
-    float s = 0.0f;
     const int i = sid % n, part = sid / n;
-    if (part < per) {
-#pragma unroll 8
-      for (int q = part; q < a.slices; q += per)
-        s += __ldcg(a.part_s + static_cast<int64_t>(q) * n + i);
-      tb.scratch[part * n + i] = s;
-    }
+    if (part < per) tb.scratch[part * n + i] = sum_partials<8>(a.part_s + i, n, part, per, a.slices);
     named_bar_sync(kBarSide, kSideThreads);
     if (sid < n) {
-      s = 0.0f;
+      float s = 0.0f;
       for (int q = 0; q < per; ++q) s += tb.scratch[q * n + sid];
       put_s<F32>(a, tb, S, sid, s);
     }
     return;
   }
-  constexpr int kAtOnce = 4;
+  // Four values by four slices on their way at once.
+  constexpr int kAtOnce = 4, kSlices = 4;
   for (int i0 = sid; i0 < n; i0 += kAtOnce * kSideThreads) {
     float s[kAtOnce] = {};
-#pragma unroll 8
-    for (int q = 0; q < a.slices; ++q) {
+    for (int q0 = 0; q0 < a.slices; q0 += kSlices) {
+      float v[kSlices][kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int i = i0 + u * kSideThreads;
-        if (i < n) s[u] += __ldcg(a.part_s + static_cast<int64_t>(q) * n + i);
-      }
+      for (int q = 0; q < kSlices; ++q)
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int i = i0 + u * kSideThreads;
+          v[q][u] = q0 + q < a.slices && i < n
+                        ? __ldcg(a.part_s + static_cast<int64_t>(q0 + q) * n + i) : 0.0f;
+        }
+#pragma unroll
+      for (int q = 0; q < kSlices; ++q)
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) s[u] += v[q][u];
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
@@ -331,6 +350,10 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   ring.full = tb.full;
   ring.rows_full = tb.rows_full;
   ring.empty = tb.empty;
+  if (tid == kConsumers) {
+    prefetch_tensormap(&mw);
+    prefetch_tensormap(&mb);
+  }
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&tb.full[i], 1);
@@ -342,8 +365,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
     // This block's counter, and word that it is zero: blocks wait for that before they share a
     // tile, by which time all have long started.
     a.counters[me] = 0;
-    __threadfence();
-    atomicAdd(&a.bar[0], 1);
+    arrive_global(&a.bar[0]);
   }
   {  // The rows' adapters, and the batch's different ones by first appearance.
     const int m = tid - kConsumers;
@@ -491,8 +513,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
         named_bar_sync(kBarSide, kSideThreads);
       }
       if (sid == 0) {
-        __threadfence();
-        atomicAdd(&a.bar[1], 1);
+        arrive_global(&a.bar[1]);
         (void)spin_until(&a.bar[1], G, a.timeout_ns, a.err);
       }
       __syncwarp();

@@ -457,6 +457,21 @@ __device__ __forceinline__ float2 take_pair(const float* red, int branch, int ro
   return s;
 }
 
+// Arrivals at a counter in global memory. Release and acquire at gpu scope: what the thread, and
+// through the block barrier before it the whole block, wrote is visible to whoever sees the
+// arrival (a full fence on either side took a microsecond).
+__device__ __forceinline__ void arrive_global(int* counter) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter) : "memory");
+}
+__device__ __forceinline__ int count_global(int* counter) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+               : "=r"(old)
+               : "l"(counter)
+               : "memory");
+  return old;
+}
+
 // One thread: wait until `target` blocks have arrived at *bar (bounded).
 __device__ __forceinline__ bool spin_until(int* bar, int target, uint64_t timeout_ns, int* err) {
   const uint64_t t0 = globaltimer_ns();
@@ -469,7 +484,6 @@ __device__ __forceinline__ bool spin_until(int* bar, int target, uint64_t timeou
       return false;
     }
   }
-  __threadfence();
   return true;
 }
 
@@ -480,8 +494,7 @@ __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int*
                                              uint64_t timeout_ns, int* err) {
   named_bar_sync(kBarConsumers, kConsumers);
   if (tid == 0) {
-    __threadfence();
-    atomicAdd(bar, 1);
+    arrive_global(bar);
     *flag = spin_until(bar, target, timeout_ns, err) ? 1 : 0;
   }
   __syncwarp();
@@ -494,12 +507,7 @@ __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int*
 template <int kConsumers>
 __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid, int* flag) {
   named_bar_sync(kBarConsumers, kConsumers);
-  if (tid == 0) {
-    __threadfence();  // after the barrier: the whole block's writes
-    const int old = atomicAdd(counter, 1);
-    __threadfence();
-    *flag = old == parts - 1;
-  }
+  if (tid == 0) *flag = count_global(counter) == parts - 1;
   __syncwarp();
   named_bar_sync(kBarConsumers, kConsumers);
   const bool last = *flag != 0;
@@ -508,24 +516,50 @@ __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid,
 
 // v[c] += the shares that blocks first..last hold of place i0 + c * kConsumers (< limit), in block
 // order. `part`: [grid][2][part_floats]; a tile's first block holds its share in the second
-// half. All loads of one block are independent: one L2 latency per block, not per value.
+// half. Four blocks' loads are on their way at once: an L2 latency for four of them, not one each.
 template <int kConsumers, int C>
 __device__ __forceinline__ void add_shares(float2 (&v)[C], const float* part, int64_t part_floats,
                                            int first, int last, int i0, int limit) {
-  for (int b = first; b <= last; ++b) {
-    const float2* p = reinterpret_cast<const float2*>(
-        part + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * part_floats);
-    float2 w[C];
+  constexpr int kAtOnce = 4;
+  for (int b0 = first; b0 <= last; b0 += kAtOnce) {
+    float2 w[kAtOnce][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      w[c] = i0 + c * kConsumers < limit ? __ldcg(p + i0 + c * kConsumers)
-                                         : make_float2(0.0f, 0.0f);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int b = b0 + u;
+      const float2* p = reinterpret_cast<const float2*>(
+          part + (static_cast<int64_t>(b) * 2 + (b == first ? 1 : 0)) * part_floats);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      v[c].x += w[c].x;
-      v[c].y += w[c].y;
+      for (int c = 0; c < C; ++c)
+        w[u][c] = b <= last && i0 + c * kConsumers < limit ? __ldcg(p + i0 + c * kConsumers)
+                                                           : make_float2(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        v[c].x += w[u][c].x;
+        v[c].y += w[u][c].y;
+      }
     }
   }
+}
+
+// The sum of p[q * stride] for q = first, first + step, ... below n, in that order. kAtOnce loads
+// are on their way at once, the last ones too: an unrolled loop would take its remainder one L2
+// latency at a time, longer than everything else here.
+template <int kAtOnce>
+__device__ __forceinline__ float sum_partials(const float* p, int64_t stride, int first, int step,
+                                              int n) {
+  float s = 0.0f;
+  for (int q0 = first; q0 < n; q0 += kAtOnce * step) {
+    float v[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      v[u] = q0 + u * step < n ? __ldcg(p + (q0 + u * step) * stride) : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) s += v[u];
+  }
+  return s;
 }
 
 // Weight producer, before it fills the stage at `c` (the issued-th overall): the stage is free
