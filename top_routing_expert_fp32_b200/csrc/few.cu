@@ -124,7 +124,7 @@ static_assert(ring_stages(ring_bytes<kBF16>(kMaxRows, kMaxE), 4) >= kInFlight, "
 static_assert(ring_stages(ring_bytes<kF32>(kMaxRows, kMaxE), 4) >= kInFlight, "ring");
 
 // H. 16-bit kinds: per tile of 8 rows and 32 values of F two planes (the first and the second
-// bf16 term) of 32 threads x 16 bytes, each thread's four pairs in block order (stream.cuh):
+// bf16 term) of 32 threads x 16 bytes, each thread's four pairs (stream.cuh's Frag):
 // one coalesced load per plane. fp32: plain rows.
 __host__ __device__ inline int64_t h_groups(int64_t F) { return (F + 255) / 256 * 8; }
 constexpr int kHGroupBytes = 1024;
@@ -427,7 +427,7 @@ __device__ __forceinline__ void store_h(const FewArgs& a, const Part& pt, int r,
       *reinterpret_cast<float2*>(static_cast<float*>(a.H) + (pt.row0 + r) * h_row_f32(a.F) + f) =
           make_float2(h0, h1);
   } else {
-    const int pair = (f & 31) >> 1, t = pair >> 2, block = ((pair & 3) - t) & 3;
+    const int pair = (f & 31) >> 1, t = pair & 3, block = pair >> 2;
     uint32_t* w = reinterpret_cast<uint32_t*>(
                       static_cast<uint8_t*>(a.H) +
                       ((pt.tile + (r >> 3)) * h_groups(a.F) + (f >> 5)) * kHGroupBytes) +

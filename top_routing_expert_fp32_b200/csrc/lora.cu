@@ -45,7 +45,7 @@ struct LoraArgs {
   void* Y;
   float* part_s;   // [slices][M][rank]
   float* part;     // [grid][2][part_floats]: sums of shared tiles
-  int* counters;   // [kMaxGrid]: arrivals at shared tiles
+  int* counters;   // [kMaxGrid][kWarps]: arrivals at shared tiles, per warp for bf16
   int* bar;        // [3] workspace header ints, zero at rest: blocks that started, blocks that
                    // have their partial S out, blocks that finished
   int* err;
@@ -81,8 +81,14 @@ constexpr size_t kMaxSmem = 232448;
 __host__ __device__ constexpr size_t s_bytes(int M, int rank) {
   return sizeof(float) * static_cast<size_t>((M + 7) / 8 * 8) * pieces_of(rank) * kPieceRanks;
 }
-__host__ __device__ constexpr size_t lora_ring_bytes(int M, int rank) {
-  return (kMaxSmem - 1024 - kRedBytes - s_bytes(M, rank) - sizeof(LoraTables)) &
+// The consumers' sums: fp32 as in the few-token layer; bf16 a strip of 16 columns per warp, fp32,
+// kStripPitch floats a row.
+constexpr int kStripPitch = 18;
+__host__ __device__ constexpr size_t sum_bytes(int M, bool f32) {
+  return f32 ? kRedBytes : sizeof(float) * LoraTeam::kWarps * ((M + 7) / 8 * 8) * kStripPitch;
+}
+__host__ __device__ constexpr size_t lora_ring_bytes(int M, int rank, bool f32) {
+  return (kMaxSmem - 1024 - sum_bytes(M, f32) - s_bytes(M, rank) - sizeof(LoraTables)) &
          ~size_t(1023);
 }
 // A stage's rows, whole tiles of 8.
@@ -90,7 +96,7 @@ __host__ __device__ constexpr int lora_row_bytes(int M, bool f32) {
   return (M + 7) / 8 * 8 * (f32 ? kRowPitch128F32 : kRowPitch128);
 }
 __host__ __device__ constexpr int lora_stages(int M, int rank, bool f32) {
-  const int s = static_cast<int>(lora_ring_bytes(M, rank) /
+  const int s = static_cast<int>(lora_ring_bytes(M, rank, f32) /
                                  (kStageBytes + static_cast<size_t>(lora_row_bytes(M, f32))));
   return s < kMaxStages ? s : kMaxStages;
 }
@@ -232,36 +238,24 @@ __device__ void gather_s(const LoraArgs& a, LoraTables& tb, uint8_t* S, int sid)
   }
 }
 
-// Two columns of a row of the addend (zeros without one), and of Y. Each value is read and
+// fp32: two columns of a row of the addend (zeros without one), and of Y. Each value is read and
 // written by one thread, the addend first, so the two may be the same array.
-template <bool F32>
 __device__ __forceinline__ float2 load_addend(const LoraArgs& a, int m, int n) {
   if (a.addend == nullptr || m >= a.M || n >= a.N) return make_float2(0.0f, 0.0f);
-  const int64_t at = static_cast<int64_t>(m) * a.N + n;
-  if constexpr (F32) {
-    return *reinterpret_cast<const float2*>(static_cast<const float*>(a.addend) + at);
-  } else {
-    const uint32_t w =
-        *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.addend) + at);
-    return make_float2(bf16_bits_to_float(w & 0xFFFFu), bf16_bits_to_float(w >> 16));
-  }
+  return *reinterpret_cast<const float2*>(static_cast<const float*>(a.addend) +
+                                          static_cast<int64_t>(m) * a.N + n);
 }
-template <bool F32>
 __device__ __forceinline__ void store_y(const LoraArgs& a, int m, int n, float2 v) {
   if (m >= a.M || n >= a.N) return;
-  const int64_t at = static_cast<int64_t>(m) * a.N + n;
-  if constexpr (F32)
-    *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + at) = v;
-  else
-    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.Y) + at) = pack_bf16x2(v.x, v.y);
+  *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + static_cast<int64_t>(m) * a.N + n) = v;
 }
 
-// acc += S x (this warp's two pieces of an adapters' stage). `box`: the warp's box, `piece0`: the
-// first piece of the tile's list that it holds.
-template <int WK, int NT>
-__device__ __forceinline__ void expand(Acc<WK, NT>& acc, uint32_t box, int warp, int lane,
-                                       const LoraTables& tb, const uint8_t* S, int M, int piece0,
-                                       int n_pieces, int per_slot) {
+// fp32: acc += S x (this warp's two pieces of an adapters' stage). `box`: the warp's box, `piece0`:
+// the first piece of the tile's list that it holds.
+template <int NT>
+__device__ __forceinline__ void expand_f32(Acc<kF32, NT>& acc, uint32_t box, int warp, int lane,
+                                           const LoraTables& tb, const uint8_t* S, int piece0,
+                                           int n_pieces, int per_slot) {
   const int ranks = per_slot * kPieceRanks;
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
@@ -270,58 +264,207 @@ __device__ __forceinline__ void expand(Acc<WK, NT>& acc, uint32_t box, int warp,
     const int slot = piece / per_slot, r0 = (piece - slot * per_slot) * kPieceRanks;
     const uint64_t rows = tb.slot_rows[slot];
     const uint32_t row0 = static_cast<uint32_t>((warp & 1) * 32 + h * kPieceRanks);
-    if constexpr (WK == kF32) {
-      float w[kPieceRanks];
+    float w[kPieceRanks];
 #pragma unroll
-      for (int i = 0; i < kPieceRanks; ++i) {
-        const uint32_t r = row0 + i;
-        const uint32_t at = box + r * 128 +
-                            (((static_cast<uint32_t>(lane) >> 2) ^ (r & 7u)) << 4) +
-                            (static_cast<uint32_t>(lane) & 3u) * 4;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at) : "memory");
-      }
+    for (int i = 0; i < kPieceRanks; ++i) {
+      const uint32_t r = row0 + i;
+      const uint32_t at = box + r * 128 + (((static_cast<uint32_t>(lane) >> 2) ^ (r & 7u)) << 4) +
+                          (static_cast<uint32_t>(lane) & 3u) * 4;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at) : "memory");
+    }
 #pragma unroll
-      for (int m = 0; m < 8 * NT; ++m) {
-        if ((rows >> m) & 1ull) {
-          const float* s = reinterpret_cast<const float*>(S) + m * ranks + r0;
-          float sum = 0.0f;
+    for (int m = 0; m < 8 * NT; ++m) {
+      if ((rows >> m) & 1ull) {
+        const float* s = reinterpret_cast<const float*>(S) + m * ranks + r0;
+        float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < kPieceRanks; ++i) sum = fmaf(w[i], s[i], sum);
-          acc.v[m] += sum;
-        }
-      }
-    } else {
-      const int b = lane >> 3, i = lane & 7, g = lane >> 2, t = lane & 3;
-      // Matrices of one load: (column halves lo, hi) x (ranks 0-7, 8-15).
-      const uint32_t r = row0 + (b >> 1) * 8 + i;
-      uint32_t w[4][4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        ldsm_x4_trans(box + r * 128 + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (r & 7u)) << 4),
-                      w[m]);
-      const uint32_t* hi = reinterpret_cast<const uint32_t*>(S);
-      const uint32_t* lo = hi + (M + 7) / 8 * 8 * ranks / 2;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint32_t mine = static_cast<uint32_t>(rows >> (8 * j)) & 0xFFu;
-        if (mine == 0) continue;
-        const int at = ((8 * j + g) * ranks + r0) / 2 + t;
-        const uint32_t h0 = hi[at], h1 = hi[at + 4], l0 = lo[at], l1 = lo[at + 4];
-        const bool even = (mine >> (2 * t)) & 1u, odd = (mine >> (2 * t + 1)) & 1u;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_bf16(c, w[m], h0, h1);
-          mma_bf16(c, w[m], l0, l1);
-          float* o = &acc.v[(m * NT + j) * 4];
-          o[0] += even ? c[0] : 0.0f;
-          o[1] += odd ? c[1] : 0.0f;
-          o[2] += even ? c[2] : 0.0f;
-          o[3] += odd ? c[3] : 0.0f;
-        }
+        for (int i = 0; i < kPieceRanks; ++i) sum = fmaf(w[i], s[i], sum);
+        acc.v[m] += sum;
       }
     }
   }
+}
+
+// ---- bf16 consumers. A warp owns 16 columns of the tile and all of the reduction, so its sums are
+// final in its registers: it needs neither the other warps nor a barrier to write them, or its
+// share of them, and goes on with the next tile while others still multiply. It pays with
+// shared-memory reads: every warp reads all the activation rows (48 rows: 770 of a stage's 1424
+// cycles of HBM time). With the reduction cut over the warps as in the few-token layer, whose
+// sums meet in shared memory eight rows at a time, 48 rows took 43 us, 11 of them for that.
+
+// Sums v[j][c]: row 8 j + 2 t + (c & 1), column g + 8 (c >> 1) of the warp's 16, lane = 4 g + t.
+template <int NT>
+struct Strip {
+  float v[NT][4];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[j][c] = 0.0f;
+  }
+};
+
+// Shared address of the 16 bytes of a box's k-row r that lane l of a transposed load addresses:
+// matrices (column halves) x (two groups of eight k-rows).
+__device__ __forceinline__ uint32_t strip_piece(uint32_t box, uint32_t r, int warp, int lane) {
+  const uint32_t chunk = static_cast<uint32_t>((warp & 3) * 2 + ((lane >> 3) & 1));
+  return box + r * 128 + ((chunk ^ (r & 7u)) << 4);
+}
+
+// acc += a stage of 128 k. `release` hands the stage back once it is read.
+template <int NT, class F>
+__device__ __forceinline__ void strip_stage(Strip<NT>& acc, uint32_t stage, const uint8_t* rows,
+                                            int warp, int lane, int k0, int K, F release) {
+  uint32_t w[4][2][4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {  // 32 k each
+    const uint32_t box = stage + static_cast<uint32_t>((q >> 1) * 2 + (warp >> 2)) * kBoxBytes +
+                         static_cast<uint32_t>(q & 1) * 32 * 128;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      ldsm_x4_trans(strip_piece(box, 16 * s + (lane >> 4) * 8 + (lane & 7), warp, lane),
+                    w[q][s]);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    Frag<NT, false> f;
+    f.load_rows(rows, kRowPitch128, q, k0 + q * 32, K, lane);
+    if (q == 3) release();
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        mma_bf16(acc.v[j], w[q][s], f.r[j][0][2 * s], f.r[j][0][2 * s + 1]);
+  }
+}
+
+// acc += S x (the pieces piece0 .. of an adapters' stage).
+template <int NT>
+__device__ __forceinline__ void strip_expand(Strip<NT>& acc, uint32_t stage, int warp, int lane,
+                                             const LoraTables& tb, const uint8_t* S, int M,
+                                             int piece0, int n_pieces, int per_slot) {
+  const int ranks = per_slot * kPieceRanks, g = lane >> 2, t = lane & 3;
+  const uint32_t* hi = reinterpret_cast<const uint32_t*>(S);
+  const uint32_t* lo = hi + (M + 7) / 8 * 8 * ranks / 2;
+  int slot = piece0 / per_slot, part = piece0 - slot * per_slot;
+#pragma unroll 2
+  for (int h = 0; h < kStagePieces; ++h) {
+    if (piece0 + h >= n_pieces) return;
+    const uint64_t rows = tb.slot_rows[slot];
+    const uint32_t box = stage + static_cast<uint32_t>((h >> 2) * 2 + (warp >> 2)) * kBoxBytes;
+    uint32_t w[4];
+    ldsm_x4_trans(strip_piece(box, (h & 3) * kPieceRanks + (lane >> 4) * 8 + (lane & 7), warp, lane),
+                  w);
+    const int r0 = part * kPieceRanks;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint32_t mine = static_cast<uint32_t>(rows >> (8 * j)) & 0xFFu;
+      if (mine == 0) continue;
+      const int at = ((8 * j + g) * ranks + r0) / 2 + t;
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      mma_bf16(c, w, hi[at], hi[at + 4]);
+      mma_bf16(c, w, lo[at], lo[at + 4]);
+      const bool even = (mine >> (2 * t)) & 1u, odd = (mine >> (2 * t + 1)) & 1u;
+      acc.v[j][0] += even ? c[0] : 0.0f;
+      acc.v[j][1] += odd ? c[1] : 0.0f;
+      acc.v[j][2] += even ? c[2] : 0.0f;
+      acc.v[j][3] += odd ? c[3] : 0.0f;
+    }
+    if (++part == per_slot) {
+      part = 0;
+      ++slot;
+    }
+  }
+}
+
+// Y of the warp's columns (from n0 on): sums plus addend, through the warp's shared memory, so that
+// a lane reads and writes 16 bytes of a row.
+template <int NT>
+__device__ __forceinline__ void strip_store(const LoraArgs& a, const Strip<NT>& acc, float* strip,
+                                            int n0, int lane) {
+  constexpr int kTimes = (NT * 16 + 31) / 32;
+  const int half = lane & 1, n = n0 + half * 8;
+  uint4 extra[kTimes];
+#pragma unroll
+  for (int i = 0; i < kTimes; ++i) {
+    const int m = i * 16 + (lane >> 1);
+    extra[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.addend != nullptr && m < a.M && n < a.N)
+      extra[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.addend) +
+                                                 static_cast<int64_t>(m) * a.N + n);
+  }
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if (8 * j < a.M) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        strip[(8 * j + 2 * t + (c & 1)) * kStripPitch + g + 8 * (c >> 1)] = acc.v[j][c];
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kTimes; ++i) {
+    const int m = i * 16 + (lane >> 1);
+    if (m < a.M && n < a.N) {
+      const float2* v = reinterpret_cast<const float2*>(strip + m * kStripPitch + half * 8);
+      const uint32_t e[4] = {extra[i].x, extra[i].y, extra[i].z, extra[i].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        y[q] = pack_bf16x2(v[q].x + bf16_bits_to_float(e[q] & 0xFFFFu),
+                           v[q].y + bf16_bits_to_float(e[q] >> 16));
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) +
+                                static_cast<int64_t>(m) * a.N + n) =
+          make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+  __syncwarp();  // the strip is read before the next tile's sums overwrite it
+}
+
+// The warp's sums of a tile that blocks first..last share: its share to L2; the last of them to
+// arrive adds all shares up in block order and writes Y.
+template <int NT>
+__device__ __forceinline__ void strip_share(const LoraArgs& a, Strip<NT>& acc, float* strip, int n0,
+                                            int tid, bool is_first, int first, int last) {
+  const int lane = tid & 31;
+  auto share = [&](int b, bool head) {
+    return reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(b) * 2 + (head ? 1 : 0)) *
+                                                  a.part_floats) + tid;
+  };
+  float4* mine = share(static_cast<int>(blockIdx.x), is_first);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    if (8 * j < a.M)
+      mine[j * kConsumers] = make_float4(acc.v[j][0], acc.v[j][1], acc.v[j][2], acc.v[j][3]);
+  __syncwarp();  // the warp's writes, then its arrival
+  int old = 0;
+  if (lane == 0)
+    old = count_global(a.counters + first * LoraTeam::kWarps + (tid >> 5));
+  old = __shfl_sync(0xFFFFFFFFu, old, 0);
+  if (old != last - first) return;
+  constexpr int kAtOnce = NT <= 2 ? 4 : 2;  // blocks whose shares are on their way at once
+  acc.zero();
+  for (int b0 = first; b0 <= last; b0 += kAtOnce) {
+    float4 w[kAtOnce][NT];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        w[u][j] = b0 + u <= last && 8 * j < a.M
+                      ? __ldcg(share(b0 + u, b0 + u == first) + j * kConsumers)
+                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        acc.v[j][0] += w[u][j].x;
+        acc.v[j][1] += w[u][j].y;
+        acc.v[j][2] += w[u][j].z;
+        acc.v[j][3] += w[u][j].w;
+      }
+  }
+  strip_store<NT>(a, acc, strip, n0, lane);
 }
 
 template <int WK, int NT>
@@ -334,8 +477,8 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* red = reinterpret_cast<float*>(smem + lora_ring_bytes(a.M, a.rank));
-  uint8_t* S_mem = reinterpret_cast<uint8_t*>(red) + kRedBytes;  // S, scaled
+  float* red = reinterpret_cast<float*>(smem + lora_ring_bytes(a.M, a.rank, kIsF32));
+  uint8_t* S_mem = reinterpret_cast<uint8_t*>(red) + sum_bytes(a.M, kIsF32);  // S, scaled
   LoraTables& tb = *reinterpret_cast<LoraTables*>(S_mem + s_bytes(a.M, a.rank));
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
@@ -364,7 +507,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
     fence_barrier_init();
     // This block's counter, and word that it is zero: blocks wait for that before they share a
     // tile, by which time all have long started.
-    a.counters[me] = 0;
+    for (int i = 0; i < LoraTeam::kWarps; ++i) a.counters[me * LoraTeam::kWarps + i] = 0;
     arrive_global(&a.bar[0]);
   }
   {  // The rows' adapters, and the batch's different ones by first appearance.
@@ -534,100 +677,131 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       }
       __syncwarp();
     };
-    RedTurn<WK> turn{red};
     Cursor cur;
-    const int first_row = (warp >> 2) * kBoxRows + warp_row<WK>(warp);
-    segments([&](int cb, int k0, int k1) {
-      Acc<WK, NT> acc;
-      acc.zero();
-      for (int k = k0; k < k1; ++k) {
-        if (k >= k_steps) take_s();
-        if (ok && (!mbar_wait(&tb.full[cur.stage], cur.phase, a.timeout_ns) ||
-                   !mbar_wait(&tb.rows_full[cur.stage], cur.phase, a.timeout_ns))) {
-          ok = false;
-          record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+    auto wait_stage = [&] {
+      if (ok && (!mbar_wait(&tb.full[cur.stage], cur.phase, a.timeout_ns) ||
+                 !mbar_wait(&tb.rows_full[cur.stage], cur.phase, a.timeout_ns))) {
+        ok = false;
+        record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
+      }
+      __syncwarp();  // the lanes leave the wait one by one; what follows is for whole warps
+    };
+    auto release = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
+    };
+    // Before a thread counts its arrival at a shared tile: every block's counters are at zero.
+    auto wait_started = [&](bool counts) {
+      if (!all_started && counts) (void)spin_until(&a.bar[0], G, a.timeout_ns, a.err);
+      __syncwarp();
+      all_started = true;
+    };
+    if constexpr (!kIsF32) {
+      float* strip = red + warp * ((a.M + 7) / 8 * 8) * kStripPitch;
+      segments([&](int cb, int k0, int k1) {
+        Strip<NT> acc;
+        acc.zero();
+        for (int k = k0; k < k1; ++k) {
+          if (k >= k_steps) take_s();
+          wait_stage();
+          const uint32_t stage =
+              smem_u32(ring.weights) + static_cast<uint32_t>(cur.stage) * kStageBytes;
+          if (k < k_steps) {
+            strip_stage<NT>(acc, stage, ring.rows + cur.stage * ring.row_bytes, warp, lane,
+                            k * 2 * kBoxRows, a.K, release);
+          } else {
+            strip_expand<NT>(acc, stage, warp, lane, tb, S_mem, a.M,
+                             (k - k_steps) * kStagePieces, n_pieces, per_slot);
+            release();
+          }
+          cur.next(ring.stages);
         }
-        __syncwarp();  // the lanes leave the wait one by one; what follows is for whole warps
-        const uint32_t box = smem_u32(ring.weights) +
-                             static_cast<uint32_t>(cur.stage) * kStageBytes +
-                             static_cast<uint32_t>(warp >> 1) * kBoxBytes;
-        const uint8_t* rows = ring.rows + cur.stage * ring.row_bytes;
-        const int at = k * 2 * kBoxRows + first_row;
-        if (k >= k_steps) {
-          expand<WK, NT>(acc, box, warp, lane, tb, S_mem, a.M,
-                         (k - k_steps) * kStagePieces + (warp >> 2) * 4 + (warp & 1) * 2, n_pieces,
-                         per_slot);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
-        } else if constexpr (kIsF32) {
-          multiply_f32<NT>(acc, box, warp, lane, smem_u32(rows) + first_row * 4, kRowPitch128F32,
-                           a.M, at, a.K);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
+        const int n0 = cb * S::kCols + warp * 16;
+        if (k0 == 0 && k1 == steps) {
+          strip_store<NT>(a, acc, strip, n0, lane);
         } else {
-          Weights<WK> w;
-          Frag<NT, false> f;
-          w.load(box, warp, lane);
-          f.load_rows(rows, kRowPitch128, first_row / 32, at, a.K, lane);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tb.empty[cur.stage]);
-          multiply<WK, NT, false>(acc, w, f);
+          const long long at = static_cast<long long>(cb) * steps;
+          wait_started(lane == 0);
+          strip_share<NT>(a, acc, strip, n0, tid, k0 == 0, sp.owner(at), sp.owner(at + steps - 1));
         }
-        cur.next(ring.stages);
-      }
-      const bool whole = k0 == 0 && k1 == steps;
-      float2* mine = reinterpret_cast<float2*>(
-          a.part + (static_cast<int64_t>(me) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (8 * j >= a.M) break;
-        float2 extra[P::kMine];  // loaded before the warps' sums meet
-#pragma unroll
-        for (int q = 0; q < P::kMine; ++q) {
-          const int i = tid + q * kConsumers;
-          extra[q] = whole ? load_addend<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i))
-                           : make_float2(0.0f, 0.0f);
+        return true;
+      });
+    } else {
+      RedTurn<WK> turn{red};
+      const int first_row = (warp >> 2) * kBoxRows + warp_row<WK>(warp);
+      segments([&](int cb, int k0, int k1) {
+        Acc<WK, NT> acc;
+        acc.zero();
+        for (int k = k0; k < k1; ++k) {
+          if (k >= k_steps) take_s();
+          wait_stage();
+          const uint32_t box = smem_u32(ring.weights) +
+                               static_cast<uint32_t>(cur.stage) * kStageBytes +
+                               static_cast<uint32_t>(warp >> 1) * kBoxBytes;
+          const uint8_t* rows = ring.rows + cur.stage * ring.row_bytes;
+          if (k >= k_steps)
+            expand_f32<NT>(acc, box, warp, lane, tb, S_mem,
+                           (k - k_steps) * kStagePieces + (warp >> 2) * 4 + (warp & 1) * 2,
+                           n_pieces, per_slot);
+          else
+            multiply_f32<NT>(acc, box, warp, lane, smem_u32(rows) + first_row * 4, kRowPitch128F32,
+                             a.M, k * 2 * kBoxRows + first_row, a.K);
+          release();
+          cur.next(ring.stages);
         }
-        float* sums = turn.next();
-        put_tile<WK, NT>(sums, acc, j, warp, lane);
-        named_bar_sync(kBarConsumers, kConsumers);
+        const bool whole = k0 == 0 && k1 == steps;
+        float2* mine = reinterpret_cast<float2*>(
+            a.part + (static_cast<int64_t>(me) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
 #pragma unroll
-        for (int q = 0; q < P::kMine; ++q) {
-          const int i = tid + q * kConsumers;
-          float2 v = take_pair<WK>(sums, -1, P::row(i), P::col(i));
-          v.x += extra[q].x;
-          v.y += extra[q].y;
-          if (whole) store_y<kIsF32>(a, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
-          else mine[j * P::kCount + i] = v;
+        for (int j = 0; j < NT; ++j) {
+          if (8 * j >= a.M) break;
+          float2 extra[P::kMine];  // loaded before the warps' sums meet
+#pragma unroll
+          for (int q = 0; q < P::kMine; ++q) {
+            const int i = tid + q * kConsumers;
+            extra[q] = whole ? load_addend(a, 8 * j + P::row(i), cb * S::kCols + P::col(i))
+                             : make_float2(0.0f, 0.0f);
+          }
+          float* sums = turn.next();
+          put_tile<WK, NT>(sums, acc, j, warp, lane);
+          named_bar_sync(kBarConsumers, kConsumers);
+#pragma unroll
+          for (int q = 0; q < P::kMine; ++q) {
+            const int i = tid + q * kConsumers;
+            float2 v = take_pair<WK>(sums, -1, P::row(i), P::col(i));
+            v.x += extra[q].x;
+            v.y += extra[q].y;
+            if (whole) store_y(a, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
+            else mine[j * P::kCount + i] = v;
+          }
         }
-      }
-      if (!whole) {
-        const long long at = static_cast<long long>(cb) * steps;
-        const int first = sp.owner(at), last = sp.owner(at + steps - 1);
-        if (!all_started && tid == 0) (void)spin_until(&a.bar[0], G, a.timeout_ns, a.err);
-        __syncwarp();
-        all_started = true;  // (thread 0 counts the arrivals)
-        if (last_to_finish<kConsumers>(a.counters + first, last - first + 1, tid, &tb.flag)) {
-          constexpr int kChunk = 8;
-          const int limit = (a.M + 7) / 8 * P::kCount;
-          for (int i0 = tid; i0 < limit; i0 += kChunk * kConsumers) {
-            float2 v[kChunk];
+        if (!whole) {
+          const long long at = static_cast<long long>(cb) * steps;
+          const int first = sp.owner(at), last = sp.owner(at + steps - 1);
+          wait_started(tid == 0);
+          if (last_to_finish<kConsumers>(a.counters + first * LoraTeam::kWarps, last - first + 1,
+                                         tid, &tb.flag)) {
+            constexpr int kChunk = 8;
+            const int limit = (a.M + 7) / 8 * P::kCount;
+            for (int i0 = tid; i0 < limit; i0 += kChunk * kConsumers) {
+              float2 v[kChunk];
 #pragma unroll
-            for (int q = 0; q < kChunk; ++q) {
-              const int i = i0 + q * kConsumers;
-              v[q] = load_addend<kIsF32>(a, P::row(i), cb * S::kCols + P::col(i));
-            }
-            add_shares<kConsumers>(v, a.part, a.part_floats, first, last, i0, limit);
+              for (int q = 0; q < kChunk; ++q) {
+                const int i = i0 + q * kConsumers;
+                v[q] = load_addend(a, P::row(i), cb * S::kCols + P::col(i));
+              }
+              add_shares<kConsumers>(v, a.part, a.part_floats, first, last, i0, limit);
 #pragma unroll
-            for (int q = 0; q < kChunk; ++q) {
-              const int i = i0 + q * kConsumers;
-              if (i < limit) store_y<kIsF32>(a, P::row(i), cb * S::kCols + P::col(i), v[q]);
+              for (int q = 0; q < kChunk; ++q) {
+                const int i = i0 + q * kConsumers;
+                if (i < limit) store_y(a, P::row(i), cb * S::kCols + P::col(i), v[q]);
+              }
             }
           }
         }
-      }
-      return true;
-    });
+        return true;
+      });
+    }
   }
 
   // The last block out returns the barrier counters to zero for the next launch.
@@ -683,7 +857,7 @@ cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void*
 size_t lora_few_workspace_bytes(const moe_lora_problem& p) {
   const int64_t M = std::min<int64_t>(p.M, kMaxRows);
   return up256(sizeof(float) * kMaxGrid * p.rank) +  // slices x rows
-         up256(sizeof(int) * kMaxGrid) + up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(M));
+         up256(sizeof(int) * kMaxGrid * LoraTeam::kWarps) + up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(M));
 }
 
 cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, void* scratch,
@@ -700,7 +874,7 @@ cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, voi
   a.part_s = reinterpret_cast<float*>(w);
   w += up256(sizeof(float) * kMaxGrid * p.rank);
   a.counters = reinterpret_cast<int*>(w);
-  w += up256(sizeof(int) * kMaxGrid);
+  w += up256(sizeof(int) * kMaxGrid * LoraTeam::kWarps);
   a.part = reinterpret_cast<float*>(w);
   a.part_floats = lora_part_floats(p.M);
   a.bar = bar;

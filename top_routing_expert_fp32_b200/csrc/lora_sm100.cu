@@ -196,19 +196,11 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           if (!kAll && ((tiles >> j) & 1u) == 0) continue;
-          const uint4 v = *reinterpret_cast<const uint4*>(xs + (8 * j + g) * 128 +
-                                                          (((kg * 4 + t) ^ g) << 4));
-          const bool one = (t & 1) != 0, two = (t & 2) != 0;
-          const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
-                         a3 = one ? v.x : v.w;
-          x[j][0] = two ? a2 : a0;
-          x[j][1] = two ? a3 : a1;
-          x[j][2] = two ? a0 : a2;
-          x[j][3] = two ? a1 : a3;
+          stream::ldsm_x4(smem_u32(xs) + (8 * j + i8) * 128 + (((kg * 4 + b) ^ i8) << 4), x[j]);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int row = kg * 32 + static_cast<int>(stream::block_row(2 * s + (b >> 1), i8));
+          const int row = kg * 32 + 16 * s + (b >> 1) * 8 + i8;
           uint32_t w[RT][4];
 #pragma unroll
           for (int r = 0; r < RT; ++r)

@@ -20,14 +20,8 @@
 // 16-bit weights [k][n] (n contiguous) become the row operand of mma.m16n8k16 through transposed
 // ldmatrix (16 output columns x 16 k per instruction), the activation rows its 8 columns: one
 // instruction per 512 bytes of weights and 8 rows, far from the tensor cores' limit, where the
-// tcgen05 tiles of 64 or 128 rows would mostly multiply padding.
-//
-// Order of k. Within 32 k-rows, thread t of a quad holds the 8 consecutive values k = 8t..8t+7 of
-// an activation row (one 16-byte load), that is four pairs w = 0..3. The instructions need them in
-// four blocks; block b takes each thread's pair w = (b + t) & 3, and the transposed loads fetch
-// the matching weight rows 8t + 2w + {0, 1}: any one-to-one order of k gives the same sum, and
-// this one makes the eight weight rows of a block differ modulo 8, so the swizzled shared-memory
-// reads have no bank conflicts.
+// tcgen05 tiles of 64 or 128 rows would mostly multiply padding. The rows come through plain
+// ldmatrix, 32 k of 8 rows per instruction, their pitch 16 bytes modulo the 128 of all banks.
 #pragma once
 
 #include "common.cuh"
@@ -165,6 +159,13 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 __device__ __forceinline__ void mma_bf16(float* c, const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
@@ -208,8 +209,8 @@ struct Acc {
   }
 };
 
-// One thread's activation values of 32 k: for each row tile the pairs of the four blocks; with
-// SPLIT each value is the sum of two bf16 terms (planes 0 and 1).
+// One thread's activation values of 32 k: for each row tile its pairs k = 8 q + 2 t + {0, 1} of
+// row g (lane = 4 g + t); with SPLIT each value is the sum of two bf16 terms (planes 0 and 1).
 template <int NT, bool SPLIT>
 struct Frag {
   uint32_t r[NT][SPLIT ? 2 : 1][4];
@@ -230,34 +231,26 @@ struct Frag {
       }
   }
 
-  // From plain rows: thread t of quad `lane / 4` reads the 16 bytes of its four pairs, block b
-  // takes pair (b + t) & 3. `group`: 32-value group in the rows; k0: its first k within the
-  // reduction of K (past its end nothing was copied: zeros).
+  // From plain rows: 32-value group `group`; k0: its first k within the reduction of K (past its end
+  // nothing was copied: zeros; K is a multiple of 8).
   __device__ __forceinline__ void load_rows(const uint8_t* rows, int row_pitch, int group, int k0,
                                             int K, int lane) {
     static_assert(!SPLIT, "one plane");
-    const int t = lane & 3;
-    const bool one = (t & 1) != 0, two = (t & 2) != 0;
+    const uint32_t at =
+        smem_u32(rows) + static_cast<uint32_t>((lane & 7) * row_pitch + group * 64 + (lane >> 3) * 16);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      uint4 v = *reinterpret_cast<const uint4*>(rows + (8 * j + (lane >> 2)) * row_pitch +
-                                                group * 64 + t * 16);
-      if (k0 + 8 * t >= K) v = make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z,
-                     a3 = one ? v.x : v.w;
-      r[j][0][0] = two ? a2 : a0;
-      r[j][0][1] = two ? a3 : a1;
-      r[j][0][2] = two ? a0 : a2;
-      r[j][0][3] = two ? a1 : a3;
+    for (int j = 0; j < NT; ++j)
+      ldsm_x4(at + static_cast<uint32_t>(8 * j * row_pitch), r[j][0]);
+    if (k0 + 32 > K) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (k0 + 8 * q >= K) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) r[j][0][q] = 0u;
+        }
     }
   }
 };
-
-// Row of a 32-row group that lane l of a transposed load addresses for block b.
-__device__ __forceinline__ uint32_t block_row(int b, int i) {
-  const int t = i >> 1;
-  return static_cast<uint32_t>(8 * t + 2 * ((b + t) & 3) + (i & 1));
-}
 
 // A warp's weights of one stage, as the transposed loads deliver them: registers, so that the
 // stage can be handed back before the arithmetic.
@@ -272,7 +265,7 @@ struct Weights {
       // Matrices of one load: (column halves lo, hi) x (blocks 2s, 2s + 1).
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t k = block_row(2 * s + (b >> 1), i);
+        const uint32_t k = static_cast<uint32_t>(16 * s + (b >> 1) * 8 + i);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
           ldsm_x4_trans(rows + k * 128 + ((static_cast<uint32_t>(m * 2 + (b & 1)) ^ (k & 7u)) << 4),
@@ -280,7 +273,7 @@ struct Weights {
       }
     } else {
       // One load takes 16 columns (bytes) of all four blocks.
-      const uint32_t k = block_row(b, i);
+      const uint32_t k = static_cast<uint32_t>(lane);
 #pragma unroll
       for (int m = 0; m < 4; ++m)
         ldsm_x4_trans(rows + k * 128 +
