@@ -81,11 +81,16 @@ constexpr size_t kMaxSmem = 232448;
 __host__ __device__ constexpr size_t s_bytes(int M, int rank) {
   return sizeof(float) * static_cast<size_t>((M + 7) / 8 * 8) * pieces_of(rank) * kPieceRanks;
 }
-// The consumers' sums: fp32 as in the few-token layer; bf16 a strip of 16 columns per warp, fp32,
-// kStripPitch floats a row.
+// The consumers' sums: fp32 as in the few-token layer; bf16 per warp, or pair of warps, 16 columns of
+// the rows at kStripPitch floats a row, or the sums that a pair exchanges.
 constexpr int kStripPitch = 18;
+__host__ __device__ constexpr int row_tiles_of(int M) {  // kernels are made for these
+  const int n = (M + 7) / 8;
+  return n <= 4 ? n : n <= 6 ? 6 : 8;
+}
 __host__ __device__ constexpr size_t sum_bytes(int M, bool f32) {
-  return f32 ? kRedBytes : sizeof(float) * LoraTeam::kWarps * ((M + 7) / 8 * 8) * kStripPitch;
+  return f32 ? kRedBytes
+             : sizeof(float) * LoraTeam::kWarps * row_tiles_of(M) * 8 * kStripPitch;
 }
 __host__ __device__ constexpr size_t lora_ring_bytes(int M, int rank, bool f32) {
   return (kMaxSmem - 1024 - sum_bytes(M, f32) - s_bytes(M, rank) - sizeof(LoraTables)) &
@@ -287,88 +292,121 @@ __device__ __forceinline__ void expand_f32(Acc<kF32, NT>& acc, uint32_t box, int
 
 // ---- bf16 consumers. A warp owns 16 columns of the tile and all of the reduction, so its sums are
 // final in its registers: it needs neither the other warps nor a barrier to write them, or its
-// share of them, and goes on with the next tile while others still multiply. It pays with
-// shared-memory reads: every warp reads all the activation rows (48 rows: 770 of a stage's 1424
-// cycles of HBM time). With the reduction cut over the warps as in the few-token layer, whose
-// sums meet in shared memory eight rows at a time, 48 rows took 43 us, 11 of them for that.
+// share of them, and goes on with the next tile while others still multiply. (With the reduction
+// cut over four warps as in the few-token layer, whose sums meet in shared memory eight rows at a
+// time, 48 rows took 43 us, 11 of them for that.) It pays with shared-memory reads, since every
+// warp reads all the activation rows: above 32 rows a pair of warps owns 32 columns, half of the
+// reduction each, and the second hands its sums to the first (48 rows: 45 us without the pairs,
+// ... with them).
+constexpr int halves_of(int NT) { return NT > 4 ? 2 : 1; }
 
-// Sums v[j][c]: row 8 j + 2 t + (c & 1), column g + 8 (c >> 1) of the warp's 16, lane = 4 g + t.
+// Sums v[h][j][c]: row 8 j + 2 t + (c & 1), column 16 h + g + 8 (c >> 1) of the warp's, where
+// lane = 4 g + t.
 template <int NT>
 struct Strip {
-  float v[NT][4];
+  static constexpr int kHalves = halves_of(NT);  // of the reduction; groups of 16 columns
+  float v[kHalves][NT][4];
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[j][c] = 0.0f;
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[h][j][c] = 0.0f;
   }
 };
 
-// Shared address of the 16 bytes of a box's k-row r that lane l of a transposed load addresses:
-// matrices (column halves) x (two groups of eight k-rows).
-__device__ __forceinline__ uint32_t strip_piece(uint32_t box, uint32_t r, int warp, int lane) {
-  const uint32_t chunk = static_cast<uint32_t>((warp & 3) * 2 + ((lane >> 3) & 1));
-  return box + r * 128 + ((chunk ^ (r & 7u)) << 4);
-}
+// A warp's place: its columns' number among the tile's, its half of the reduction, the box of a
+// side-by-side pair and the first 16-byte piece of the box's rows.
+template <int NT>
+struct Place {
+  static constexpr int kHalves = halves_of(NT);
+  static constexpr int kOwners = LoraTeam::kWarps / kHalves;  // warps that write sums
+  int owner, half, side, piece;
+  __device__ explicit Place(int warp)
+      : owner(warp % kOwners), half(warp / kOwners), side(owner / (kOwners / 2)),
+        piece(owner % (kOwners / 2) * 2 * kHalves) {}
+  // Shared address of the 16 bytes that lane l of a transposed load addresses: 16 k-rows from row0
+  // of the box on, column group h.
+  __device__ __forceinline__ uint32_t weights(uint32_t box, int row0, int h, int lane) const {
+    const uint32_t r = static_cast<uint32_t>(row0 + (lane >> 4) * 8 + (lane & 7));
+    const uint32_t chunk = static_cast<uint32_t>(piece + h * 2 + ((lane >> 3) & 1));
+    return box + r * 128 + ((chunk ^ (r & 7u)) << 4);
+  }
+};
 
 // acc += a stage of 128 k. `release` hands the stage back once it is read.
 template <int NT, class F>
-__device__ __forceinline__ void strip_stage(Strip<NT>& acc, uint32_t stage, const uint8_t* rows,
-                                            int warp, int lane, int k0, int K, F release) {
-  uint32_t w[4][2][4];
+__device__ __forceinline__ void strip_stage(Strip<NT>& acc, const Place<NT>& at, uint32_t stage,
+                                            const uint8_t* rows, int lane, int k0, int K,
+                                            F release) {
+  constexpr int H = halves_of(NT), kGroups = 4 / H;  // of 32 k
+  uint32_t w[kGroups][2][H][4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {  // 32 k each
-    const uint32_t box = stage + static_cast<uint32_t>((q >> 1) * 2 + (warp >> 2)) * kBoxBytes +
-                         static_cast<uint32_t>(q & 1) * 32 * 128;
+  for (int q = 0; q < kGroups; ++q) {
+    const int k32 = at.half * kGroups + q;
+    const uint32_t box = stage + static_cast<uint32_t>((k32 >> 1) * 2 + at.side) * kBoxBytes;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      ldsm_x4_trans(strip_piece(box, 16 * s + (lane >> 4) * 8 + (lane & 7), warp, lane),
-                    w[q][s]);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        ldsm_x4_trans(at.weights(box, (k32 & 1) * 32 + 16 * s, h, lane), w[q][s][h]);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < kGroups; ++q) {
+    const int k32 = at.half * kGroups + q;
     Frag<NT, false> f;
-    f.load_rows(rows, kRowPitch128, q, k0 + q * 32, K, lane);
-    if (q == 3) release();
+    f.load_rows(rows, kRowPitch128, k32, k0 + k32 * 32, K, lane);
+    if (q == kGroups - 1) release();
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        mma_bf16(acc.v[j], w[q][s], f.r[j][0][2 * s], f.r[j][0][2 * s + 1]);
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          mma_bf16(acc.v[h][j], w[q][s][h], f.r[j][0][2 * s], f.r[j][0][2 * s + 1]);
   }
 }
 
-// acc += S x (the pieces piece0 .. of an adapters' stage).
+// acc += S x (the warp's pieces, of those from piece0 on, of an adapters' stage).
 template <int NT>
-__device__ __forceinline__ void strip_expand(Strip<NT>& acc, uint32_t stage, int warp, int lane,
-                                             const LoraTables& tb, const uint8_t* S, int M,
-                                             int piece0, int n_pieces, int per_slot) {
+__device__ __forceinline__ void strip_expand(Strip<NT>& acc, const Place<NT>& at, uint32_t stage,
+                                             int lane, const LoraTables& tb, const uint8_t* S,
+                                             int M, int piece0, int n_pieces, int per_slot) {
+  constexpr int H = halves_of(NT), kPieces = kStagePieces / H;
   const int ranks = per_slot * kPieceRanks, g = lane >> 2, t = lane & 3;
   const uint32_t* hi = reinterpret_cast<const uint32_t*>(S);
   const uint32_t* lo = hi + (M + 7) / 8 * 8 * ranks / 2;
+  piece0 += at.half * kPieces;
   int slot = piece0 / per_slot, part = piece0 - slot * per_slot;
 #pragma unroll 2
-  for (int h = 0; h < kStagePieces; ++h) {
-    if (piece0 + h >= n_pieces) return;
+  for (int i = 0; i < kPieces; ++i) {
+    if (piece0 + i >= n_pieces) return;
     const uint64_t rows = tb.slot_rows[slot];
-    const uint32_t box = stage + static_cast<uint32_t>((h >> 2) * 2 + (warp >> 2)) * kBoxBytes;
-    uint32_t w[4];
-    ldsm_x4_trans(strip_piece(box, (h & 3) * kPieceRanks + (lane >> 4) * 8 + (lane & 7), warp, lane),
-                  w);
+    const int in_stage = at.half * kPieces + i;
+    const uint32_t box = stage + static_cast<uint32_t>((in_stage >> 2) * 2 + at.side) * kBoxBytes;
+    uint32_t w[H][4];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      ldsm_x4_trans(at.weights(box, (in_stage & 3) * kPieceRanks, h, lane), w[h]);
     const int r0 = part * kPieceRanks;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const uint32_t mine = static_cast<uint32_t>(rows >> (8 * j)) & 0xFFu;
       if (mine == 0) continue;
-      const int at = ((8 * j + g) * ranks + r0) / 2 + t;
-      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma_bf16(c, w, hi[at], hi[at + 4]);
-      mma_bf16(c, w, lo[at], lo[at + 4]);
+      const int s = ((8 * j + g) * ranks + r0) / 2 + t;
+      const uint32_t h0 = hi[s], h1 = hi[s + 4], l0 = lo[s], l1 = lo[s + 4];
       const bool even = (mine >> (2 * t)) & 1u, odd = (mine >> (2 * t + 1)) & 1u;
-      acc.v[j][0] += even ? c[0] : 0.0f;
-      acc.v[j][1] += odd ? c[1] : 0.0f;
-      acc.v[j][2] += even ? c[2] : 0.0f;
-      acc.v[j][3] += odd ? c[3] : 0.0f;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma_bf16(c, w[h], h0, h1);
+        mma_bf16(c, w[h], l0, l1);
+        acc.v[h][j][0] += even ? c[0] : 0.0f;
+        acc.v[h][j][1] += odd ? c[1] : 0.0f;
+        acc.v[h][j][2] += even ? c[2] : 0.0f;
+        acc.v[h][j][3] += odd ? c[3] : 0.0f;
+      }
     }
     if (++part == per_slot) {
       part = 0;
@@ -377,92 +415,151 @@ __device__ __forceinline__ void strip_expand(Strip<NT>& acc, uint32_t stage, int
   }
 }
 
+// The two warps of a pair, at a tile's end: the second's sums through shared memory (`strip`,
+// owned by the pair) to the first, which goes on to write them. True in the first. Barriers
+// kBarPair + owner: the sums are there; + kOwners: the strip is free again (also before its first
+// use, so the first arrives there at the start and after each write).
+constexpr int kBarPair = 5;
+template <int NT>
+__device__ __forceinline__ bool strip_meet(Strip<NT>& acc, const Place<NT>& at, float* strip,
+                                           int lane) {
+  constexpr int H = halves_of(NT);
+  static_assert(H == 1 || sizeof(float4) * 32 * H * NT <=
+                              sizeof(float) * 2 * NT * 8 * kStripPitch, "strip");
+  if constexpr (H == 2) {
+    float4* x = reinterpret_cast<float4*>(strip) + lane;
+    if (at.half == 1) {
+      named_bar_sync(kBarPair + Place<NT>::kOwners + at.owner, 64);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          x[(h * NT + j) * 32] = make_float4(acc.v[h][j][0], acc.v[h][j][1], acc.v[h][j][2],
+                                             acc.v[h][j][3]);
+      named_bar_arrive(kBarPair + at.owner, 64);
+      return false;
+    }
+    named_bar_sync(kBarPair + at.owner, 64);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float4 v = x[(h * NT + j) * 32];
+        acc.v[h][j][0] += v.x;
+        acc.v[h][j][1] += v.y;
+        acc.v[h][j][2] += v.z;
+        acc.v[h][j][3] += v.w;
+      }
+    __syncwarp();  // read before strip_store overwrites it
+  }
+  return true;
+}
+template <int NT>
+__device__ __forceinline__ void strip_free(const Place<NT>& at) {
+  if (halves_of(NT) == 2 && at.half == 0)
+    named_bar_arrive(kBarPair + Place<NT>::kOwners + at.owner, 64);
+}
+
 // Y of the warp's columns (from n0 on): sums plus addend, through the warp's shared memory, so that
-// a lane reads and writes 16 bytes of a row.
+// a lane reads and writes 16 bytes of a row. An element's addend is read by the lane that writes
+// it, before it does: the two may be the same array.
 template <int NT>
 __device__ __forceinline__ void strip_store(const LoraArgs& a, const Strip<NT>& acc, float* strip,
                                             int n0, int lane) {
   constexpr int kTimes = (NT * 16 + 31) / 32;
-  const int half = lane & 1, n = n0 + half * 8;
-  uint4 extra[kTimes];
-#pragma unroll
-  for (int i = 0; i < kTimes; ++i) {
-    const int m = i * 16 + (lane >> 1);
-    extra[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (a.addend != nullptr && m < a.M && n < a.N)
-      extra[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.addend) +
-                                                 static_cast<int64_t>(m) * a.N + n);
-  }
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    if (8 * j < a.M) {
+  for (int h = 0; h < halves_of(NT); ++h) {
+    const int n = n0 + h * 16 + (lane & 1) * 8;
+    uint4 extra[kTimes];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        strip[(8 * j + 2 * t + (c & 1)) * kStripPitch + g + 8 * (c >> 1)] = acc.v[j][c];
+    for (int i = 0; i < kTimes; ++i) {
+      const int m = i * 16 + (lane >> 1);
+      extra[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.addend != nullptr && m < a.M && n < a.N)
+        extra[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.addend) +
+                                                   static_cast<int64_t>(m) * a.N + n);
     }
-  }
-  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kTimes; ++i) {
-    const int m = i * 16 + (lane >> 1);
-    if (m < a.M && n < a.N) {
-      const float2* v = reinterpret_cast<const float2*>(strip + m * kStripPitch + half * 8);
-      const uint32_t e[4] = {extra[i].x, extra[i].y, extra[i].z, extra[i].w};
-      uint32_t y[4];
+    for (int j = 0; j < NT; ++j) {
+      if (8 * j < a.M) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        y[q] = pack_bf16x2(v[q].x + bf16_bits_to_float(e[q] & 0xFFFFu),
-                           v[q].y + bf16_bits_to_float(e[q] >> 16));
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) +
-                                static_cast<int64_t>(m) * a.N + n) =
-          make_uint4(y[0], y[1], y[2], y[3]);
+        for (int c = 0; c < 4; ++c)
+          strip[(8 * j + 2 * t + (c & 1)) * kStripPitch + g + 8 * (c >> 1)] = acc.v[h][j][c];
+      }
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      const int m = i * 16 + (lane >> 1);
+      if (m < a.M && n < a.N) {
+        const float2* v =
+            reinterpret_cast<const float2*>(strip + m * kStripPitch + (lane & 1) * 8);
+        const uint32_t e[4] = {extra[i].x, extra[i].y, extra[i].z, extra[i].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          y[q] = pack_bf16x2(v[q].x + bf16_bits_to_float(e[q] & 0xFFFFu),
+                             v[q].y + bf16_bits_to_float(e[q] >> 16));
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) +
+                                  static_cast<int64_t>(m) * a.N + n) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+    __syncwarp();  // the strip is read before the next sums overwrite it
   }
-  __syncwarp();  // the strip is read before the next tile's sums overwrite it
 }
 
 // The warp's sums of a tile that blocks first..last share: its share to L2; the last of them to
 // arrive adds all shares up in block order and writes Y.
 template <int NT>
-__device__ __forceinline__ void strip_share(const LoraArgs& a, Strip<NT>& acc, float* strip, int n0,
-                                            int tid, bool is_first, int first, int last) {
-  const int lane = tid & 31;
+__device__ __forceinline__ void strip_share(const LoraArgs& a, Strip<NT>& acc,
+                                            const Place<NT>& at, float* strip, int n0, int lane,
+                                            bool is_first, int first, int last) {
+  constexpr int H = halves_of(NT), kPerRow = 32 * Place<NT>::kOwners;
   auto share = [&](int b, bool head) {
     return reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(b) * 2 + (head ? 1 : 0)) *
-                                                  a.part_floats) + tid;
+                                                  a.part_floats) + at.owner * 32 + lane;
   };
   float4* mine = share(static_cast<int>(blockIdx.x), is_first);
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-    if (8 * j < a.M)
-      mine[j * kConsumers] = make_float4(acc.v[j][0], acc.v[j][1], acc.v[j][2], acc.v[j][3]);
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      if (8 * j < a.M)
+        mine[(j * H + h) * kPerRow] = make_float4(acc.v[h][j][0], acc.v[h][j][1], acc.v[h][j][2],
+                                                  acc.v[h][j][3]);
   __syncwarp();  // the warp's writes, then its arrival
   int old = 0;
-  if (lane == 0)
-    old = count_global(a.counters + first * LoraTeam::kWarps + (tid >> 5));
+  if (lane == 0) old = count_global(a.counters + first * LoraTeam::kWarps + at.owner);
   old = __shfl_sync(0xFFFFFFFFu, old, 0);
   if (old != last - first) return;
   constexpr int kAtOnce = NT <= 2 ? 4 : 2;  // blocks whose shares are on their way at once
-  acc.zero();
-  for (int b0 = first; b0 <= last; b0 += kAtOnce) {
-    float4 w[kAtOnce][NT];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u)
+  for (int h = 0; h < H; ++h) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        w[u][j] = b0 + u <= last && 8 * j < a.M
-                      ? __ldcg(share(b0 + u, b0 + u == first) + j * kConsumers)
-                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u)
+      for (int c = 0; c < 4; ++c) acc.v[h][j][c] = 0.0f;
+    for (int b0 = first; b0 <= last; b0 += kAtOnce) {
+      float4 w[kAtOnce][NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        acc.v[j][0] += w[u][j].x;
-        acc.v[j][1] += w[u][j].y;
-        acc.v[j][2] += w[u][j].z;
-        acc.v[j][3] += w[u][j].w;
-      }
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          w[u][j] = b0 + u <= last && 8 * j < a.M
+                        ? __ldcg(share(b0 + u, b0 + u == first) + (j * H + h) * kPerRow)
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc.v[h][j][0] += w[u][j].x;
+          acc.v[h][j][1] += w[u][j].y;
+          acc.v[h][j][2] += w[u][j].z;
+          acc.v[h][j][3] += w[u][j].w;
+        }
+    }
   }
   strip_store<NT>(a, acc, strip, n0, lane);
 }
@@ -697,7 +794,10 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       all_started = true;
     };
     if constexpr (!kIsF32) {
-      float* strip = red + warp * ((a.M + 7) / 8 * 8) * kStripPitch;
+      const Place<NT> place(warp);
+      // (A pair's strip is two warps' long.)
+      float* strip = red + place.owner * (halves_of(NT) * NT * 8 * kStripPitch);
+      strip_free<NT>(place);
       segments([&](int cb, int k0, int k1) {
         Strip<NT> acc;
         acc.zero();
@@ -707,25 +807,31 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
           const uint32_t stage =
               smem_u32(ring.weights) + static_cast<uint32_t>(cur.stage) * kStageBytes;
           if (k < k_steps) {
-            strip_stage<NT>(acc, stage, ring.rows + cur.stage * ring.row_bytes, warp, lane,
+            strip_stage<NT>(acc, place, stage, ring.rows + cur.stage * ring.row_bytes, lane,
                             k * 2 * kBoxRows, a.K, release);
           } else {
-            strip_expand<NT>(acc, stage, warp, lane, tb, S_mem, a.M,
+            strip_expand<NT>(acc, place, stage, lane, tb, S_mem, a.M,
                              (k - k_steps) * kStagePieces, n_pieces, per_slot);
             release();
           }
           cur.next(ring.stages);
         }
-        const int n0 = cb * S::kCols + warp * 16;
+        if (!strip_meet<NT>(acc, place, strip, lane)) return true;
+        const int n0 = cb * S::kCols + place.owner * 16 * halves_of(NT);
         if (k0 == 0 && k1 == steps) {
           strip_store<NT>(a, acc, strip, n0, lane);
         } else {
           const long long at = static_cast<long long>(cb) * steps;
           wait_started(lane == 0);
-          strip_share<NT>(a, acc, strip, n0, tid, k0 == 0, sp.owner(at), sp.owner(at + steps - 1));
+          strip_share<NT>(a, acc, place, strip, n0, lane, k0 == 0, sp.owner(at),
+                          sp.owner(at + steps - 1));
         }
+        strip_free<NT>(place);
         return true;
       });
+      // (The last arrival there: no barrier is left half way.)
+      if (halves_of(NT) == 2 && place.half == 1)
+        named_bar_sync(kBarPair + Place<NT>::kOwners + place.owner, 64);
     } else {
       RedTurn<WK> turn{red};
       const int first_row = (warp >> 2) * kBoxRows + warp_row<WK>(warp);
