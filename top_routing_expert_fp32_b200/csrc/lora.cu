@@ -3,8 +3,9 @@
 // for at most 64 rows, in one cooperative kernel (more rows: lora_sm100.cu, lora_f32.cu).
 //
 // What bounds it: one pass over W (and over the used adapters). W runs through the ring of
-// stream.cuh in equal shares per block, as the few-token layer's down projection does. The
-// adapters' part hides behind it:
+// stream.cuh in equal shares per block, as the few-token layer's down projection does; on top come
+// the launch, the first stage's latency (4 us) and the last tiles' sums (3 us). The adapters' part
+// hides behind the stream:
 //   1. Shrink. Beside the stream, two warps compute S = X A: block (row, slice of K), a 16-byte
 //      piece of an A row per thread, fp32 partial sums to L2. They arrive at the grid barrier,
 //      wait for it, add everybody's partial sums up in shared memory and tell the consumers.
@@ -81,8 +82,8 @@ constexpr size_t kMaxSmem = 232448;
 __host__ __device__ constexpr size_t s_bytes(int M, int rank) {
   return sizeof(float) * static_cast<size_t>((M + 7) / 8 * 8) * pieces_of(rank) * kPieceRanks;
 }
-// The consumers' sums: fp32 as in the few-token layer; bf16 per warp, or pair of warps, 16 columns of
-// the rows at kStripPitch floats a row, or the sums that a pair exchanges.
+// The consumers' sums: fp32 as in the few-token layer; bf16 per warp, or pair of warps, 16 columns
+// of the rows at kStripPitch floats a row, or the sums that a pair exchanges.
 constexpr int kStripPitch = 18;
 __host__ __device__ constexpr int row_tiles_of(int M) {  // kernels are made for these
   const int n = (M + 7) / 8;
@@ -209,7 +210,8 @@ __device__ void gather_s(const LoraArgs& a, LoraTables& tb, uint8_t* S, int sid)
   while (per * 2 <= a.slices && per * 2 * n <= kSideThreads) per *= 2;
   if (per > 1) {
     const int i = sid % n, part = sid / n;
-    if (part < per) tb.scratch[part * n + i] = sum_partials<8>(a.part_s + i, n, part, per, a.slices);
+    if (part < per)
+      tb.scratch[part * n + i] = sum_partials<8>(a.part_s + i, n, part, per, a.slices);
     named_bar_sync(kBarSide, kSideThreads);
     if (sid < n) {
       float s = 0.0f;
@@ -292,12 +294,13 @@ __device__ __forceinline__ void expand_f32(Acc<kF32, NT>& acc, uint32_t box, int
 
 // ---- bf16 consumers. A warp owns 16 columns of the tile and all of the reduction, so its sums are
 // final in its registers: it needs neither the other warps nor a barrier to write them, or its
-// share of them, and goes on with the next tile while others still multiply. (With the reduction
-// cut over four warps as in the few-token layer, whose sums meet in shared memory eight rows at a
-// time, 48 rows took 43 us, 11 of them for that.) It pays with shared-memory reads, since every
-// warp reads all the activation rows: above 32 rows a pair of warps owns 32 columns, half of the
-// reduction each, and the second hands its sums to the first (48 rows: 45 us without the pairs,
-// ... with them).
+// share of them, and goes on with the next tile while others still multiply. It pays with
+// shared-memory reads, since every warp reads all the activation rows: above 32 rows a pair of
+// warps owns 32 columns, half of the reduction each, and the second hands its sums to the first.
+// Against the few-token layer's way (the reduction over four warps, whose sums meet in shared
+// memory eight rows at a time): 1 row of 4096 x 4096 13.2 us against 13.6, 32 rows of
+// 4096 x 14336 with their adapters 33.8 against 35.2, 48 rows 42.7 against 43.2 (45.0 without
+// the pairs).
 constexpr int halves_of(int NT) { return NT > 4 ? 2 : 1; }
 
 // Sums v[h][j][c]: row 8 j + 2 t + (c & 1), column 16 h + g + 8 (c >> 1) of the warp's, where
@@ -963,7 +966,8 @@ cudaError_t launch_few(const moe_lora_problem& p, const LoraArgs& a, const void*
 size_t lora_few_workspace_bytes(const moe_lora_problem& p) {
   const int64_t M = std::min<int64_t>(p.M, kMaxRows);
   return up256(sizeof(float) * kMaxGrid * p.rank) +  // slices x rows
-         up256(sizeof(int) * kMaxGrid * LoraTeam::kWarps) + up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(M));
+         up256(sizeof(int) * kMaxGrid * LoraTeam::kWarps) +
+         up256(sizeof(float) * 2 * kMaxGrid * lora_part_floats(M));
 }
 
 cudaError_t launch_lora_few(const moe_lora_problem& p, const LoraTensors& t, void* scratch,

@@ -231,13 +231,13 @@ struct Frag {
       }
   }
 
-  // From plain rows: 32-value group `group`; k0: its first k within the reduction of K (past its end
-  // nothing was copied: zeros; K is a multiple of 8).
+  // From plain rows: 32-value group `group`; k0: its first k within the reduction of K (past its
+  // end nothing was copied: zeros; K is a multiple of 8).
   __device__ __forceinline__ void load_rows(const uint8_t* rows, int row_pitch, int group, int k0,
                                             int K, int lane) {
     static_assert(!SPLIT, "one plane");
-    const uint32_t at =
-        smem_u32(rows) + static_cast<uint32_t>((lane & 7) * row_pitch + group * 64 + (lane >> 3) * 16);
+    const uint32_t at = smem_u32(rows) + static_cast<uint32_t>((lane & 7) * row_pitch +
+                                                               group * 64 + (lane >> 3) * 16);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       ldsm_x4(at + static_cast<uint32_t>(8 * j * row_pitch), r[j][0]);
