@@ -46,7 +46,7 @@ struct LoraArgs {
   void* Y;
   float* part_s;   // [slices][M][rank]
   float* part;     // [grid][2][part_floats]: sums of shared tiles
-  int* counters;   // [kMaxGrid][kWarps]: arrivals at shared tiles, per warp for bf16
+  int* counters;   // [kMaxGrid][kWarps]: the warps' arrivals at shared tiles
   int* bar;        // [3] workspace header ints, zero at rest: blocks that started, blocks that
                    // have their partial S out, blocks that finished
   int* err;
@@ -78,6 +78,7 @@ __host__ __device__ constexpr int pieces_of(int rank) {
 }
 
 constexpr size_t kMaxSmem = 232448;
+static_assert(2 * LoraTeam::kWarps * 16 * 32 * sizeof(float) <= kRedBytes, "the parts' sums");
 // S: whole row tiles of whole pieces, fp32 or two bf16 terms, zeros beyond M and the rank.
 __host__ __device__ constexpr size_t s_bytes(int M, int rank) {
   return sizeof(float) * static_cast<size_t>((M + 7) / 8 * 8) * pieces_of(rank) * kPieceRanks;
@@ -245,51 +246,183 @@ __device__ void gather_s(const LoraArgs& a, LoraTables& tb, uint8_t* S, int sid)
   }
 }
 
-// fp32: two columns of a row of the addend (zeros without one), and of Y. Each value is read and
-// written by one thread, the addend first, so the two may be the same array.
-__device__ __forceinline__ float2 load_addend(const LoraArgs& a, int m, int n) {
-  if (a.addend == nullptr || m >= a.M || n >= a.N) return make_float2(0.0f, 0.0f);
-  return *reinterpret_cast<const float2*>(static_cast<const float*>(a.addend) +
-                                          static_cast<int64_t>(m) * a.N + n);
-}
-__device__ __forceinline__ void store_y(const LoraArgs& a, int m, int n, float2 v) {
-  if (m >= a.M || n >= a.N) return;
-  *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + static_cast<int64_t>(m) * a.N + n) = v;
+// ---- fp32 consumers, on the CUDA cores. A warp has eight rows, both 32-column boxes of the tile
+// (a lane one column of each) and 1 / kParts of a stage's k; where there are fewer row tiles than
+// warps, the parts' sums meet in shared memory. The loops are rolled: with the rows of all tiles
+// unrolled in every warp a short call spent 11 us fetching instructions (64 rows, K = 64).
+template <int NT>
+struct RowsF32 {
+  static constexpr int kParts = LoraTeam::kWarps / NT;
+  static constexpr int kMine = 16 / kParts;  // of the (box, row) sums of a row tile, per warp
+  float v[2][8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[0][r] = v[1][r] = 0.0f;
+  }
+};
+
+__device__ __forceinline__ float ld_weight_f32(uint32_t box, int row, int lane) {
+  const uint32_t r = static_cast<uint32_t>(row), l = static_cast<uint32_t>(lane);
+  float w;
+  asm volatile("ld.shared.f32 %0, [%1];"
+               : "=f"(w)
+               : "r"(box + r * 128 + (((l >> 2) ^ (r & 7u)) << 4) + (l & 3u) * 4)
+               : "memory");
+  return w;
 }
 
-// fp32: acc += S x (this warp's two pieces of an adapters' stage). `box`: the warp's box, `piece0`:
-// the first piece of the tile's list that it holds.
+// acc += the warp's k of a stage. `x`: shared address of its first row. 16 terms at a time on their
+// own, which keeps the rounding error low.
 template <int NT>
-__device__ __forceinline__ void expand_f32(Acc<kF32, NT>& acc, uint32_t box, int warp, int lane,
-                                           const LoraTables& tb, const uint8_t* S, int piece0,
-                                           int n_pieces, int per_slot) {
+__device__ __forceinline__ void stage_f32(RowsF32<NT>& acc, uint32_t stage, uint32_t x, int part,
+                                          int lane, int k0, int K) {
+  constexpr int kDepth = 2 * kBoxRows / RowsF32<NT>::kParts;
+#pragma unroll 1
+  for (int k = part * kDepth; k < (part + 1) * kDepth && k0 + k < K; k += 16) {
+    const uint32_t box = stage + static_cast<uint32_t>(k / kBoxRows) * 2 * kBoxBytes;
+    float s[2][8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s[0][r] = s[1][r] = 0.0f;
+#pragma unroll 1
+    for (int q = k; q < k + 16 && k0 + q < K; q += 4) {
+      float w[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          w[c][i] = ld_weight_f32(box + c * kBoxBytes, q % kBoxRows + i, lane);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float4 v = ld_shared_f4(x + static_cast<uint32_t>(r * kRowPitch128F32 + q * 4));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          s[c][r] = fmaf(w[c][0], v.x, s[c][r]);
+          s[c][r] = fmaf(w[c][1], v.y, s[c][r]);
+          s[c][r] = fmaf(w[c][2], v.z, s[c][r]);
+          s[c][r] = fmaf(w[c][3], v.w, s[c][r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      acc.v[0][r] += s[0][r];
+      acc.v[1][r] += s[1][r];
+    }
+  }
+}
+
+// acc += S x (every kParts-th of the pieces, from piece0 on, of an adapters' stage).
+template <int NT>
+__device__ __forceinline__ void expand_f32(RowsF32<NT>& acc, uint32_t stage, int tile, int part,
+                                           int lane, const LoraTables& tb, const uint8_t* S,
+                                           int piece0, int n_pieces, int per_slot) {
   const int ranks = per_slot * kPieceRanks;
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
+  for (int h = part; h < kStagePieces; h += RowsF32<NT>::kParts) {
     const int piece = piece0 + h;
     if (piece >= n_pieces) return;
     const int slot = piece / per_slot, r0 = (piece - slot * per_slot) * kPieceRanks;
-    const uint64_t rows = tb.slot_rows[slot];
-    const uint32_t row0 = static_cast<uint32_t>((warp & 1) * 32 + h * kPieceRanks);
-    float w[kPieceRanks];
+    const uint32_t mine = static_cast<uint32_t>(tb.slot_rows[slot] >> (8 * tile)) & 0xFFu;
+    if (mine == 0) continue;
+    const uint32_t box = stage + static_cast<uint32_t>(h >> 2) * 2 * kBoxBytes;
+    float w[2][kPieceRanks];
 #pragma unroll
-    for (int i = 0; i < kPieceRanks; ++i) {
-      const uint32_t r = row0 + i;
-      const uint32_t at = box + r * 128 + (((static_cast<uint32_t>(lane) >> 2) ^ (r & 7u)) << 4) +
-                          (static_cast<uint32_t>(lane) & 3u) * 4;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at) : "memory");
-    }
+    for (int i = 0; i < kPieceRanks; ++i)
 #pragma unroll
-    for (int m = 0; m < 8 * NT; ++m) {
-      if ((rows >> m) & 1ull) {
-        const float* s = reinterpret_cast<const float*>(S) + m * ranks + r0;
-        float sum = 0.0f;
+      for (int c = 0; c < 2; ++c)
+        w[c][i] = ld_weight_f32(box + c * kBoxBytes, (h & 3) * kPieceRanks + i, lane);
 #pragma unroll
-        for (int i = 0; i < kPieceRanks; ++i) sum = fmaf(w[i], s[i], sum);
-        acc.v[m] += sum;
+    for (int r = 0; r < 8; ++r) {
+      if ((mine >> r) & 1u) {
+        const float* s = reinterpret_cast<const float*>(S) + (8 * tile + r) * ranks + r0;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPieceRanks; ++i) {
+          s0 = fmaf(w[0][i], s[i], s0);
+          s1 = fmaf(w[1][i], s[i], s1);
+        }
+        acc.v[0][r] += s0;
+        acc.v[1][r] += s1;
       }
     }
   }
+}
+
+// Y of kMine sums of one lane: those from `first` on of its (box, row) pairs, box-major. An
+// element's addend is read by the lane that writes it, before it does.
+template <int NT>
+__device__ __forceinline__ void store_f32(const LoraArgs& a, const float (&v)[RowsF32<NT>::kMine],
+                                          int first, int tile, int n0, int lane) {
+  const float* addend = static_cast<const float*>(a.addend);
+  int64_t at[RowsF32<NT>::kMine];
+  float e[RowsF32<NT>::kMine];
+#pragma unroll
+  for (int q = 0; q < RowsF32<NT>::kMine; ++q) {
+    const int i = first + q, m = 8 * tile + (i & 7), n = n0 + (i >> 3) * 32 + lane;
+    at[q] = m < a.M && n < a.N ? static_cast<int64_t>(m) * a.N + n : -1;
+    e[q] = addend != nullptr && at[q] >= 0 ? addend[at[q]] : 0.0f;
+  }
+#pragma unroll
+  for (int q = 0; q < RowsF32<NT>::kMine; ++q)
+    if (at[q] >= 0) static_cast<float*>(a.Y)[at[q]] = v[q] + e[q];
+}
+
+// A tile's end: the parts' sums together, then Y, or the warp's share of a tile that blocks
+// first..last share, whose last arrival adds the shares up in block order.
+template <int NT>
+__device__ __forceinline__ void finish_f32(const LoraArgs& a, const RowsF32<NT>& acc, float* red,
+                                           int n0, int tid, bool whole, bool is_first, int first,
+                                           int last) {
+  using R = RowsF32<NT>;
+  const int lane = tid & 31, warp = tid >> 5, tile = warp % NT, part = warp / NT;
+  const int mine = part * R::kMine;  // the first of the warp's sums
+  float v[R::kMine];
+  if constexpr (R::kParts == 1) {
+#pragma unroll
+    for (int q = 0; q < R::kMine; ++q) v[q] = acc.v[q >> 3][q & 7];
+  } else {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) red[(warp * 16 + q) * 32 + lane] = acc.v[q >> 3][q & 7];
+    named_bar_sync(kBarConsumers, kConsumers);
+#pragma unroll
+    for (int q = 0; q < R::kMine; ++q) {
+      v[q] = 0.0f;
+#pragma unroll
+      for (int p = 0; p < R::kParts; ++p)
+        v[q] += red[((p * NT + tile) * 16 + mine + q) * 32 + lane];
+    }
+  }
+  if (8 * tile >= a.M) return;
+  if (!whole) {
+    auto share = [&](int b, bool head) {
+      return a.part + (static_cast<int64_t>(b) * 2 + (head ? 1 : 0)) * a.part_floats +
+             warp * (R::kMine * 32) + lane;
+    };
+    float* out = share(static_cast<int>(blockIdx.x), is_first);
+#pragma unroll
+    for (int q = 0; q < R::kMine; ++q) out[q * 32] = v[q];
+    __syncwarp();  // the warp's writes, then its arrival
+    int old = 0;
+    if (lane == 0) old = count_global(a.counters + first * LoraTeam::kWarps + warp);
+    old = __shfl_sync(0xFFFFFFFFu, old, 0);
+    if (old != last - first) return;
+    // (The sums of four blocks are on their way at once.)
+#pragma unroll
+    for (int q = 0; q < R::kMine; ++q) v[q] = 0.0f;
+    for (int b0 = first; b0 <= last; b0 += 4) {
+      float w[4][R::kMine];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int q = 0; q < R::kMine; ++q)
+          w[u][q] = b0 + u <= last ? __ldcg(share(b0 + u, b0 + u == first) + q * 32) : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int q = 0; q < R::kMine; ++q) v[q] += w[u][q];
+    }
+  }
+  store_f32<NT>(a, v, mine, tile, n0, lane);
 }
 
 // ---- bf16 consumers. A warp owns 16 columns of the tile and all of the reduction, so its sums are
@@ -572,7 +705,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mb,
                 const __grid_constant__ LoraArgs a) {
   using S = Shape<WK>;
-  using P = Places<WK>;
   constexpr bool kIsF32 = WK == kF32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -836,78 +968,35 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       if (halves_of(NT) == 2 && place.half == 1)
         named_bar_sync(kBarPair + Place<NT>::kOwners + place.owner, 64);
     } else {
-      RedTurn<WK> turn{red};
-      const int first_row = (warp >> 2) * kBoxRows + warp_row<WK>(warp);
+      const int tile = warp % NT, part = warp / NT;
+      int turn = 0;  // of two buffers: a write there is past the barrier after the last read
       segments([&](int cb, int k0, int k1) {
-        Acc<WK, NT> acc;
+        RowsF32<NT> acc;
         acc.zero();
         for (int k = k0; k < k1; ++k) {
           if (k >= k_steps) take_s();
           wait_stage();
-          const uint32_t box = smem_u32(ring.weights) +
-                               static_cast<uint32_t>(cur.stage) * kStageBytes +
-                               static_cast<uint32_t>(warp >> 1) * kBoxBytes;
-          const uint8_t* rows = ring.rows + cur.stage * ring.row_bytes;
-          if (k >= k_steps)
-            expand_f32<NT>(acc, box, warp, lane, tb, S_mem,
-                           (k - k_steps) * kStagePieces + (warp >> 2) * 4 + (warp & 1) * 2,
-                           n_pieces, per_slot);
-          else
-            multiply_f32<NT>(acc, box, warp, lane, smem_u32(rows) + first_row * 4, kRowPitch128F32,
-                             a.M, k * 2 * kBoxRows + first_row, a.K);
+          const uint32_t stage =
+              smem_u32(ring.weights) + static_cast<uint32_t>(cur.stage) * kStageBytes;
+          if (8 * tile < a.M) {
+            if (k >= k_steps)
+              expand_f32<NT>(acc, stage, tile, part, lane, tb, S_mem,
+                             (k - k_steps) * kStagePieces, n_pieces, per_slot);
+            else
+              stage_f32<NT>(acc, stage,
+                            smem_u32(ring.rows) + static_cast<uint32_t>(
+                                cur.stage * ring.row_bytes + 8 * tile * kRowPitch128F32),
+                            part, lane, k * 2 * kBoxRows, a.K);
+          }
           release();
           cur.next(ring.stages);
         }
         const bool whole = k0 == 0 && k1 == steps;
-        float2* mine = reinterpret_cast<float2*>(
-            a.part + (static_cast<int64_t>(me) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (8 * j >= a.M) break;
-          float2 extra[P::kMine];  // loaded before the warps' sums meet
-#pragma unroll
-          for (int q = 0; q < P::kMine; ++q) {
-            const int i = tid + q * kConsumers;
-            extra[q] = whole ? load_addend(a, 8 * j + P::row(i), cb * S::kCols + P::col(i))
-                             : make_float2(0.0f, 0.0f);
-          }
-          float* sums = turn.next();
-          put_tile<WK, NT>(sums, acc, j, warp, lane);
-          named_bar_sync(kBarConsumers, kConsumers);
-#pragma unroll
-          for (int q = 0; q < P::kMine; ++q) {
-            const int i = tid + q * kConsumers;
-            float2 v = take_pair<WK>(sums, -1, P::row(i), P::col(i));
-            v.x += extra[q].x;
-            v.y += extra[q].y;
-            if (whole) store_y(a, 8 * j + P::row(i), cb * S::kCols + P::col(i), v);
-            else mine[j * P::kCount + i] = v;
-          }
-        }
-        if (!whole) {
-          const long long at = static_cast<long long>(cb) * steps;
-          const int first = sp.owner(at), last = sp.owner(at + steps - 1);
-          wait_started(tid == 0);
-          if (last_to_finish<kConsumers>(a.counters + first * LoraTeam::kWarps, last - first + 1,
-                                         tid, &tb.flag)) {
-            constexpr int kChunk = 8;
-            const int limit = (a.M + 7) / 8 * P::kCount;
-            for (int i0 = tid; i0 < limit; i0 += kChunk * kConsumers) {
-              float2 v[kChunk];
-#pragma unroll
-              for (int q = 0; q < kChunk; ++q) {
-                const int i = i0 + q * kConsumers;
-                v[q] = load_addend(a, P::row(i), cb * S::kCols + P::col(i));
-              }
-              add_shares<kConsumers>(v, a.part, a.part_floats, first, last, i0, limit);
-#pragma unroll
-              for (int q = 0; q < kChunk; ++q) {
-                const int i = i0 + q * kConsumers;
-                if (i < limit) store_y(a, P::row(i), cb * S::kCols + P::col(i), v[q]);
-              }
-            }
-          }
-        }
+        const long long at = static_cast<long long>(cb) * steps;
+        if (!whole) wait_started(lane == 0);
+        turn ^= 1;
+        finish_f32<NT>(a, acc, red + turn * (LoraTeam::kWarps * 16 * 32), cb * S::kCols, tid, whole,
+                       k0 == 0, whole ? 0 : sp.owner(at), whole ? 0 : sp.owner(at + steps - 1));
         return true;
       });
     }
