@@ -1,7 +1,9 @@
 // fp32 form of the shared projection with per-row adapters for more than 64 rows (see lora.cu),
 // on the CUDA cores: S = scale (X A), then 64 x 64 tiles of X W whose epilogue adds S B and the
-// addend. Sums are kept in runs of 64 terms that are added up afterwards, so the rounding error
-// grows with the run length, not with K.
+// addend. Bound by the FMA and shared-memory pipes for many tiles; few tiles cut K over the blocks
+// of a cluster, whose sums meet in distributed shared memory (128 rows, 4096 x 512: 58 us, without
+// the cut and the prefetch 241). Sums are kept in runs of 64 terms that are added up afterwards, so
+// the rounding error grows with the run length, not with K.
 #include <algorithm>
 #include <cstdint>
 
@@ -12,8 +14,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kShrinkThreads = 128;
+constexpr int kShrinkThreads = 512;
 constexpr int kTile = 64, kDepth = 16, kRun = 64, kThreads = 256;
+constexpr int kMaxSplits = 8;
 
 // One block per row: 4 ranks per thread, the rest of the threads over k.
 __global__ void __launch_bounds__(kShrinkThreads)
@@ -35,15 +38,26 @@ __global__ void __launch_bounds__(kShrinkThreads)
     for (int k0 = sub; k0 < K; k0 += subs * kRun) {
       float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
       const int k1 = min(K, k0 + subs * kRun);
-#pragma unroll 4
-      for (int k = k0; k < k1; k += subs) {
-        const float x = X[m * K + k];
-        const float4 w = __ldg(reinterpret_cast<const float4*>(
-            A + (static_cast<int64_t>(ad) * K + k) * rank + v * 4));
-        run.x = fmaf(x, w.x, run.x);
-        run.y = fmaf(x, w.y, run.y);
-        run.z = fmaf(x, w.z, run.z);
-        run.w = fmaf(x, w.w, run.w);
+      constexpr int kAtOnce = 8;  // k whose loads are on their way at once
+      for (int kk = k0; kk < k1; kk += kAtOnce * subs) {
+        float x[kAtOnce];
+        float4 w[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int k = kk + u * subs;
+          const bool in = k < k1;
+          x[u] = in ? X[m * K + k] : 0.f;
+          w[u] = in ? __ldg(reinterpret_cast<const float4*>(
+                          A + (static_cast<int64_t>(ad) * K + k) * rank + v * 4))
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          run.x = fmaf(x[u], w[u].x, run.x);
+          run.y = fmaf(x[u], w[u].y, run.y);
+          run.z = fmaf(x[u], w[u].z, run.z);
+          run.w = fmaf(x[u], w[u].w, run.w);
+        }
       }
       acc.x += run.x;
       acc.y += run.y;
@@ -60,50 +74,63 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
 }
 
+// Tile (blockIdx.y, blockIdx.x), share blockIdx.z of K; the shares of a tile are one cluster.
 __global__ void __launch_bounds__(kThreads)
     project_f32_kernel(const float* __restrict__ X, const float* __restrict__ W,
                        const float* __restrict__ B, const int32_t* __restrict__ adapter,
                        const float* __restrict__ S, const float* addend, float* Y, int64_t M,
                        int K, int N, int L, int rank) {
-  __shared__ float xs[kDepth][kTile + 4];
-  __shared__ float ws[kDepth][kTile];
+  struct Stage {
+    float x[kDepth][kTile + 4];
+    float w[kDepth][kTile];
+  };
+  __shared__ __align__(16) Stage stages[2];
+  static_assert(sizeof(stages) >= sizeof(float) * kTile * kTile, "the sums take their place");
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile;
   const int n0 = static_cast<int>(blockIdx.x) * kTile;
-  const int tr = static_cast<int>(threadIdx.x) / 16, tc = static_cast<int>(threadIdx.x) % 16;
+  const int tid = static_cast<int>(threadIdx.x), tr = tid / 16, tc = tid % 16;
+  const int splits = static_cast<int>(gridDim.z), split = static_cast<int>(blockIdx.z);
+  const int chunk = (K + splits * kRun - 1) / (splits * kRun) * kRun;
+  const int k_begin = min(K, split * chunk), k_end = min(K, k_begin + chunk);
+
+  // 64 rows x 16 k of X, 16 k x 64 columns of W: a float4 of each per thread.
+  const int lr = tid / 4, lk = tid % 4 * 4;
+  float4 x, w;
+  auto load = [&](int k0) {
+    x = w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m0 + lr < M && k0 + lk < k_end)
+      x = *reinterpret_cast<const float4*>(X + (m0 + lr) * K + k0 + lk);
+    if (k0 + tr < k_end && n0 + tc * 4 < N)
+      w = __ldg(reinterpret_cast<const float4*>(W + static_cast<int64_t>(k0 + tr) * N + n0 +
+                                                tc * 4));
+  };
+  auto put = [&](Stage& st) {
+    st.x[lk][lr] = x.x;
+    st.x[lk + 1][lr] = x.y;
+    st.x[lk + 2][lr] = x.z;
+    st.x[lk + 3][lr] = x.w;
+    *reinterpret_cast<float4*>(&st.w[tr][tc * 4]) = w;
+  };
   float acc[4][4] = {}, run[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += kDepth) {
-    {  // 64 rows x 16 k of X, 16 k x 64 columns of W: one float4 each
-      const int r = static_cast<int>(threadIdx.x) / 4, k = (static_cast<int>(threadIdx.x) % 4) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m0 + r < M && k0 + k < K)
-        x = *reinterpret_cast<const float4*>(X + (m0 + r) * K + k0 + k);
-      xs[k][r] = x.x;
-      xs[k + 1][r] = x.y;
-      xs[k + 2][r] = x.z;
-      xs[k + 3][r] = x.w;
-      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k0 + tr < K && n0 + tc * 4 < N)
-        w = __ldg(reinterpret_cast<const float4*>(W + static_cast<int64_t>(k0 + tr) * N + n0 +
-                                                  tc * 4));
-      *reinterpret_cast<float4*>(&ws[tr][tc * 4]) = w;
-    }
-    __syncthreads();
+  load(k_begin);
+  put(stages[0]);
+  __syncthreads();
+  int cur = 0;
+  for (int k0 = k_begin; k0 < k_end; k0 += kDepth, cur ^= 1) {
+    const bool more = k0 + kDepth < k_end;
+    if (more) load(k0 + kDepth);  // under way during this stage's products
+    const Stage& st = stages[cur];
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
-      float x[4];
+      const float4 xv = *reinterpret_cast<const float4*>(&st.x[k][tr * 4]);
+      const float4 wv = *reinterpret_cast<const float4*>(&st.w[k][tc * 4]);
+      const float xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = xs[k][tr * 4 + i];
-      const float4 w = *reinterpret_cast<const float4*>(&ws[k][tc * 4]);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        run[i][0] = fmaf(x[i], w.x, run[i][0]);
-        run[i][1] = fmaf(x[i], w.y, run[i][1]);
-        run[i][2] = fmaf(x[i], w.z, run[i][2]);
-        run[i][3] = fmaf(x[i], w.w, run[i][3]);
-      }
+        for (int j = 0; j < 4; ++j) run[i][j] = fmaf(xs[i], ws[j], run[i][j]);
     }
-    __syncthreads();
-    if ((k0 / kDepth) % (kRun / kDepth) == kRun / kDepth - 1 || k0 + kDepth >= K) {
+    if (((k0 - k_begin) / kDepth) % (kRun / kDepth) == kRun / kDepth - 1 || !more) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -112,27 +139,54 @@ __global__ void __launch_bounds__(kThreads)
           run[i][j] = 0.f;
         }
     }
+    if (more) put(stages[cur ^ 1]);  // last read before the barrier of the step before
+    __syncthreads();
   }
-  const int n = n0 + tc * 4;
-  if (n >= N) return;
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + tr * 4 + i;
-    if (m >= M) break;
-    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  // The block's sums in place of the stages; each block then finishes its share of the rows.
+  float* sums = reinterpret_cast<float*>(stages);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(sums + (tr * 4 + i) * kTile + tc * 4) =
+        make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  cluster_sync_all();
+  const int rows = kTile / splits;
+  for (int item = tid; item < rows * (kTile / 4); item += kThreads) {
+    const int r0 = split * rows + item / (kTile / 4), c4 = item % (kTile / 4) * 4;
+    const int64_t m = m0 + r0;
+    const int n = n0 + c4;
+    if (m >= M || n >= N) continue;
+    const uint32_t here = smem_u32(sums + r0 * kTile + c4);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < splits; ++b) {
+      float4 v;
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                   : "r"(mapa_shared(here, static_cast<uint32_t>(b)))
+                   : "memory");
+      y.x += v.x;
+      y.y += v.y;
+      y.z += v.z;
+      y.w += v.w;
+    }
     const int ad = adapter[m];
     if (ad >= 0 && ad < L) {
       const float* s = S + m * rank;
       const float* b = B + static_cast<int64_t>(ad) * rank * N + n;
+      float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int r = 0; r < rank; ++r) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(b + static_cast<int64_t>(r) * N));
-        d.x = fmaf(s[r], w.x, d.x);
-        d.y = fmaf(s[r], w.y, d.y);
-        d.z = fmaf(s[r], w.z, d.z);
-        d.w = fmaf(s[r], w.w, d.w);
+        const float4 bv = __ldg(reinterpret_cast<const float4*>(b + static_cast<int64_t>(r) * N));
+        d.x = fmaf(s[r], bv.x, d.x);
+        d.y = fmaf(s[r], bv.y, d.y);
+        d.z = fmaf(s[r], bv.z, d.z);
+        d.w = fmaf(s[r], bv.w, d.w);
       }
+      y.x += d.x;
+      y.y += d.y;
+      y.z += d.z;
+      y.w += d.w;
     }
-    float4 y = make_float4(acc[i][0] + d.x, acc[i][1] + d.y, acc[i][2] + d.z, acc[i][3] + d.w);
     if (addend != nullptr) {
       const float4 q = *reinterpret_cast<const float4*>(addend + m * N + n);
       y.x += q.x;
@@ -142,6 +196,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     *reinterpret_cast<float4*>(Y + m * N + n) = y;
   }
+  cluster_sync_all();  // no block leaves while another reads its sums
 }
 
 }  // namespace
@@ -162,15 +217,33 @@ cudaError_t launch_lora_f32(const moe_lora_problem& p, const LoraTensors& t, voi
   const int64_t rows_per_launch = int64_t(65535) * kTile;
   for (int64_t m = 0; m < p.M; m += rows_per_launch) {
     const int64_t rows = std::min(rows_per_launch, p.M - m);
-    const dim3 grid(static_cast<unsigned>((p.N + kTile - 1) / kTile),
-                    static_cast<unsigned>((rows + kTile - 1) / kTile));
-    project_f32_kernel<<<grid, kThreads, 0, stream>>>(
-        static_cast<const float*>(t.X) + m * p.K, static_cast<const float*>(t.W),
-        static_cast<const float*>(t.B), t.adapter + m, S + m * p.rank,
-        t.addend != nullptr ? static_cast<const float*>(t.addend) + m * p.N : nullptr,
-        static_cast<float*>(t.Y) + m * p.N, rows, static_cast<int>(p.K), static_cast<int>(p.N),
-        p.adapters, p.rank);
-    e = cudaGetLastError();
+    const int64_t tiles = (p.N + kTile - 1) / kTile * ((rows + kTile - 1) / kTile);
+    // K over a cluster's blocks until the device has four blocks per SM, 128 k each at least.
+    int splits = 1;
+    while (splits < kMaxSplits && tiles * splits * 2 <= 4 * num_sms() && p.K >= 256 * splits)
+      splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.N + kTile - 1) / kTile),
+                       static_cast<unsigned>((rows + kTile - 1) / kTile),
+                       static_cast<unsigned>(splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const float* addend =
+        t.addend != nullptr ? static_cast<const float*>(t.addend) + m * p.N : nullptr;
+    e = cudaLaunchKernelEx(&cfg, project_f32_kernel, static_cast<const float*>(t.X) + m * p.K,
+                           static_cast<const float*>(t.W), static_cast<const float*>(t.B),
+                           t.adapter + m, static_cast<const float*>(S) + m * p.rank, addend,
+                           static_cast<float*>(t.Y) + m * p.N, rows, static_cast<int>(p.K),
+                           static_cast<int>(p.N), static_cast<int>(p.adapters),
+                           static_cast<int>(p.rank));
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
