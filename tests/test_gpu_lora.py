@@ -101,6 +101,14 @@ FEW = [
     dict(M=5, K=100, N=516, L=3, r=12, dtype=F32, addend=True),
     dict(M=30, K=512, N=68, L=9, r=128, dtype=F32, none=0.2),
     dict(M=64, K=64, N=128, L=4, r=8, dtype=F32, addend=True),
+    dict(M=12, K=4096, N=40, L=3, r=16, addend=True),                # a tile shared by many blocks
+    dict(M=40, K=1000, N=136, L=30, r=24, addend=True),              # pairs of warps
+    dict(M=50, K=256, N=20480, L=50, r=16, addend=True),             # and whole tiles
+    dict(M=63, K=4096, N=4096, L=5, r=96, none=0.2),
+    dict(M=12, K=260, N=1000, L=3, r=20, dtype=F32, addend=True),
+    dict(M=41, K=1284, N=252, L=20, r=36, dtype=F32, none=0.3),
+    dict(M=10, K=132, N=16384, L=2, r=64, dtype=F32, addend=True),
+    dict(M=64, K=4096, N=512, L=64, r=16, dtype=F32, scale=False),
 ]
 
 MANY = [
@@ -121,6 +129,9 @@ MANY = [
     dict(M=3000, K=256, N=4096, L=3, r=32, none=1.0),         # no row has an adapter
     dict(M=65, K=100, N=132, L=7, r=12, dtype=F32, addend=True),
     dict(M=130, K=1028, N=260, L=3, r=128, dtype=F32, rows=20, none=0.3),
+    dict(M=70, K=4, N=4, L=2, r=4, dtype=F32),
+    dict(M=300, K=4100, N=68, L=5, r=4, dtype=F32, addend=True),     # K over eight blocks
+    dict(M=257, K=260, N=1028, L=9, r=64, dtype=F32, none=0.1),
 ]
 
 

@@ -1,5 +1,5 @@
 // fp32 form of the shared projection with per-row adapters for more than 64 rows (see lora.cu),
-// on the CUDA cores: S = scale (X A), then 64 x 64 tiles of X W whose epilogue adds S B and the
+// on the CUDA cores: S = scale (X A), then 128 x 64 tiles of X W whose epilogue adds S B and the
 // addend. Bound by the FMA and shared-memory pipes for many tiles; few tiles cut K over the blocks
 // of a cluster, whose sums meet in distributed shared memory (128 rows, 4096 x 512: 58 us, without
 // the cut and the prefetch 241). Sums are kept in runs of 64 terms that are added up afterwards, so
@@ -15,7 +15,7 @@ namespace moe {
 namespace {
 
 constexpr int kShrinkThreads = 512;
-constexpr int kTile = 64, kDepth = 16, kRun = 64, kThreads = 256;
+constexpr int kRows = 128, kTile = 64, kDepth = 16, kRun = 64, kThreads = 256;
 constexpr int kMaxSplits = 8;
 
 // One block per row: 4 ranks per thread, the rest of the threads over k.
@@ -74,6 +74,21 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
 }
 
+// Two fp32 values in one register pair, for the two-wide fused multiply-add.
+__device__ __forceinline__ uint64_t both(float v) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(v));
+  return d;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ void fma_pair(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+
 // Tile (blockIdx.y, blockIdx.x), share blockIdx.z of K; the shares of a tile are one cluster.
 __global__ void __launch_bounds__(kThreads)
     project_f32_kernel(const float* __restrict__ X, const float* __restrict__ W,
@@ -81,76 +96,90 @@ __global__ void __launch_bounds__(kThreads)
                        const float* __restrict__ S, const float* addend, float* Y, int64_t M,
                        int K, int N, int L, int rank) {
   struct Stage {
-    float x[kDepth][kTile + 4];
+    float x[kDepth][kRows + 4];
     float w[kDepth][kTile];
   };
-  __shared__ __align__(16) Stage stages[2];
-  static_assert(sizeof(stages) >= sizeof(float) * kTile * kTile, "the sums take their place");
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile;
+  __shared__ __align__(16) union {
+    Stage stages[2];
+    float sums[kRows * kTile];
+  } sh;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kRows;
   const int n0 = static_cast<int>(blockIdx.x) * kTile;
   const int tid = static_cast<int>(threadIdx.x), tr = tid / 16, tc = tid % 16;
   const int splits = static_cast<int>(gridDim.z), split = static_cast<int>(blockIdx.z);
   const int chunk = (K + splits * kRun - 1) / (splits * kRun) * kRun;
   const int k_begin = min(K, split * chunk), k_end = min(K, k_begin + chunk);
 
-  // 64 rows x 16 k of X, 16 k x 64 columns of W: a float4 of each per thread.
+  // 128 rows x 16 k of X, 16 k x 64 columns of W: two float4 and one per thread.
   const int lr = tid / 4, lk = tid % 4 * 4;
-  float4 x, w;
+  float4 x[2], w;
   auto load = [&](int k0) {
-    x = w = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m0 + lr < M && k0 + lk < k_end)
-      x = *reinterpret_cast<const float4*>(X + (m0 + lr) * K + k0 + lk);
+    x[0] = x[1] = w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (m0 + h * 64 + lr < M && k0 + lk < k_end)
+        x[h] = *reinterpret_cast<const float4*>(X + (m0 + h * 64 + lr) * K + k0 + lk);
     if (k0 + tr < k_end && n0 + tc * 4 < N)
       w = __ldg(reinterpret_cast<const float4*>(W + static_cast<int64_t>(k0 + tr) * N + n0 +
                                                 tc * 4));
   };
   auto put = [&](Stage& st) {
-    st.x[lk][lr] = x.x;
-    st.x[lk + 1][lr] = x.y;
-    st.x[lk + 2][lr] = x.z;
-    st.x[lk + 3][lr] = x.w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      st.x[lk][h * 64 + lr] = x[h].x;
+      st.x[lk + 1][h * 64 + lr] = x[h].y;
+      st.x[lk + 2][h * 64 + lr] = x[h].z;
+      st.x[lk + 3][h * 64 + lr] = x[h].w;
+    }
     *reinterpret_cast<float4*>(&st.w[tr][tc * 4]) = w;
   };
-  float acc[4][4] = {}, run[4][4] = {};
+  // Eight rows by four columns per thread, two columns per instruction.
+  float acc[8][4] = {};
+  uint64_t run[8][2] = {};
   load(k_begin);
-  put(stages[0]);
+  put(sh.stages[0]);
   __syncthreads();
   int cur = 0;
   for (int k0 = k_begin; k0 < k_end; k0 += kDepth, cur ^= 1) {
     const bool more = k0 + kDepth < k_end;
     if (more) load(k0 + kDepth);  // under way during this stage's products
-    const Stage& st = stages[cur];
+    const Stage& st = sh.stages[cur];
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
-      const float4 xv = *reinterpret_cast<const float4*>(&st.x[k][tr * 4]);
-      const float4 wv = *reinterpret_cast<const float4*>(&st.w[k][tc * 4]);
-      const float xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
+      const float4 x0 = *reinterpret_cast<const float4*>(&st.x[k][tr * 8]);
+      const float4 x1 = *reinterpret_cast<const float4*>(&st.x[k][tr * 8 + 4]);
+      const ulonglong2 wv = *reinterpret_cast<const ulonglong2*>(&st.w[k][tc * 4]);
+      const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) run[i][j] = fmaf(xs[i], ws[j], run[i][j]);
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t xx = both(xs[i]);
+        fma_pair(run[i][0], xx, wv.x);
+        fma_pair(run[i][1], xx, wv.y);
+      }
     }
     if (((k0 - k_begin) / kDepth) % (kRun / kDepth) == kRun / kDepth - 1 || !more) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[i][j] += run[i][j];
-          run[i][j] = 0.f;
+        for (int j = 0; j < 2; ++j) {
+          const float2 v = halves(run[i][j]);
+          acc[i][2 * j] += v.x;
+          acc[i][2 * j + 1] += v.y;
+          run[i][j] = 0u;
         }
     }
-    if (more) put(stages[cur ^ 1]);  // last read before the barrier of the step before
+    if (more) put(sh.stages[cur ^ 1]);  // last read before the barrier of the step before
     __syncthreads();
   }
 
   // The block's sums in place of the stages; each block then finishes its share of the rows.
-  float* sums = reinterpret_cast<float*>(stages);
+  float* sums = sh.sums;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<float4*>(sums + (tr * 4 + i) * kTile + tc * 4) =
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float4*>(sums + (tr * 8 + i) * kTile + tc * 4) =
         make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
   cluster_sync_all();
-  const int rows = kTile / splits;
+  const int rows = kRows / splits;
   for (int item = tid; item < rows * (kTile / 4); item += kThreads) {
     const int r0 = split * rows + item / (kTile / 4), c4 = item % (kTile / 4) * 4;
     const int64_t m = m0 + r0;
@@ -214,17 +243,17 @@ cudaError_t launch_lora_f32(const moe_lora_problem& p, const LoraTensors& t, voi
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Rows in grid.y: at most 65535 tiles a launch.
-  const int64_t rows_per_launch = int64_t(65535) * kTile;
+  const int64_t rows_per_launch = int64_t(65535) * kRows;
   for (int64_t m = 0; m < p.M; m += rows_per_launch) {
     const int64_t rows = std::min(rows_per_launch, p.M - m);
-    const int64_t tiles = (p.N + kTile - 1) / kTile * ((rows + kTile - 1) / kTile);
+    const int64_t tiles = (p.N + kTile - 1) / kTile * ((rows + kRows - 1) / kRows);
     // K over a cluster's blocks until the device has four blocks per SM, 128 k each at least.
     int splits = 1;
     while (splits < kMaxSplits && tiles * splits * 2 <= 4 * num_sms() && p.K >= 256 * splits)
       splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((p.N + kTile - 1) / kTile),
-                       static_cast<unsigned>((rows + kTile - 1) / kTile),
+                       static_cast<unsigned>((rows + kRows - 1) / kRows),
                        static_cast<unsigned>(splits));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
