@@ -39,6 +39,8 @@ constexpr int kMaxRecords = kMaxRows * 8;
 constexpr int kMaxE = 64;
 // Products: an expert's kept rows in pieces of at most Shape::kPieceRows (16 or 32).
 constexpr int kMaxParts = kMaxE + kMaxRecords / 16;
+constexpr int kMaxWarps = 16;
+constexpr int kCounters = kMaxGrid * (kMaxWarps + 1);
 constexpr int kMaxSlices = 64;  // pieces of D of the router's partial logits
 
 struct FewArgs {
@@ -59,7 +61,8 @@ struct FewArgs {
   float* colsum;
   float* part_logits;  // [slices][N][E]
   float* part;         // [grid][2][part_floats]: sums of shared tiles
-  int* counters;       // [2][kMaxGrid]: arrivals at shared up and down tiles
+  int* counters;       // [kMaxGrid][kMaxWarps]: the warps' arrivals at shared up tiles, then
+                       // [kMaxGrid]: the blocks' at shared down tiles
   void* H;             // see h_groups
   int* bar;            // [2] workspace header ints, zero at rest
   int* err;
@@ -463,6 +466,172 @@ __device__ __forceinline__ void finish_h(const FewArgs& a, const Tables& tb, con
   store_h<WK>(a, pt, r, f, v0, v1);
 }
 
+// 16- and 8-bit weights: a warp owns 16 columns of the tile, both matrices and all of k, so its
+// sums are final in its registers: it makes H, or writes its share, without the other warps, and
+// goes on with the next tile while they still multiply. (With the matrices and k cut over the
+// warps, whose sums met in shared memory eight rows at a time, the 8-bit Mixtral-shaped layer took
+// 231 us for 8 tokens and 332 for 32, against 224 and 315; bf16 the same.)
+//   v[matrix][j][c]: row 8 j + 2 t + (c & 1), lane = 4 g + t; column g + 8 (c >> 1) of the 16
+//   (bf16) or 2 g + (c >> 1) (8-bit).
+template <int NT>
+struct UpSums {
+  float v[2][NT][4];
+};
+
+// acc += a stage (64 k) of both matrices.
+template <int WK, int NT>
+__device__ __forceinline__ void up_stage(UpSums<NT>& acc, Consumer<WK>& c, int k0, int D) {
+  const uint32_t stage =
+      smem_u32(c.ring.weights) + static_cast<uint32_t>(c.cur.stage) * kStageBytes;
+  constexpr int kSideWarps = Team<WK>::kWarps / 2;
+  const uint32_t side = static_cast<uint32_t>(c.warp / kSideWarps);
+  const int at = c.warp % kSideWarps;  // which 16 columns of the box
+  Frag<NT, false> f[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    f[q].load_rows(c.rows(), kRowPitch, q, k0 + q * 32, D, c.lane);
+  constexpr int kLoads = WK == kBF16 ? 4 : 2;  // of a matrix: 16 or 32 k each
+  uint32_t w[2][kLoads][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t r = static_cast<uint32_t>(
+          WK == kBF16 ? 16 * i + (c.lane >> 4) * 8 + (c.lane & 7) : 32 * i + c.lane);
+      const uint32_t chunk =
+          static_cast<uint32_t>(WK == kBF16 ? at * 2 + ((c.lane >> 3) & 1) : at);
+      ldsm_x4_trans(stage + (static_cast<uint32_t>(m) * 2 + side) * kBoxBytes + r * 128 +
+                        ((chunk ^ (r & 7u)) << 4),
+                    w[m][i]);
+    }
+  c.release();
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)  // 16 k each
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t x[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (WK == kBF16) {
+            x[2 * h] = w[m][2 * q + b][2 * h];
+            x[2 * h + 1] = w[m][2 * q + b][2 * h + 1];
+          } else {
+            i8x4_to_bf16(w[m][q][2 * b + h], x[2 * h], x[2 * h + 1]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          mma_bf16(acc.v[m][j], x, f[q].r[j][0][2 * b], f[q].r[j][0][2 * b + 1]);
+      }
+}
+
+// H of the warp's columns (from f0 on) of the piece's rows.
+template <int WK, int NT>
+__device__ __forceinline__ void finish_strip(const FewArgs& a, const Tables& tb, const Part& pt,
+                                             const UpSums<NT>& s, int f0, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if (8 * j >= pt.n) break;
+    if constexpr (WK == kW8) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        finish_h<WK>(a, tb, pt, 8 * j + 2 * t + r, f0 + 2 * g,
+                     make_float2(s.v[0][j][r], s.v[0][j][2 + r]),
+                     make_float2(s.v[1][j][r], s.v[1][j][2 + r]));
+    } else {
+      // Two columns of a row to one lane: of lanes g and g + 1 (g even) the first takes row 2 t, the
+      // second row 2 t + 1.
+      const bool odd = (g & 1) != 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 v[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float mine = odd ? s.v[m][j][2 * h + 1] : s.v[m][j][2 * h];
+          const float other = __shfl_xor_sync(
+              0xFFFFFFFFu, odd ? s.v[m][j][2 * h] : s.v[m][j][2 * h + 1], 4);
+          v[m] = odd ? make_float2(other, mine) : make_float2(mine, other);
+        }
+        finish_h<WK>(a, tb, pt, 8 * j + 2 * t + (odd ? 1 : 0), f0 + 8 * h + (g & ~1), v[0], v[1]);
+      }
+    }
+  }
+}
+
+template <int WK, int NT>
+__device__ __forceinline__ void up_strip(const FewArgs& a, Tables& tb, Consumer<WK>& c,
+                                         const SplitK& sp, long long tile, int steps, int k0,
+                                         int k1, const Part pt, int fb) {
+  constexpr int kConsumers = Team<WK>::kConsumers;
+  UpSums<NT> acc;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc.v[m][j][q] = 0.0f;
+  for (int s = k0; s < k1; ++s) {
+    c.wait_full();
+    up_stage<WK, NT>(acc, c, s * kBoxRows, a.D);
+  }
+  const int f0 = fb * Shape<WK>::kCols + c.warp * 16;
+  if (k0 > 0 || k1 < steps) {
+    const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
+    auto share = [&](int b, bool head) {
+      return reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(b) * 2 + (head ? 1 : 0)) *
+                                                    a.part_floats) + c.tid;
+    };
+    float4* mine = share(static_cast<int>(blockIdx.x), k0 == 0);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        mine[(2 * j + m) * kConsumers] =
+            make_float4(acc.v[m][j][0], acc.v[m][j][1], acc.v[m][j][2], acc.v[m][j][3]);
+    __syncwarp();  // the warp's writes, then its arrival
+    int old = 0;
+    if (c.lane == 0) old = count_global(a.counters + first * kMaxWarps + c.warp);
+    old = __shfl_sync(0xFFFFFFFFu, old, 0);
+    if (old != last - first) return;
+    // The last to arrive adds the shares up in block order, two blocks' loads at a time.
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float4 sum[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+      for (int b0 = first; b0 <= last; b0 += 2) {
+        float4 w[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            w[u][m] = b0 + u <= last
+                          ? __ldcg(share(b0 + u, b0 + u == first) + (2 * j + m) * kConsumers)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            sum[m].x += w[u][m].x;
+            sum[m].y += w[u][m].y;
+            sum[m].z += w[u][m].z;
+            sum[m].w += w[u][m].w;
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        acc.v[m][j][0] = sum[m].x;
+        acc.v[m][j][1] = sum[m].y;
+        acc.v[m][j][2] = sum[m].z;
+        acc.v[m][j][3] = sum[m].w;
+      }
+    }
+  }
+  finish_strip<WK, NT>(a, tb, pt, acc, f0, c.lane);
+}
+
+// fp32 weights: the warps' sums meet in shared memory.
 template <int WK, int NT>
 __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer<WK>& c,
                                         const SplitK& sp, long long tile, int steps, int k0,
@@ -476,18 +645,9 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer<W
   for (int s = k0; s < k1; ++s) {
     c.wait_full();
     const int d0 = s * kBoxRows + first_row;
-    if constexpr (WK == kF32) {
-      multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, smem_u32(c.rows()) + first_row * 4,
-                       kRowPitchF32, pt.n, d0, a.D);
-      c.release();
-    } else {
-      Weights<WK> w;
-      Frag<NT, false> f;
-      w.load(c.my_box(), c.warp, c.lane);
-      f.load_rows(c.rows(), kRowPitch, first_row / 32, d0, a.D, c.lane);
-      c.release();
-      multiply<WK, NT, false>(acc, w, f);
-    }
+    multiply_f32<NT>(acc, c.my_box(), c.warp, c.lane, smem_u32(c.rows()) + first_row * 4,
+                     kRowPitchF32, pt.n, d0, a.D);
+    c.release();
   }
 
   // Both branches' sums over the block's stages; the whole tile's, or a share of it.
@@ -512,7 +672,9 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer<W
   }
   if (whole) return;
   const int first = sp.owner(tile * steps), last = sp.owner(tile * steps + steps - 1);
-  if (!last_to_finish<kConsumers>(a.counters + first, last - first + 1, c.tid, &tb.flag)) return;
+  if (!last_to_finish<kConsumers>(a.counters + first * kMaxWarps, last - first + 1, c.tid,
+                                  &tb.flag))
+    return;
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
     float2 h[2][P::kMine];
 #pragma unroll
@@ -598,10 +760,10 @@ __device__ __forceinline__ void store_out(const FewArgs& a, int t, int d, float2
 // CALL(row tiles) for n rows, where a piece has at most MAXNT row tiles.
 #define MOE_FEW_ROWS(n, CALL)                             \
   do {                                                    \
-    if (MAXNT == 1 || (n) <= 8) CALL(1);                  \
-    else if (MAXNT == 2 || (n) <= 16) CALL(MAXNT < 2 ? 1 : 2);  \
-    else if ((n) <= 24) CALL(MAXNT < 4 ? 1 : 3);          \
-    else CALL(MAXNT < 4 ? 1 : 4);                         \
+    if (MAXNT == 1 || (n) <= 8) { CALL(1); }              \
+    else if (MAXNT == 2 || (n) <= 16) { CALL((MAXNT < 2 ? 1 : 2)); }  \
+    else if ((n) <= 24) { CALL((MAXNT < 4 ? 1 : 3)); }    \
+    else { CALL((MAXNT < 4 ? 1 : 4)); }                   \
   } while (0)
 
 // ------------------------------------------------------------------ the kernel
@@ -637,8 +799,8 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
     }
     fence_barrier_init();
     // Arrivals at this block's shared tiles; seen by the others after the first grid barrier.
-    a.counters[blockIdx.x] = 0;
-    a.counters[kMaxGrid + blockIdx.x] = 0;
+    for (int i = 0; i < kMaxWarps; ++i) a.counters[blockIdx.x * kMaxWarps + i] = 0;
+    a.counters[kMaxGrid * kMaxWarps + blockIdx.x] = 0;
   }
   __syncthreads();
 
@@ -827,7 +989,11 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       const int k1 = static_cast<int>(min(static_cast<long long>(up_steps), k0 + (u1 - s)));
       const Part pt = tb.part[tile / up_cols];
       const int fb = static_cast<int>(tile % up_cols);
-#define MOE_UP(NT) up_tile<WK, NT>(a, tb, c, up, tile, up_steps, k0, k1, pt, fb)
+#define MOE_UP(NT)                                                        \
+  if constexpr (WK == kF32)                                               \
+    up_tile<WK, NT>(a, tb, c, up, tile, up_steps, k0, k1, pt, fb);        \
+  else                                                                    \
+    up_strip<WK, NT>(a, tb, c, up, tile, up_steps, k0, k1, pt, fb)
       MOE_FEW_ROWS(pt.n, MOE_UP);
 #undef MOE_UP
       s += k1 - k0;
@@ -865,7 +1031,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       if (!whole) {
         const int first = down.owner(tile * down_steps),
                   last = down.owner(tile * down_steps + down_steps - 1);
-        if (last_to_finish<kConsumers>(a.counters + kMaxGrid + first, last - first + 1, tid,
+        if (last_to_finish<kConsumers>(a.counters + kMaxGrid * kMaxWarps + first, last - first + 1, tid,
                                        &tb.flag)) {
           constexpr int kChunk = WK == kW8 ? 4 : 8;
           for (int i0 = tid; i0 < a.N * P::kPairs; i0 += kChunk * kConsumers) {
@@ -1002,7 +1168,7 @@ size_t few_workspace_bytes(const moe_problem& p) {
   const int64_t R = N * p.k;
   // bf16 problems may come with either weight kind: the larger of the two.
   const int kind = p.dtype == MOE_DTYPE_F32 ? kF32 : kW8;
-  return up256(sizeof(float) * kMaxSlices * N * p.E) + up256(sizeof(int) * 2 * kMaxGrid) +
+  return up256(sizeof(float) * kMaxSlices * N * p.E) + up256(sizeof(int) * kCounters) +
          up256(sizeof(float) * 2 * kMaxGrid * part_floats_of(kind, N)) +
          up256(kind == kF32 ? sizeof(float) * R * h_row_f32(p.F)
                             : static_cast<size_t>((std::min<int64_t>(p.E, R) + R / 8) *
@@ -1032,7 +1198,7 @@ cudaError_t launch_few(const moe_problem& p, int64_t capacity, const FewTensors&
   a.part_logits = reinterpret_cast<float*>(w);
   w += up256(sizeof(float) * kMaxSlices * p.N * p.E);
   a.counters = reinterpret_cast<int*>(w);
-  w += up256(sizeof(int) * 2 * kMaxGrid);
+  w += up256(sizeof(int) * kCounters);
   a.part = reinterpret_cast<float*>(w);
   a.part_floats = part_floats_of(p.dtype == MOE_DTYPE_F32 ? kF32 : kW8, p.N);
   w += up256(sizeof(float) * 2 * kMaxGrid * a.part_floats);
