@@ -212,6 +212,23 @@ def test_graph_replay_and_other_stream(abi):
     assert abi.device_error(ws) == 0
 
 
+def _guarded(nbytes, n=4096):
+    """A workspace of nbytes inside a larger buffer whose other bytes are known."""
+    buf = torch.full((nbytes + 2 * n,), 0x5A, dtype=torch.uint8, device="cuda")
+    buf[n:n + 256] = 0  # the header
+    return buf, buf[n:n + nbytes], lambda: bool((buf[:n] == 0x5A).all() and (buf[-n:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("name", ["one_by_one", "drops_token_major", "one_expert_64_rows",
+                                  "two_experts_all_rows", "most_records", "f32_tiny", "f32_drops"])
+def test_writes_stay_in_the_workspace(abi, name):
+    cfg = next(c for c in CASES if c.name == name)
+    inp = inputs.make_inputs(cfg, "cuda")
+    buf, ws, intact = _guarded(abi.workspace_size(abi.problem(cfg)))
+    _run(abi, cfg, inp, ws=ws)
+    assert intact()
+
+
 def test_two_streams_at_once(abi):
     # Calls on two streams, one of high priority, with a workspace each and other kernels beside
     # them: every call's own result, no wait that runs out.

@@ -209,6 +209,22 @@ def test_graph_replay_and_other_stream(abi, M):
     assert abi.device_error(ws) == 0
 
 
+@pytest.mark.parametrize("kw", [FEW[0], FEW[1], FEW[7], FEW[9], FEW[14], FEW[17], FEW[20],
+                                MANY[1], MANY[4], MANY[12], MANY[16], MANY[18]],
+                         ids=lambda k: "-".join(str(v) for v in k.values()))
+def test_writes_stay_in_the_workspace(abi, kw):
+    import ctypes
+    c = Case(**kw)
+    p = abi.lora_problem(c.M, c.K, c.N, c.L, c.r, c.dtype)
+    size = ctypes.c_size_t()
+    assert abi.lib.moe_lora_workspace_size(ctypes.byref(p), ctypes.byref(size)) == 0
+    n, pad = size.value, 4096
+    buf = torch.full((n + 2 * pad,), 0x5A, dtype=torch.uint8, device="cuda")
+    buf[pad:pad + 256] = 0  # the header
+    c.check(c.run(abi, ws=buf[pad:pad + n]))
+    assert (buf[:pad] == 0x5A).all() and (buf[-pad:] == 0x5A).all()
+
+
 @pytest.mark.parametrize("M", [4, 200])
 def test_two_streams_at_once(abi, M):
     # Calls on two streams, one of high priority, with a workspace each: every call's own result.

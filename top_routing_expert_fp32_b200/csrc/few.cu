@@ -542,8 +542,8 @@ __device__ __forceinline__ void finish_strip(const FewArgs& a, const Tables& tb,
                      make_float2(s.v[0][j][r], s.v[0][j][2 + r]),
                      make_float2(s.v[1][j][r], s.v[1][j][2 + r]));
     } else {
-      // Two columns of a row to one lane: of lanes g and g + 1 (g even) the first takes row 2 t, the
-      // second row 2 t + 1.
+      // Two columns of a row to one lane: of lanes g and g + 1 (g even) the first takes row 2 t,
+      // the second row 2 t + 1.
       const bool odd = (g & 1) != 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1031,8 +1031,8 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       if (!whole) {
         const int first = down.owner(tile * down_steps),
                   last = down.owner(tile * down_steps + down_steps - 1);
-        if (last_to_finish<kConsumers>(a.counters + kMaxGrid * kMaxWarps + first, last - first + 1, tid,
-                                       &tb.flag)) {
+        if (last_to_finish<kConsumers>(a.counters + kMaxGrid * kMaxWarps + first, last - first + 1,
+                                       tid, &tb.flag)) {
           constexpr int kChunk = WK == kW8 ? 4 : 8;
           for (int i0 = tid; i0 < a.N * P::kPairs; i0 += kChunk * kConsumers) {
             float2 v[kChunk];

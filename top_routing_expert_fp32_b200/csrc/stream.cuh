@@ -47,9 +47,9 @@ constexpr int kBarConsumers = 1, kBarAll = 2, kBarRows = 3, kBarSide = 4;  // na
 
 // A stage is four boxes: two side by side (kCols output columns) times either two matrices with
 // the same 64 k-rows, or 128 k-rows of one matrix. Where the reduction is cut over the warps, a
-// box's warps each take 32 of its k-rows and a segment of kSeg columns: two warps for 16- and 32-bit weights, four for 8-bit ones, whose
-// conversion to bf16 is what their warps spend their time on (Mixtral-shaped layer, 8 tokens:
-// 300 us with 8 warps, 245 with 16).
+// box's warps each take 32 of its k-rows and a segment of kSeg columns: two warps for 16- and 32-bit
+// weights, four for 8-bit ones, whose conversion to bf16 is what their warps spend their time on
+// (Mixtral-shaped layer, 8 tokens: 300 us with 8 warps, 245 with 16).
 // kPieceRows: activation rows of one product (tiles of 8); an expert with more rows is streamed
 // again for the next piece. It is what the registers hold without spilling: a spill costs an L2
 // access here, since the ring leaves the L1 cache almost nothing (8-bit weights, 32 tokens:
