@@ -390,12 +390,12 @@ moe_status moe_lora_workspace_size(const moe_lora_problem* p, size_t* bytes);
  * [-1, L) is recorded as MOE_DEVERR_BAD_INDEX and treated as -1. scale may be NULL (1 for
  * every adapter). addend may be NULL; it may be Y itself (Y += ...), otherwise Y must not
  * overlap any input. Rows may come in any order; adjacent rows of one adapter share its reads.
+ *   X A and all sums are fp32; for bf16 scale (X A) enters the product with B (which must be
+ *   finite) as two bf16 terms (16 bits of mantissa); the result is rounded once.
  *   At most 64 rows: one cooperative kernel that streams W once (one block per SM, as
- *   moe_forward_few); X A and all sums in fp32, for bf16 scale (X A) as two bf16 terms (16 bits
- *   of mantissa) in the product with B (which must be finite), one rounding to the output type.
- *   More rows, bf16: X A in fp32, rounded to bf16 with its scale, and one tcgen05 product over
- *   [X, X A] with fp32 accumulation. Its cost grows with the number of different adapters
- *   among each 256 adjacent rows. More rows, fp32: CUDA cores.
+ *   moe_forward_few). More rows, bf16: X A, and one tcgen05 product over [X, X A] with fp32
+ *   accumulation. Its cost grows with the number of different adapters among each 256 adjacent
+ *   rows. More rows, fp32: CUDA cores.
  * Deterministic. Pointers: device memory, 16-byte aligned (adapter, scale: 4-byte). */
 moe_status moe_lora_forward(const moe_lora_problem* p, const void* X, const void* W,
                             const void* A, const void* B, const int32_t* adapter,

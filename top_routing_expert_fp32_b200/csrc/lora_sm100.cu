@@ -9,9 +9,10 @@
 //   1. shrink_kernel: S = X A. A group of 8 or 32 rows per cluster of blocks, K cut over the
 //      blocks and their warps; each warp streams (adapter of the group, piece of K) steps
 //      through its own TMA ring into mma.m16n8k16 (ranks x rows), the fp32 sums meet through
-//      distributed shared memory. S is rounded to bf16 once, with its scale: it is a
-//      tensor-core operand, and its rounding (2^-8 of the adapter's part) is no larger than the
-//      output's own.
+//      distributed shared memory. S, scaled, becomes two bf16 terms (16 bits of mantissa), both
+//      operands of the product with B, as for few rows: a row's result has the same accuracy
+//      whatever the batch. (In one term the error against 64 bits was 1.3 times the output
+//      rounding's own where the adapter's part is as large as the rest.)
 //   2. lora_gemm: the product, launched as a programmatic dependent of 1: it waits for S only when
 //      its first tile comes to the extra k-steps, so the shrink hides behind the main loop.
 #include <algorithm>
@@ -27,11 +28,17 @@ namespace {
 
 constexpr int kUnit = 16;          // k of one MMA
 constexpr int kStageUnits = 4;     // MMAs per 64-wide k-block
-// MMAs of an adapter: its rank in units of 16; above 64, whole k-blocks (a k-block then holds
-// one 64-column piece of S).
-__host__ __device__ constexpr int units_of_rank(int rank) {
+// Pieces of B of an adapter, 16 ranks each, and how many a k-block takes. A k-block's A tile holds
+// both terms of S for its pieces, so B is loaded once for the two: up to rank 32 all of a row's S
+// (a k-block then takes the pieces of several adapters), above that 32 ranks (two pieces).
+__host__ __device__ constexpr int pieces_of_rank(int rank) {
   const int u = (rank + kUnit - 1) / kUnit;
-  return u <= kStageUnits ? u : (u + kStageUnits - 1) / kStageUnits * kStageUnits;
+  return u <= 2 ? u : (u + 1) / 2 * 2;
+}
+__host__ __device__ constexpr int block_pieces(int rank) { return rank <= 32 ? kStageUnits : 2; }
+// Ranks of a group: 64 columns of a row of S hold a group's first terms, then its second ones.
+__host__ __device__ constexpr int group_ranks(int rank) {
+  return rank <= 32 ? pieces_of_rank(rank) * kUnit : 32;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -52,6 +59,7 @@ struct ShrinkArgs {
   int64_t M;
   int K, L, rank;
   int ld;             // columns of S, a multiple of 64
+  int group;          // ranks of every 64 of them
   int tile_rows;      // 128 or 256
   int cluster;        // blocks per row group
   uint64_t timeout_ns;
@@ -284,8 +292,8 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
     const int ad = s_tile[row0 - tile0 + l];
     const float sc = ad >= 0 && a.scale != nullptr ? a.scale[ad] : 1.0f;
     uint32_t* out = reinterpret_cast<uint32_t*>(a.S + (row0 + l) * a.ld);
-    for (int c = lane; c < a.ld / 2; c += 32) {
-      uint32_t v = 0u;
+    for (int c = lane; c < a.ld / 64 * a.group / 2; c += 32) {
+      uint32_t hi = 0u, lo = 0u;
       if (2 * c < a.rank && ad >= 0) {
         // All blocks' values are on their way before the first is added.
         const uint32_t here =
@@ -314,9 +322,17 @@ shrink_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
             }
           }
         }
-        v = pack_bf16x2(s0 * sc, s1 * sc);
+        s0 *= sc;
+        s1 *= sc;
+        hi = pack_bf16x2(s0, s1);
+        // A value that is infinite, or becomes so in bf16, has no remainder.
+        const float r0 = s0 - bf16_bits_to_float(hi & 0xFFFFu);
+        const float r1 = s1 - bf16_bits_to_float(hi >> 16);
+        lo = pack_bf16x2(fabsf(r0) < INFINITY ? r0 : 0.0f, fabsf(r1) < INFINITY ? r1 : 0.0f);
       }
-      out[c] = v;
+      const int at = 2 * c / a.group * 32 + c % (a.group / 2);
+      out[at] = hi;
+      out[at + a.group / 2] = lo;
     }
   }
   cluster_sync_all();  // no block leaves while another reads its sums
@@ -394,7 +410,10 @@ struct GemmArgs {
   int* err;
   uint64_t timeout_ns;
   int64_t M;
-  int K, N, units;
+  int K, N;
+  int units;        // pieces of B of an adapter
+  int per_block;    // pieces of a k-block
+  int second_step;  // bytes from a piece's first terms to its second ones in a row of the A tile
 };
 
 template <bool PAIR, int NB>
@@ -496,7 +515,7 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
             if (!s_ready) pdl_wait();
             s_ready = true;
             slots = p.n_slots[m_tile];
-            kbs = num_kb + (slots * p.units + kStageUnits - 1) / kStageUnits;
+            kbs = num_kb + (slots * p.units + p.per_block - 1) / p.per_block;
             if (slots > 0) {  // their adapters, in whole 16-byte pieces
               const uint32_t n = static_cast<uint32_t>(slots + 3) / 4 * 16;
               mbar_arrive_expect_tx(ids_full, n);
@@ -531,10 +550,10 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
                                  plain);
             }
           } else {
-            // k-block of up to four (slot, 16 ranks) units u = slot * units + v: S's columns for
-            // all of them, B's rows and the slots' lane masks.
-            const int u0 = (kb - num_kb) * kStageUnits;
-            const int n = min(kStageUnits, slots * p.units - u0);
+            // k-block of up to four units u = slot * units + v (a piece of 16 ranks of the slot's
+            // adapter): S's columns for all of them, B's rows and the slots' lane masks.
+            const int u0 = (kb - num_kb) * p.per_block;
+            const int n = min(p.per_block, slots * p.units - u0);
             const int slot0 = u0 / p.units, slot1 = (u0 + n - 1) / p.units;
             const int64_t list = m_tile * S::kTileRows;
             const uint32_t mask_bytes = (slot1 - slot0 + 1) * S::kMaskWords * 4;
@@ -544,7 +563,7 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
               bulk_g2s(sM + c.stage * S::kMaskBytes, p.masks + (list + slot0) * S::kMaskWords,
                        mask_bytes, &full[c.stage]);
             }
-            const int s_col = p.units > kStageUnits ? (u0 % p.units) * kUnit : 0;
+            const int s_col = p.units > 2 ? (u0 % p.units) / 2 * 64 : 0;
             if (PAIR) tma_load_2d_pair_hint(a_dst, &ms, bar, s_col, row0, keep);
             else tma_load_2d_hint(a_dst, &ms, &full[c.stage], s_col, row0, keep);
             if (kb == num_kb) {
@@ -601,7 +620,7 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
             if (!s_ready) pdl_wait();
             s_ready = true;
             units = p.n_slots[m_tile] * p.units;
-            kbs = num_kb + (units + kStageUnits - 1) / kStageUnits;
+            kbs = num_kb + (units + p.per_block - 1) / p.per_block;
           }
           if (!mbar_wait(&full[stage], phase, p.timeout_ns)) {
             record_error(p.err, MOE_DEVERR_WAIT_TIMEOUT);
@@ -626,7 +645,7 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
               }
             }
           } else {
-            const int u0 = (kb - num_kb) * kStageUnits, n = min(kStageUnits, units - u0);
+            const int u0 = (kb - num_kb) * p.per_block, n = min(p.per_block, units - u0);
             const int slot0 = u0 / p.units;
             const uint32_t* masks = reinterpret_cast<const uint32_t*>(sM + stage * S::kMaskBytes);
             for (int j = 0; j < n; ++j) {
@@ -635,13 +654,18 @@ lora_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtens
 #pragma unroll
               for (int w = 0; w < S::kMaskWords; ++w)
                 off[w] = masks[(slot - slot0) * S::kMaskWords + w];
-              const uint64_t ad = smem_desc_sw128(a_addr + (v % kStageUnits) * 32, 16, 1024);
+              const uint32_t s_addr = a_addr + (v % p.per_block) * 32;
               for (int h = 0; h < mmas; ++h) {
                 const uint64_t bd =
                     smem_desc_sw128(b_addr + 2 * h * kBoxBytes + j * kUnitBytes, kBoxBytes, 1024);
                 const uint32_t dh = d + static_cast<uint32_t>(256 * h);
-                if (PAIR) umma_bf16_ss_pair_masked(dh, ad, bd, S::kIdesc, off);
-                else umma_bf16_ss_masked(dh, ad, bd, S::kIdesc, off);
+                auto term = [&](uint32_t at) {
+                  const uint64_t ad = smem_desc_sw128(at, 16, 1024);
+                  if (PAIR) umma_bf16_ss_pair_masked(dh, ad, bd, S::kIdesc, off);
+                  else umma_bf16_ss_masked(dh, ad, bd, S::kIdesc, off);
+                };
+                term(s_addr);
+                term(s_addr + p.second_step);
               }
             }
           }
@@ -775,7 +799,7 @@ int64_t tiles_of(const moe_lora_problem& p) {
   return (p.M + tile_rows_of(p) - 1) / tile_rows_of(p);
 }
 int s_cols_of(const moe_lora_problem& p) {
-  return (units_of_rank(p.rank) * kUnit + 63) / 64 * 64;
+  return (pieces_of_rank(p.rank) * kUnit + group_ranks(p.rank) - 1) / group_ranks(p.rank) * 64;
 }
 
 template <int RT, int NT>
@@ -874,6 +898,7 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
   a.masks = masks;
   a.err = err;
   a.ld = s_cols_of(p);
+  a.group = group_ranks(p.rank);
   a.M = p.M;
   a.K = static_cast<int>(p.K);
   a.L = p.adapters;
@@ -922,7 +947,9 @@ cudaError_t launch_lora_sm100(const moe_lora_problem& p, const LoraTensors& t, v
   g.M = p.M;
   g.K = static_cast<int>(p.K);
   g.N = static_cast<int>(p.N);
-  g.units = units_of_rank(p.rank);
+  g.units = pieces_of_rank(p.rank);
+  g.per_block = block_pieces(p.rank);
+  g.second_step = 2 * group_ranks(p.rank);
   if (pairs) return launch_gemm<true, 4>(p, mx, mw, ms, mb, g, stream);
   if (nb == 4) return launch_gemm<false, 4>(p, mx, mw, ms, mb, g, stream);
   if (nb == 2) return launch_gemm<false, 2>(p, mx, mw, ms, mb, g, stream);
