@@ -109,7 +109,8 @@ enum {
  *   drop_policy     MOE_DROP_ZERO: a dropped slot contributes nothing and the kept slots keep
  *                   their gates; MOE_DROP_RENORM_KEPT: when a token has dropped and kept
  *                   slots, the kept gates are divided by their sum (GShard case A, MoE series
- *                   2.2: (w1, w2) -> (1, 0) when the second expert overflows)
+ *                   2.2: (w1, w2) -> (1, 0) when the second expert overflows); kept gates that
+ *                   are all 0 in fp32 (logits more than 104 below the largest) share equally
  *   routing_mode    MOE_ROUTE_* (selection variant; needs a noise array unless TOPK)
  *   min_capacity    >= 0; the capacity is max(ceil(CF*N*k/E), min_capacity) (MoE series 2.1)
  * bf16 problems need D and F to be multiples of 8 (16-byte rows for the tensor-memory
@@ -247,7 +248,8 @@ moe_status moe_expert_down(const moe_problem* p, const void* H, const int32_t* o
 /* Gate-weighted combine (Grok-1 book 5.3.5; LLMs-from-scratch 12.2; MoE series 2.2):
  *   out[t] = sum_{j=0..k-1} [!dropped[t,j]] * g[t,j] * Y[offsets[topk_idx[t,j]] + pos[t,j]]
  * with g = topk_gate, except under MOE_DROP_RENORM_KEPT for a token with both dropped and kept
- * slots: g[t,j] = topk_gate[t,j] / (sum of its kept slots' gates, fp32, ascending j).
+ * slots: g[t,j] = topk_gate[t,j] / (sum of its kept slots' gates, fp32, ascending j), or, where
+ * that sum is 0, 1 / (number of its kept slots).
  * Accumulated in fp32 in ascending j, rounded once to the output dtype; a token whose slots
  * are all dropped gets 0. `dropped` may be NULL only without a capacity
  * (capacity_factor <= 0: nothing is dropped); with a capacity it is required

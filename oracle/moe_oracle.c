@@ -448,7 +448,8 @@ void oracle_expert_ffn_w8(int64_t n_rec, const int32_t* rec_token, const int32_t
  * Yrec holds one row per record in record order (t*k + j). */
 /* out[t] = sum over kept slots j of g'[t,j] * Y[t,j]. policy 0: g' = g. policy 1 ([GS] 2.2
  * case A): when a token has both dropped and kept slots, g'[t,j] = g[t,j] / (sum of the kept
- * slots' gates), so that the kept gates sum to 1 ((w1, w2) -> (1, 0) for top-2). */
+ * slots' gates), so that the kept gates sum to 1 ((w1, w2) -> (1, 0) for top-2); kept gates that
+ * are all 0 (underflow) share the weight equally. */
 void oracle_combine_policy(int64_t N, int32_t k, int64_t D, const double* gate,
                            const uint8_t* dropped, int32_t policy, const double* Yrec,
                            double* out) {
@@ -467,7 +468,7 @@ void oracle_combine_policy(int64_t N, int32_t k, int64_t D, const double* gate,
     for (int32_t j = 0; j < k; ++j) {
       const int64_t r = t * k + j;
       if (dropped && dropped[r]) continue;
-      const double g = reweight ? gate[r] / kept_sum : gate[r];
+      const double g = !reweight ? gate[r] : kept_sum == 0.0 ? 1.0 / kept : gate[r] / kept_sum;
       const double* y = Yrec + r * D;
       for (int64_t d = 0; d < D; ++d) o[d] += g * y[d];
     }

@@ -127,3 +127,15 @@ def test_case_a_bruteforce_forward(oracle_lib):
             g = o["gate"][t, j] / s if len(keep) < k else o["gate"][t, j]
             ref[t] += g * ((a * expit(a) * b) @ W3[e].astype(np.float64))
     np.testing.assert_allclose(o["out"], ref, rtol=1e-12, atol=1e-12)
+
+
+def test_case_a_reweight_of_zero_gates(oracle_lib):
+    # Kept gates that are all 0 share the weight equally instead of dividing 0 by 0; token 2 keeps
+    # everything, so nothing is reweighted.
+    gate = np.array([[1.0, 0.0, 0.0], [1.0, 0.0, 0.0], [1.0, 0.0, 0.0]])
+    dropped = np.array([[1, 0, 0], [1, 1, 0], [0, 0, 0]], dtype=np.uint8)
+    Y = np.arange(1.0, 19.0).reshape(3, 3, 2)
+    out = oracle_lib.combine(gate, dropped, Y, policy=oracle_lib.DROP_RENORM_KEPT)
+    np.testing.assert_array_equal(out[0], 0.5 * Y[0, 1] + 0.5 * Y[0, 2])
+    np.testing.assert_array_equal(out[1], Y[1, 2])
+    np.testing.assert_array_equal(out[2], Y[2, 0])

@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(kThreads)
     if (kept > 0 && kept < k) {
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
-        if (row[j] >= 0) g[j] = g[j] / kept_sum;
+        // (Gates that fp32 holds as 0, of logits more than 104 below the largest, are equal.)
+        if (row[j] >= 0)
+          g[j] = kept_sum == 0.f ? 1.f / static_cast<float>(kept) : g[j] / kept_sum;
     }
   }
   for (int64_t c0 = first; c0 < chunks_per_row; c0 += step * kBatch) {

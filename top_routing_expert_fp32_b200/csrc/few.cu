@@ -350,12 +350,15 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
       float g = tb.gate[r];
       if (a.renorm_kept) {
         float kept = 0.0f;
-        bool lost = false;
+        int slots = 0;
         for (int j = 0; j < a.k; ++j) {
-          if (tb.pos[t * a.k + j] < a.capacity) kept += tb.gate[t * a.k + j];
-          else lost = true;
+          if (tb.pos[t * a.k + j] < a.capacity) {
+            kept += tb.gate[t * a.k + j];
+            ++slots;
+          }
         }
-        if (lost) g = g / kept;
+        // (As the combine: kept gates that are all 0 share equally.)
+        if (slots < a.k) g = kept == 0.0f ? 1.0f / static_cast<float>(slots) : g / kept;
       }
       const int row = tb.off[tb.idx[r]] + p;
       tb.row_tok[row] = static_cast<int16_t>(t);
