@@ -594,11 +594,8 @@ __device__ __forceinline__ void up_strip(const FewArgs& a, Tables& tb, Consumer<
       for (int m = 0; m < 2; ++m)
         mine[(2 * j + m) * kConsumers] =
             make_float4(acc.v[m][j][0], acc.v[m][j][1], acc.v[m][j][2], acc.v[m][j][3]);
-    __syncwarp();  // the warp's writes, then its arrival
-    int old = 0;
-    if (c.lane == 0) old = count_global(a.counters + first * kMaxWarps + c.warp);
-    old = __shfl_sync(0xFFFFFFFFu, old, 0);
-    if (old != last - first) return;
+    if (!last_warp_to_arrive(a.counters + first * kMaxWarps + c.warp, last - first + 1, c.lane))
+      return;
     // The last to arrive adds the shares up in block order, two blocks' loads at a time.
 #pragma unroll
     for (int j = 0; j < NT; ++j) {

@@ -68,7 +68,6 @@ struct LoraTables {
   int adapter[kMaxRows];         // of each row; -1: none
   float scale[kMaxRows];         // and its scale
   uint32_t firsts[2];
-  int flag;
 };
 
 constexpr int kPieceRanks = 16;
@@ -401,11 +400,8 @@ __device__ __forceinline__ void finish_f32(const LoraArgs& a, const RowsF32<NT>&
     float* out = share(static_cast<int>(blockIdx.x), is_first);
 #pragma unroll
     for (int q = 0; q < R::kMine; ++q) out[q * 32] = v[q];
-    __syncwarp();  // the warp's writes, then its arrival
-    int old = 0;
-    if (lane == 0) old = count_global(a.counters + first * LoraTeam::kWarps + warp);
-    old = __shfl_sync(0xFFFFFFFFu, old, 0);
-    if (old != last - first) return;
+    if (!last_warp_to_arrive(a.counters + first * LoraTeam::kWarps + warp, last - first + 1, lane))
+      return;
     // (The sums of four blocks are on their way at once.)
 #pragma unroll
     for (int q = 0; q < R::kMine; ++q) v[q] = 0.0f;
@@ -665,11 +661,9 @@ __device__ __forceinline__ void strip_share(const LoraArgs& a, Strip<NT>& acc,
       if (8 * j < a.M)
         mine[(j * H + h) * kPerRow] = make_float4(acc.v[h][j][0], acc.v[h][j][1], acc.v[h][j][2],
                                                   acc.v[h][j][3]);
-  __syncwarp();  // the warp's writes, then its arrival
-  int old = 0;
-  if (lane == 0) old = count_global(a.counters + first * LoraTeam::kWarps + at.owner);
-  old = __shfl_sync(0xFFFFFFFFu, old, 0);
-  if (old != last - first) return;
+  if (!last_warp_to_arrive(a.counters + first * LoraTeam::kWarps + at.owner, last - first + 1,
+                           lane))
+    return;
   constexpr int kAtOnce = NT <= 2 ? 4 : 2;  // blocks whose shares are on their way at once
 #pragma unroll
   for (int h = 0; h < H; ++h) {

@@ -465,6 +465,18 @@ __device__ __forceinline__ int count_global(int* counter) {
   return old;
 }
 
+// A warp's arrival at a counter that `parts` warps share; true in the one that arrives last, whose
+// lanes then see what all lanes of the others wrote before they arrived. The warp barriers make
+// lane 0's release and acquire the whole warp's: a shuffle orders no memory.
+__device__ __forceinline__ bool last_warp_to_arrive(int* counter, int parts, int lane) {
+  __syncwarp();
+  int old = 0;
+  if (lane == 0) old = count_global(counter);
+  old = __shfl_sync(0xFFFFFFFFu, old, 0);
+  __syncwarp();
+  return old == parts - 1;
+}
+
 // One thread: wait until `target` blocks have arrived at *bar (bounded).
 __device__ __forceinline__ bool spin_until(int* bar, int target, uint64_t timeout_ns, int* err) {
   const uint64_t t0 = globaltimer_ns();
@@ -606,6 +618,7 @@ __device__ __forceinline__ void fence_proxy_async_all() {
 }
 
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
+  __syncwarp();
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
