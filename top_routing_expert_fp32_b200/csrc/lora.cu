@@ -136,19 +136,24 @@ __device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid, int item) {
   const int chunk = (a.K + a.slices - 1) / a.slices;
   const int k0 = min(a.K, slice * chunk), k1 = min(a.K, k0 + chunk);
   const int v = sid % per_row, sub = sid / per_row;
-  float acc[kVec];
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
   if (sub < subs) {
     const int64_t x0 = static_cast<int64_t>(m) * a.K;
     const int64_t a0 = static_cast<int64_t>(ad) * a.K * a.rank + v * kVec;
-    // Four k at a time, all their loads on their way before the first product: beside the stream a
-    // load takes about 2 us (a row of 4096: the partial sums were out after 9.8 us one by one, 4.6
-    // so), and the side warps' registers hold four.
+    // Runs of 64 terms, added up in shared memory: the rounding error of one chain grows with its
+    // length, 1024 terms for 64 rows of 4096 at rank 128.
+    constexpr int kRun = 64;
+    float* sums = tb.scratch + sub * a.rank + v * kVec;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) sums[i] = 0.0f;
+    // Four k at a time, all their loads on their way before the first product of the four before:
+    // beside the stream a load takes about 2 us (a row of 4096: the partial sums were out after 9.8
+    // us one by one, 4.6 us by fours). Each row reads its own adapter, also where rows share one:
+    // 64 rows of 4096 x 4096, 64 adapters of rank 128, take 132 us, most of it here.
     constexpr int kAtOnce = 4;
-    for (int k = k0 + sub; k < k1; k += kAtOnce * subs) {
-      float x[kAtOnce];
-      uint4 w[kAtOnce];
+    static_assert(kRun % kAtOnce == 0, "whole runs");
+    float x[kAtOnce];
+    uint4 w[kAtOnce];
+    auto load = [&](int k) {
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
         const int at = k + u * subs;
@@ -160,17 +165,34 @@ __device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid, int item) {
               (a0 + static_cast<int64_t>(at) * a.rank) * (F32 ? 4 : 2)));
         }
       }
+    };
+    load(k0 + sub);
+    for (int run = k0 + sub; run < k1; run += kRun * subs) {
+      float acc[kVec];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        if (k + u * subs >= k1) break;
-        float v8[kVec];
-        unpack16<F32>(w[u], v8);
+      for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
+      const int end = min(k1, run + kRun * subs);
+      for (int k = run; k < end; k += kAtOnce * subs) {
+        float cx[kAtOnce];
+        uint4 cw[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] = fmaf(x[u], v8[i], acc[i]);
+        for (int u = 0; u < kAtOnce; ++u) {
+          cx[u] = x[u];
+          cw[u] = w[u];
+        }
+        load(k + kAtOnce * subs);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          if (k + u * subs >= end) break;
+          float v8[kVec];
+          unpack16<F32>(cw[u], v8);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] = fmaf(cx[u], v8[i], acc[i]);
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) tb.scratch[sub * a.rank + v * kVec + i] = acc[i];
+      for (int i = 0; i < kVec; ++i) sums[i] += acc[i];
+    }
   }
   named_bar_sync(kBarSide, kSideThreads);
   for (int r = sid; r < a.rank; r += kSideThreads) {

@@ -2,8 +2,8 @@
 // on the CUDA cores: S = scale (X A), then 128 x 64 tiles of X W whose epilogue adds S B and the
 // addend. Bound by the FMA and shared-memory pipes for many tiles; few tiles cut K over the blocks
 // of a cluster, whose sums meet in distributed shared memory (128 rows, 4096 x 512: 52 us, without
-// the cut and the prefetch 241). Sums are kept in runs of 64 terms that are added up afterwards, so
-// the rounding error grows with the run length, not with K.
+// the cut and the prefetch 241). Sums are kept in runs of 64 terms that are added up afterwards:
+// the rounding error of K terms grows like that of 64 + K / 64 of them in one chain.
 #include <algorithm>
 #include <cstdint>
 
@@ -202,19 +202,23 @@ __global__ void __launch_bounds__(kThreads)
     if (ad >= 0 && ad < L) {
       const float* s = S + m * rank;
       const float* b = B + static_cast<int64_t>(ad) * rank * N + n;
-      float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r0 = 0; r0 < rank; r0 += kRun) {
+        float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int r1 = min(rank, r0 + kRun);
 #pragma unroll 4
-      for (int r = 0; r < rank; ++r) {
-        const float4 bv = __ldg(reinterpret_cast<const float4*>(b + static_cast<int64_t>(r) * N));
-        d.x = fmaf(s[r], bv.x, d.x);
-        d.y = fmaf(s[r], bv.y, d.y);
-        d.z = fmaf(s[r], bv.z, d.z);
-        d.w = fmaf(s[r], bv.w, d.w);
+        for (int r = r0; r < r1; ++r) {
+          const float4 bv =
+              __ldg(reinterpret_cast<const float4*>(b + static_cast<int64_t>(r) * N));
+          d.x = fmaf(s[r], bv.x, d.x);
+          d.y = fmaf(s[r], bv.y, d.y);
+          d.z = fmaf(s[r], bv.z, d.z);
+          d.w = fmaf(s[r], bv.w, d.w);
+        }
+        y.x += d.x;
+        y.y += d.y;
+        y.z += d.z;
+        y.w += d.w;
       }
-      y.x += d.x;
-      y.y += d.y;
-      y.z += d.z;
-      y.w += d.w;
     }
     if (addend != nullptr) {
       const float4 q = *reinterpret_cast<const float4*>(addend + m * N + n);
