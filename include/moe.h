@@ -141,7 +141,9 @@ moe_status moe_capacity(const moe_problem* p, int64_t* C);
  * bf16 operand (bf16 X with more than 16 experts: the three bf16 terms of W_r, written by each
  * router call) and, for moe_forward, the intermediate buffers (routing results, X_perm, H,
  * Y) or, in their place, moe_forward_few's partial sums and intermediate activations. It grows
- * with N: a workspace also serves the same problem with fewer tokens, for every entry point. */
+ * with N: a workspace also serves the same problem with fewer tokens, for every entry point.
+ * (moe_forward_few's part, about 20 MB and 4 bytes for each value of H, is what makes the size
+ * of a small layer. With more than 64 tokens no call uses it: a workspace without it is enough.) */
 moe_status moe_workspace_size(const moe_problem* p, size_t* bytes);
 
 /* Router + softmax + top-k + gates (Grok-1 book 5.2, 5.2.3; walkthrough 1.1, 1.2;

@@ -102,6 +102,8 @@ struct Layout {
   size_t xin, xout;   // moe_forward_host / moe_forward_host_many
   size_t xin2, xout2; // second buffers of moe_forward_host_many
   size_t total_host;
+  // What the size functions answer: the above, and what moe_forward_few takes for a smaller batch.
+  size_t size, size_host;
 };
 
 Layout make_layout(const moe_problem& p) {
@@ -129,16 +131,21 @@ Layout make_layout(const moe_problem& p) {
   L.xperm = take(es * R * static_cast<size_t>(p.D));
   L.h = take(es * R * static_cast<size_t>(p.F));
   L.y = take(es * R * static_cast<size_t>(p.D));
-  // moe_forward_few's scratch shares the intermediates' place. Larger batches count it too (for 64
-  // tokens), so that a workspace also serves every smaller batch.
+  // moe_forward_few's scratch shares the intermediates' place. Larger batches, which it does not
+  // take, have no use for it: their entry points do not ask for it, but the size functions count it
+  // (for 64 tokens), so that a workspace of that size also serves every smaller batch.
   L.few = L.idx;
-  o = std::max(o, align256(L.few + few_workspace_bytes(p)));
+  const size_t few_end = align256(L.few + few_workspace_bytes(p));
+  if (p.N <= kFewMaxTokens) o = std::max(o, few_end);
   L.total = o;
-  L.xin = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
-  L.xout = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
-  L.xin2 = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
-  L.xout2 = take(es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D));
+  const size_t xbytes = es * static_cast<size_t>(p.N) * static_cast<size_t>(p.D);
+  L.xin = take(xbytes);
+  L.xout = take(xbytes);
+  L.xin2 = take(xbytes);
+  L.xout2 = take(xbytes);
   L.total_host = o;
+  L.size = std::max(L.total, few_end);
+  L.size_host = L.size + (L.total_host - L.total);
   return L;
 }
 
@@ -471,14 +478,14 @@ moe_status moe_capacity(const moe_problem* p, int64_t* C) {
 moe_status moe_workspace_size(const moe_problem* p, size_t* bytes) {
   MOE_TRY(check_problem(p));
   if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = make_layout(*p).total;
+  *bytes = make_layout(*p).size;
   return MOE_OK;
 }
 
 moe_status moe_workspace_size_host(const moe_problem* p, size_t* bytes) {
   MOE_TRY(check_problem(p));
   if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = make_layout(*p).total_host;
+  *bytes = make_layout(*p).size_host;
   return MOE_OK;
 }
 
