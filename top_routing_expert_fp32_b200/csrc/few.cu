@@ -19,7 +19,7 @@
 // (64 columns for fp32 weights, 256 for 8-bit ones: 256 bytes either way.)
 // Rows of an expert are its kept tokens in capacity order, read from X by index: no
 // permutation is written. More than 32 rows of an expert (8-bit weights: 16) are several pieces,
-// each reading the expert's weights: the sums of so many rows are what the registers hold. A
+// each reading the expert's weights: the sums of so many rows are about what the registers hold. A
 // tile shared by several blocks is summed by the last to finish, in block order, so equal inputs
 // give equal bits.
 #include <algorithm>
@@ -240,7 +240,8 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
 
 // Top-k and gates, one warp per token (the rules of select.cuh's plain top-k: descending fp32
 // logits, the lower index first among equals, gates from exp(z - max)). The selection always
-// yields k distinct experts, whatever the logits hold.
+// yields k distinct experts, whatever the logits hold; a NaN, which that scan neither replaces nor
+// takes for another value, ranks by its bits here (a positive one first).
 template <int kWarps>
 __device__ void select_all(const FewArgs& a, Tables& tb, const float* z, int warp, int lane) {
   for (int t = warp; t < a.N; t += kWarps) {
@@ -769,8 +770,9 @@ __device__ __forceinline__ void store_out(const FewArgs& a, int t, int d, float2
 // ------------------------------------------------------------------ the kernel
 
 // MAXNT: row tiles of the largest possible piece (the tokens of a batch bound an expert's rows).
-// A kernel that holds only what its batch can need keeps its loops out of local memory: a spill
-// costs an L2 access here, since the ring leaves the L1 cache almost nothing.
+// A kernel that holds only what its batch can need keeps its loops out of local memory (8-bit, two
+// row tiles: 40 bytes of a thread spilled, 208 loaded back over the kernel's code): a spill costs
+// an L2 access here, since the ring leaves the L1 cache almost nothing.
 template <int WK, int MAXNT>
 __global__ void __launch_bounds__(Team<WK>::kThreads, 1)
 few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,

@@ -19,9 +19,11 @@
 //     more than a stage's 1424 cycles of HBM time from 13 rows on.
 // 16-bit weights [k][n] (n contiguous) become the row operand of mma.m16n8k16 through transposed
 // ldmatrix (16 output columns x 16 k per instruction), the activation rows its 8 columns: one
-// instruction per 512 bytes of weights and 8 rows, far from the tensor cores' limit, where the
-// tcgen05 tiles of 64 or 128 rows would mostly multiply padding. The rows come through plain
-// ldmatrix, 32 k of 8 rows per instruction, their pitch 16 bytes modulo the 128 of all banks.
+// instruction per 512 bytes of weights and 8 rows, far from the tensor cores' limit: the stream
+// bounds the 16-bit layer, so that tcgen05, with the weights' columns as its 128 rows, has nothing
+// to win there (not tried for 33 to 64 rows of adapters, which the stream does not bound). The rows
+// come through plain ldmatrix, 32 k of 8 rows per instruction, their pitch 16 bytes modulo the 128
+// of all banks.
 #pragma once
 
 #include "common.cuh"
@@ -51,9 +53,9 @@ constexpr int kBarConsumers = 1, kBarAll = 2, kBarRows = 3, kBarSide = 4;  // na
 // weights, four for 8-bit ones, whose conversion to bf16 is what their warps spend their time on
 // (Mixtral-shaped layer, 8 tokens: 300 us with 8 warps, 245 with 16).
 // kPieceRows: activation rows of one product (tiles of 8); an expert with more rows is streamed
-// again for the next piece. It is what the registers hold without spilling: a spill costs an L2
-// access here, since the ring leaves the L1 cache almost nothing (8-bit weights, 32 tokens:
-// 1300 us with pieces of 32 rows, 359 us of 16).
+// again for the next piece. It is what the registers hold, but for a few words: a spill costs an L2
+// access here, since the ring leaves the L1 cache almost nothing (8-bit weights, 32 tokens: 1300 us
+// with pieces of 32 rows, 359 us of 16, whose kernel still spills 40 bytes of a thread).
 template <int WK>
 struct Shape;
 template <>
