@@ -3,8 +3,8 @@
 1. A warp's arrival at a counter in global memory (lane 0 counts, all lanes then read what other
    warps wrote) has a warp barrier on both sides: a shuffle orders no memory. There is one function
    for it.
-2. Block barriers for part of a block (bar.sync and its kin) are for warps whose lanes are together;
-   each helper that issues one brings them together first."""
+2. Block barriers for part of a block (bar.sync and its kin) are for warps whose lanes are together:
+   a warp barrier stands before each."""
 import glob
 import os
 import re
@@ -42,15 +42,16 @@ def test_arrivals_of_a_warp_have_barriers_on_both_sides():
                for m in re.finditer(r"\bcount_global\(", src)]
     assert {name for name, _ in callers} == {"stream.cuh"} and len(callers) == 3
     block = _body(sources["stream.cuh"], "last_to_finish")
-    assert len(re.findall("named_bar_sync", block)) == 2 and "count_global" in block
+    assert len(re.findall("bar_sync", block)) == 2 and "count_global" in block
 
 
 def test_partial_block_barriers_are_reached_by_whole_warps():
     asm = re.compile(r'"[^"]*\bbar(?:rier)?\.(?:cta\.)?(?:sync|arrive|red)\b')
-    helpers = {"common.cuh": ["named_bar_sync", "named_bar_any"], "stream.cuh": ["named_bar_arrive"]}
+    call = re.compile(r"(\w[^\n]*\n[ ]*)?(?:if \()?\bnamed_bar_(?:sync|any)\((?!uint32_t)")
     for name, src in _sources().items():
-        names = helpers.get(name, [])
-        assert len(asm.findall(src)) == len(names), name
-        for helper in names:
-            body = _body(src, helper)
-            assert body.index("__syncwarp()") < asm.search(body).start(), (name, helper)
+        # The instructions themselves: in common.cuh's two helpers and stream.cuh's arrival.
+        assert len(asm.findall(src)) == {"common.cuh": 2, "stream.cuh": 1}.get(name, 0), name
+        for m in call.finditer(src):
+            assert (m.group(1) or "").split() == ["__syncwarp();"], (name, m.group(0))
+    body = _body(_sources()["stream.cuh"], "bar_arrive")
+    assert body.index("__syncwarp()") < asm.search(body).start()

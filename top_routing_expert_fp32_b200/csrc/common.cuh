@@ -503,18 +503,14 @@ __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
-// Barrier over `count` threads (whole warps) of this CTA, id 1..15 (0 is __syncthreads). The
-// instruction is for warps whose lanes are together, and lanes leave a wait or a loop one by one:
-// the warp barrier before it brings them back.
+// Barrier over `count` threads (whole warps) of this CTA, id 1..15 (0 is __syncthreads).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
-  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 // Barrier over `count` threads that also returns, to all of them, whether any passed true.
 __device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t count, bool pred) {
   uint32_t r;
-  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"

@@ -199,7 +199,7 @@ __device__ void partial_logits(const FewArgs& a, float* red, int tid) {
       if (q == i) v = acc[q];
     red[(i * subs + sl) * ep + e] = v;
   }
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
   for (int o = tid; o < nt * ep; o += kConsumers) {
     const int i = o / ep, ee = o & (ep - 1);
     if (ee < a.E) {
@@ -221,7 +221,7 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
     const int l = tid % n, part = tid / n;
     if (part < parts)
       red[part * n + l] = sum_partials<8>(a.part_logits + l, n, part, parts, a.slices);
-    named_bar_sync(kBarConsumers, kConsumers);
+    bar_sync(kBarConsumers, kConsumers);
     if (tid < n) {
       float s = a.bias != nullptr ? a.bias[tid % a.E] : 0.0f;
       float sum = 0.0f;
@@ -235,7 +235,7 @@ __device__ void sum_logits(const FewArgs& a, float* z, float* red, int tid) {
       z[l] = s + (a.bias != nullptr ? a.bias[l % a.E] : 0.0f);
     }
   }
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
 }
 
 // Top-k and gates, one warp per token (the rules of select.cuh's plain top-k: descending fp32
@@ -304,7 +304,7 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
     }
     if (lane == 0) tb.load[e] = base;
   }
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
   for (int r = tid; r < R; r += kConsumers) {
     const int t = r / a.k;
     tb.pos[r] = tb.pos_order[a.token_major ? r : (r - t * a.k) * a.N + t];
@@ -343,7 +343,7 @@ __device__ void assign_rows(const FewArgs& a, Tables& tb, int tid, int warp, int
       tb.n_parts = parts;
     }
   }
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
   for (int r = tid; r < R; r += kConsumers) {
     const int t = r / a.k;
     const int p = tb.pos[r];
@@ -658,7 +658,7 @@ __device__ __forceinline__ void up_tile(const FewArgs& a, Tables& tb, Consumer<W
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
     float* red = c.red.next();
     put_tile<WK, NT>(red, acc, j, c.warp, c.lane);
-    named_bar_sync(kBarConsumers, kConsumers);
+    bar_sync(kBarConsumers, kConsumers);
     for (int i = c.tid; i < P::kCount; i += kConsumers) {
       const float2 h1 = take_pair<WK>(red, 0, P::row(i), P::col(i));
       const float2 h2 = take_pair<WK>(red, 1, P::row(i), P::col(i));
@@ -725,7 +725,7 @@ __device__ __forceinline__ void down_run(const FewArgs& a, Tables& tb, Consumer<
   for (int j = 0; j < NT && 8 * j < pt.n; ++j) {
     float* red = c.red.next();
     put_tile<WK, NT>(red, acc, j, c.warp, c.lane);
-    named_bar_sync(kBarConsumers, kConsumers);
+    bar_sync(kBarConsumers, kConsumers);
     for (int i = c.tid; i < P::kCount; i += kConsumers) {
       const int r = 8 * j + P::row(i);
       if (r >= pt.n) continue;
@@ -812,10 +812,10 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
     ok = grid_barrier<kConsumers>(a.bar, G, tid, &tb.flag, a.timeout_ns, a.err);
     sum_logits<kConsumers>(a, outacc, red, tid);
     select_all<T::kWarps>(a, tb, outacc, warp, lane);
-    named_bar_sync(kBarConsumers, kConsumers);
+    bar_sync(kBarConsumers, kConsumers);
     assign_rows<kConsumers, S::kPieceRows>(a, tb, tid, warp, lane);
   }
-  named_bar_sync(kBarAll, T::kThreads);
+  bar_sync(kBarAll, T::kThreads);
 
   const int up_steps = (a.D + kBoxRows - 1) / kBoxRows;
   const int up_cols = (a.F + S::kCols - 1) / S::kCols;
@@ -939,7 +939,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
         return true;
       };
       auto h_ready = [&] {
-        named_bar_sync(kBarRows, kConsumers + 32);
+        bar_sync(kBarRows, kConsumers + 32);
         fence_proxy_async_all();
       };
       auto down_rows = [&](const Part& pt, int, int k) {
@@ -1002,7 +1002,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
     }
     fence_proxy_async_all();  // H is read by bulk copies
     if (!grid_barrier<kConsumers>(a.bar, 2 * G, tid, &tb.flag, a.timeout_ns, a.err)) c.ok = false;
-    named_bar_arrive(kBarRows, kConsumers + 32);
+    bar_arrive(kBarRows, kConsumers + 32);
 
     for (long long s = d0; s < d1;) {
       const long long tile = s / down_steps;
@@ -1010,7 +1010,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
       const int k1 = static_cast<int>(min(static_cast<long long>(down_steps), k0 + (d1 - s)));
       const int cb = static_cast<int>(tile);
       for (int i = tid; i < a.N * S::kCols; i += kConsumers) outacc[i] = 0.0f;
-      named_bar_sync(kBarConsumers, kConsumers);
+      bar_sync(kBarConsumers, kConsumers);
       for (int k = k0; k < k1;) {
         const int pi = k / run_steps;
         const int s0 = k - pi * run_steps;
@@ -1021,7 +1021,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
 #undef MOE_DOWN
         k += s1 - s0;
       }
-      named_bar_sync(kBarConsumers, kConsumers);  // the last sums are in
+      bar_sync(kBarConsumers, kConsumers);  // the last sums are in
       const bool whole = k0 == 0 && k1 == down_steps;
       float2* mine = reinterpret_cast<float2*>(
           a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * a.part_floats);
@@ -1050,7 +1050,7 @@ few_kernel(const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUten
           }
         }
       }
-      named_bar_sync(kBarConsumers, kConsumers);
+      bar_sync(kBarConsumers, kConsumers);
       s += k1 - k0;
     }
   }

@@ -194,7 +194,7 @@ __device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid, int item) {
       for (int i = 0; i < kVec; ++i) sums[i] += acc[i];
     }
   }
-  named_bar_sync(kBarSide, kSideThreads);
+  bar_sync(kBarSide, kSideThreads);
   for (int r = sid; r < a.rank; r += kSideThreads) {
     float s = 0.0f;
 #pragma unroll 4
@@ -234,7 +234,7 @@ __device__ void gather_s(const LoraArgs& a, LoraTables& tb, uint8_t* S, int sid)
     const int i = sid % n, part = sid / n;
     if (part < per)
       tb.scratch[part * n + i] = sum_partials<8>(a.part_s + i, n, part, per, a.slices);
-    named_bar_sync(kBarSide, kSideThreads);
+    bar_sync(kBarSide, kSideThreads);
     if (sid < n) {
       float s = 0.0f;
       for (int q = 0; q < per; ++q) s += tb.scratch[q * n + sid];
@@ -404,7 +404,7 @@ __device__ __forceinline__ void finish_f32(const LoraArgs& a, const RowsF32<NT>&
   } else {
 #pragma unroll
     for (int q = 0; q < 16; ++q) red[(warp * 16 + q) * 32 + lane] = acc.v[q >> 3][q & 7];
-    named_bar_sync(kBarConsumers, kConsumers);
+    bar_sync(kBarConsumers, kConsumers);
 #pragma unroll
     for (int q = 0; q < R::kMine; ++q) {
       v[q] = 0.0f;
@@ -583,17 +583,17 @@ __device__ __forceinline__ bool strip_meet(Strip<NT>& acc, const Place<NT>& at, 
   if constexpr (H == 2) {
     float4* x = reinterpret_cast<float4*>(strip) + lane;
     if (at.half == 1) {
-      named_bar_sync(kBarPair + Place<NT>::kOwners + at.owner, 64);
+      bar_sync(kBarPair + Place<NT>::kOwners + at.owner, 64);
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
           x[(h * NT + j) * 32] = make_float4(acc.v[h][j][0], acc.v[h][j][1], acc.v[h][j][2],
                                              acc.v[h][j][3]);
-      named_bar_arrive(kBarPair + at.owner, 64);
+      bar_arrive(kBarPair + at.owner, 64);
       return false;
     }
-    named_bar_sync(kBarPair + at.owner, 64);
+    bar_sync(kBarPair + at.owner, 64);
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -611,7 +611,7 @@ __device__ __forceinline__ bool strip_meet(Strip<NT>& acc, const Place<NT>& at, 
 template <int NT>
 __device__ __forceinline__ void strip_free(const Place<NT>& at) {
   if (halves_of(NT) == 2 && at.half == 0)
-    named_bar_arrive(kBarPair + Place<NT>::kOwners + at.owner, 64);
+    bar_arrive(kBarPair + Place<NT>::kOwners + at.owner, 64);
 }
 
 // Y of the warp's columns (from n0 on): sums plus addend, through the warp's shared memory, so that
@@ -901,14 +901,14 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       const int sid = tid - (kConsumers + 64);
       for (int item = me; item < a.M * a.slices; item += G) {  // one, where there are SMs enough
         shrink<kIsF32>(a, tb, sid, item);
-        named_bar_sync(kBarSide, kSideThreads);
+        bar_sync(kBarSide, kSideThreads);
       }
       if (sid == 0) {
         arrive_global(&a.bar[1]);
         (void)spin_until(&a.bar[1], G, a.timeout_ns, a.err);
       }
       __syncwarp();
-      named_bar_sync(kBarSide, kSideThreads);
+      bar_sync(kBarSide, kSideThreads);
       gather_s<kIsF32>(a, tb, S_mem, sid);
       mbar_arrive(&tb.s_ready);
     }
@@ -982,7 +982,7 @@ lora_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ 
       });
       // (The last arrival there: no barrier is left half way.)
       if (halves_of(NT) == 2 && place.half == 1)
-        named_bar_sync(kBarPair + Place<NT>::kOwners + place.owner, 64);
+        bar_sync(kBarPair + Place<NT>::kOwners + place.owner, 64);
     } else {
       const int tile = warp % NT, part = warp / NT;
       int turn = 0;  // of two buffers: a write there is past the barrier after the last read

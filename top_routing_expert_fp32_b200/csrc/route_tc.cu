@@ -378,7 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // overwritten.
       if (S > 1 && ok && it > 0)
         ok = mbar_wait_cluster(zfree, static_cast<uint32_t>(it - 1) & 1u, a.timeout_ns);
-      // Leave together: the four epilogue warps share named barriers below.
+      // Leave together: the four epilogue warps share named barriers below. (Here and there a warp's
+      // lanes, which leave a wait or a loop one by one, come together first.)
+      __syncwarp();
       if (named_bar_any(1, kEpiThreads, !ok)) {
         if (et == 0) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
         break;
@@ -422,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c < a.Ep) st_dsmem_f4(dst + c * 4u, make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]));
         mbar_arrive_cluster(mapa_shared(smem_u32(zready), static_cast<uint32_t>(q)));
         ok = mbar_wait_cluster(zready, static_cast<uint32_t>(it) & 1u, a.timeout_ns);
+        __syncwarp();
         if (named_bar_any(1, kEpiThreads, !ok)) {
           if (et == 0) record_error(a.err, MOE_DEVERR_WAIT_TIMEOUT);
           break;
@@ -480,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         zt[E] = lse * lse;
       }
       if (a.colsum_partial != nullptr || a.zl_partial != nullptr) {  // sums in token order
+        __syncwarp();
         named_bar_sync(1, kEpiThreads);
         const int64_t left = a.N - (tile * kRows + share0);
         const int valid = left < T ? static_cast<int>(left > 0 ? left : 0) : T;
@@ -487,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < valid; ++i) colsum_acc += s_z[i * (E + 1) + et];
         if (a.zl_partial != nullptr && et == 0)
           for (int i = 0; i < valid; ++i) zl_acc += s_z[i * (E + 1) + E];
+        __syncwarp();
         named_bar_sync(1, kEpiThreads);
       }
     }

@@ -125,6 +125,17 @@ struct SplitK {
   }
 };
 
+// Barriers of whole warps of the block. The instruction is for warps whose lanes are together, and
+// lanes leave a wait or a loop one by one: the warp barrier before it brings them back.
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
+  __syncwarp();
+  named_bar_sync(id, count);
+}
+__device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t count) {
+  __syncwarp();
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -390,7 +401,7 @@ struct RedTurn {
     return base + turn * (8 * 8 * kRedPitch);
   }
   __device__ void done() {
-    if (Team<WK>::kWarps != 8) named_bar_sync(kBarConsumers, Team<WK>::kConsumers);
+    if (Team<WK>::kWarps != 8) bar_sync(kBarConsumers, Team<WK>::kConsumers);
   }
 };
 
@@ -499,13 +510,13 @@ __device__ __forceinline__ bool spin_until(int* bar, int target, uint64_t timeou
 template <int kConsumers>
 __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int* flag,
                                              uint64_t timeout_ns, int* err) {
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
   if (tid == 0) {
     arrive_global(bar);
     *flag = spin_until(bar, target, timeout_ns, err) ? 1 : 0;
   }
   __syncwarp();
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
   return *flag != 0;
 }
 
@@ -513,10 +524,10 @@ __device__ __forceinline__ bool grid_barrier(int* bar, int target, int tid, int*
 // then see what the others wrote before arriving).
 template <int kConsumers>
 __device__ __forceinline__ bool last_to_finish(int* counter, int parts, int tid, int* flag) {
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
   if (tid == 0) *flag = count_global(counter) == parts - 1;
   __syncwarp();
-  named_bar_sync(kBarConsumers, kConsumers);
+  bar_sync(kBarConsumers, kConsumers);
   const bool last = *flag != 0;
   return last;
 }
@@ -617,11 +628,6 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // Generic-proxy writes of global memory before bulk copies of it, and the other way round.
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
-}
-
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
-  __syncwarp();
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 }  // namespace stream
