@@ -148,7 +148,7 @@ __device__ void shrink(const LoraArgs& a, LoraTables& tb, int sid, int item) {
     // Four k at a time, all their loads on their way before the first product of the four before:
     // beside the stream a load takes about 2 us (a row of 4096: the partial sums were out after 9.8
     // us one by one, 4.6 us by fours). Each row reads its own adapter, also where rows share one:
-    // 64 rows of 4096 x 4096, 64 adapters of rank 128, take 132 us, most of it here.
+    // 64 rows of 4096 x 4096, 64 adapters of rank 128, take 136 us, most of it here.
     constexpr int kAtOnce = 4;
     static_assert(kRun % kAtOnce == 0, "whole runs");
     float x[kAtOnce];
